@@ -10,6 +10,7 @@ from __future__ import annotations
 __all__ = [
     "cq_pack_info", "cq_analytic_levels", "act_fwht_quant_a8", "cq_gemv", "cq_gemv_f32", "cq_gemm",
     "q4_0_gemv", "cq_pack", "q4_0_pack", "cq_codebook_fit", "CqLayout", "BqmError",
+    "fp8_quant", "fp8_pack", "fp8_gemm", "fp8_gemm_grouped", "moe_route", "moe_combine", "MoeRoute",
 ]
 
 

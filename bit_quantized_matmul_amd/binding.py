@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import numpy as np
 
@@ -24,6 +25,7 @@ EXPORTED = (
     "cq_gemm", "q4_0_gemv", "q4_0_gemm", "cq_pack", "q4_0_pack", "cq_codebook_fit", "bqm_strerror",
     "kmcu_header", "kmcu_tensor", "kmcu_find", "kmcu_upload", "kmcu_upload_data", "cq_gemv_f32_noalloc",
     "q4_0_gemv_a8", "q4_0_gemm_a8", "cq_gemv_lut", "q4_0_gemv_a8_f32",
+    "fp8_quant", "fp8_pack", "fp8_gemm", "fp8_gemm_grouped", "moe_route_workspace", "moe_route", "moe_combine",
 )
 KMCU_F32, KMCU_Q4 = 1, 2
 
@@ -108,6 +110,13 @@ def load_library() -> ctypes.CDLL:
         "kmcu_find": ([P, ctypes.c_uint64, ctypes.c_char_p, ctypes.POINTER(KmcuTensor)], I),
         "kmcu_upload": ([P, ctypes.c_uint64, ctypes.POINTER(KmcuTensor), P, P], I),
         "kmcu_upload_data": ([P, ctypes.c_uint64, P, ctypes.c_uint64, P], I),
+        "fp8_quant": ([P, I, I, I, I64, I, P, P, P], I),
+        "fp8_pack": ([P, I, I, I, I, P, P, P], I),
+        "fp8_gemm": ([P, P, I, I, P, P, I, P, I, P], I),
+        "fp8_gemm_grouped": ([P, P, I, I, I, P, P, I, P, P, I, P, I, P], I),
+        "moe_route_workspace": ([I, I, I, ctypes.POINTER(I64)], I),
+        "moe_route": ([P, I, I, I, I64, I, I, P, P, P, P, P, P, I64, P], I),
+        "moe_combine": ([P, I, I64, I, P, P, I, I, P, P], I),
     }
     for name, (args, ret) in sig.items():
         fn = getattr(lib, name)
@@ -510,3 +519,207 @@ def cq_codebook_fit(samples, levels: int, iters: int = 200, table=None, raw=None
         _dev(samples, torch.float64, "samples"), samples.numel(), levels, iters,
         _dev(raw, torch.float64, "raw"), _dev(table, torch.float32, "table"), _stream()))
     return table, raw
+
+
+# ------------------------------------------ 8-bit float products, mixture of experts
+
+FP8_BLOCK = 128
+
+
+def fp8_blocks(cols: int) -> int:
+    """Blocks of 128 a row of `cols` columns takes (the last one padded)."""
+    return (cols + FP8_BLOCK - 1) // FP8_BLOCK
+
+
+def _dtype_code(dtype, name):
+    torch = _torch()
+    code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {dtype}")
+    return code
+
+
+def _row_strided(t, name):
+    """A 2-D tensor whose rows are contiguous: (pointer, dtype code, row stride)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.ndim != 2:
+        raise ValueError(f"{name} must be a 2-D tensor, got {tuple(getattr(t, 'shape', ()))}")
+    code = _dtype_code(t.dtype, name)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA/HIP tensor")
+    if t.shape[0] < 1 or t.shape[1] < 1:
+        raise ValueError(f"{name} must not be empty, got {tuple(t.shape)}")
+    rows, cols = t.stride()
+    if cols != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name}'s rows must be contiguous (stride {t.stride()})")
+    if t.shape[0] > 1 and rows < t.shape[1]:
+        raise ValueError(f"{name}'s rows must not overlap (stride {t.stride()})")
+    return ctypes.c_void_p(t.data_ptr()), code, rows
+
+
+def fp8_quant(x, swiglu: bool = False, q=None, scale=None):
+    """x [m, k] (float32, bfloat16 or float16, rows may be strided) -> (q float8_e4m3fn
+    [m, 128 kb], scale fp32 [kb, m]), one scale a token and 128 columns, kb =
+    ceil(k / 128).  With swiglu, x is [m, 2 k] = [gate | up] and silu(gate) * up
+    is quantized."""
+    torch = _torch()
+    xp, code, stride = _row_strided(x, "x")
+    m, k = x.shape
+    if swiglu:
+        if k % 2:
+            raise ValueError(f"x must hold gate and up columns, got {k}")
+        k //= 2
+    kb = fp8_blocks(k)
+    if q is None:
+        q = torch.empty((m, kb * FP8_BLOCK), dtype=torch.float8_e4m3fn, device=x.device)
+    if scale is None:
+        scale = torch.empty((kb, m), dtype=torch.float32, device=x.device)
+    _shape(q, (m, kb * FP8_BLOCK), "q")
+    _shape(scale, (kb, m), "scale")
+    _check("fp8_quant", load_library().fp8_quant(
+        xp, code, m, k, stride, int(swiglu), _dev(q, torch.float8_e4m3fn, "q"),
+        _dev(scale, torch.float32, "scale"), _stream()))
+    return q, scale
+
+
+def fp8_pack(w, q=None, scale=None):
+    """Weights [rows, cols] or [experts, rows, cols] (float32, bfloat16 or float16) ->
+    (q float8_e4m3fn [..., rows, 128 kb], scale fp32 [..., ceil(rows / 128), kb]),
+    one scale a 128 x 128 block."""
+    torch = _torch()
+    if getattr(w, "ndim", 0) not in (2, 3) or w.numel() < 1:
+        raise ValueError(f"w must be [rows, cols] or [experts, rows, cols], got {tuple(getattr(w, 'shape', ()))}")
+    code = _dtype_code(w.dtype, "w")
+    lead, (rows, cols) = tuple(w.shape[:-2]), w.shape[-2:]
+    kb = fp8_blocks(cols)
+    if q is None:
+        q = torch.empty((*lead, rows, kb * FP8_BLOCK), dtype=torch.float8_e4m3fn, device=w.device)
+    if scale is None:
+        scale = torch.empty((*lead, fp8_blocks(rows), kb), dtype=torch.float32, device=w.device)
+    _shape(q, (*lead, rows, kb * FP8_BLOCK), "q")
+    _shape(scale, (*lead, fp8_blocks(rows), kb), "scale")
+    _check("fp8_pack", load_library().fp8_pack(
+        _dev(w, w.dtype, "w"), code, lead[0] if lead else 1, rows, cols,
+        _dev(q, torch.float8_e4m3fn, "q"), _dev(scale, torch.float32, "scale"), _stream()))
+    return q, scale
+
+
+def _fp8_operands(w, w_scale, cols, q, q_scale, lead):
+    """Check a product's operands; returns (rows, m)."""
+    if cols < 1:
+        raise ValueError(f"cols must be at least 1, got {cols}")
+    kb = fp8_blocks(cols)
+    if getattr(w, "ndim", 0) != lead + 2 or w.shape[-1] != kb * FP8_BLOCK or min(w.shape) < 1:
+        raise ValueError(f"w must have shape [{'experts, ' * lead}rows, {kb * FP8_BLOCK}], "
+                         f"got {tuple(getattr(w, 'shape', ()))}")
+    rows = int(w.shape[-2])
+    _shape(w_scale, (*w.shape[:-2], fp8_blocks(rows), kb), "w_scale")
+    m = _rows2d(q, kb * FP8_BLOCK, "q")
+    _shape(q_scale, (kb, m), "q_scale")
+    return rows, m
+
+
+def fp8_gemm(w, w_scale, cols: int, q, q_scale, dtype=None, y=None):
+    """fp8_pack weights [rows, cols] x fp8_quant activations [m, cols] -> y [m, rows] of
+    `dtype` (float32, bfloat16, the default, or float16)."""
+    torch = _torch()
+    rows, m = _fp8_operands(w, w_scale, cols, q, q_scale, 0)
+    if y is None:
+        y = torch.empty((m, rows), dtype=dtype or torch.bfloat16, device=q.device)
+    elif dtype is not None and y.dtype != dtype:
+        raise ValueError(f"y must be {dtype}, got {y.dtype}")
+    _shape(y, (m, rows), "y")
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    _check("fp8_gemm", load_library().fp8_gemm(
+        _dev(w, f8, "w"), _dev(w_scale, f32, "w_scale"), rows, cols, _dev(q, f8, "q"),
+        _dev(q_scale, f32, "q_scale"), m, _dev(y, y.dtype, "y"), _dtype_code(y.dtype, "y"), _stream()))
+    return y
+
+
+def fp8_gemm_grouped(w, w_scale, cols: int, q, q_scale, offsets, row_ids=None, dtype=None, y=None):
+    """fp8_pack weights [experts, rows, cols] x fp8_quant activations [m, cols] -> y [slots,
+    rows]: rows offsets[e] .. offsets[e + 1] - 1 of y are expert e's product with
+    activation rows row_ids[p] (rows p without row_ids, and then slots = m).  Rows of
+    y outside every expert's range are not written."""
+    torch = _torch()
+    rows, m = _fp8_operands(w, w_scale, cols, q, q_scale, 1)
+    experts = int(w.shape[0])
+    _shape(offsets, (experts + 1,), "offsets")
+    slots = m
+    if row_ids is not None:
+        if getattr(row_ids, "ndim", 0) != 1 or row_ids.shape[0] < 1:
+            raise ValueError(f"row_ids must have shape [slots], got {tuple(getattr(row_ids, 'shape', ()))}")
+        slots = int(row_ids.shape[0])
+    if y is None:
+        y = torch.empty((slots, rows), dtype=dtype or torch.bfloat16, device=q.device)
+    elif dtype is not None and y.dtype != dtype:
+        raise ValueError(f"y must be {dtype}, got {y.dtype}")
+    _shape(y, (slots, rows), "y")
+    f8, f32, i32 = torch.float8_e4m3fn, torch.float32, torch.int32
+    _check("fp8_gemm_grouped", load_library().fp8_gemm_grouped(
+        _dev(w, f8, "w"), _dev(w_scale, f32, "w_scale"), experts, rows, cols, _dev(q, f8, "q"),
+        _dev(q_scale, f32, "q_scale"), m, _dev(offsets, i32, "offsets"),
+        None if row_ids is None else _dev(row_ids, i32, "row_ids"), slots, _dev(y, y.dtype, "y"),
+        _dtype_code(y.dtype, "y"), _stream()))
+    return y
+
+
+class MoeRoute(NamedTuple):
+    ids: object        # int32 [tokens, top]: the chosen experts, -1 for none
+    weights: object    # fp32 [tokens, top]
+    offsets: object    # int32 [experts + 1]: each expert's range of sorted pairs
+    row_ids: object    # int32 [tokens * top]: the token of each sorted pair, -1 past the last
+    slots: object      # int32 [tokens, top]: where each pair went, -1 for none
+
+
+def moe_route_workspace(tokens: int, experts: int, top: int) -> int:
+    """Bytes of device workspace moe_route needs."""
+    n = ctypes.c_int64()
+    _check("moe_route_workspace", load_library().moe_route_workspace(tokens, experts, top, ctypes.byref(n)))
+    return n.value
+
+
+def moe_route(logits, top: int, renorm: bool = True, workspace=None) -> MoeRoute:
+    """logits [tokens, experts] -> MoeRoute: the `top` largest logits of each token, their
+    softmax weights (over the chosen with renorm, else over all) and the pairs sorted
+    by expert."""
+    torch = _torch()
+    lp, code, stride = _row_strided(logits, "logits")
+    tokens, experts = logits.shape
+    need = moe_route_workspace(tokens, experts, top)
+    dev, i32 = logits.device, torch.int32
+    if workspace is None and need:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        _at_least(workspace, need, "workspace")
+    pairs = tokens * top
+    r = MoeRoute(torch.empty((tokens, top), dtype=i32, device=dev),
+                 torch.empty((tokens, top), dtype=torch.float32, device=dev),
+                 torch.empty((experts + 1,), dtype=i32, device=dev),
+                 torch.empty((pairs,), dtype=i32, device=dev),
+                 torch.empty((tokens, top), dtype=i32, device=dev))
+    _check("moe_route", load_library().moe_route(
+        lp, code, tokens, experts, stride, top, int(renorm), r.ids.data_ptr(), r.weights.data_ptr(),
+        r.offsets.data_ptr(), r.row_ids.data_ptr(), r.slots.data_ptr(),
+        None if workspace is None else _dev(workspace, torch.uint8, "workspace"), need, _stream()))
+    return r
+
+
+def moe_combine(y, slots, weights, out=None):
+    """out[t] = sum_j weights[t, j] * y[slots[t, j]] (slots below 0 are left out): y [rows, d],
+    slots int32 and weights fp32 [tokens, top] -> out [tokens, d] of y's type."""
+    torch = _torch()
+    if getattr(y, "ndim", 0) != 2 or y.numel() < 1:
+        raise ValueError(f"y must have shape [rows, d], got {tuple(getattr(y, 'shape', ()))}")
+    if getattr(slots, "ndim", 0) != 2 or slots.numel() < 1:
+        raise ValueError(f"slots must have shape [tokens, top], got {tuple(getattr(slots, 'shape', ()))}")
+    code = _dtype_code(y.dtype, "y")
+    tokens, top = slots.shape
+    _shape(weights, (tokens, top), "weights")
+    if out is None:
+        out = torch.empty((tokens, y.shape[1]), dtype=y.dtype, device=y.device)
+    _shape(out, (tokens, y.shape[1]), "out")
+    _check("moe_combine", load_library().moe_combine(
+        _dev(y, y.dtype, "y"), code, y.shape[0], y.shape[1], _dev(slots, torch.int32, "slots"),
+        _dev(weights, torch.float32, "weights"), tokens, top, _dev(out, y.dtype, "out"), _stream()))
+    return out

@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "bqm_common.h"
+#include "lowp_types.h"
 
 namespace bqm {
 
@@ -157,6 +158,12 @@ int check_layout(const bqm_cq_layout *L) {
 }
 
 int status_of(hipError_t e) { return e == hipSuccess ? BQM_OK : BQM_EDEVICE; }
+
+// E4M3 products: block counts and tile rows stay within a launch's second
+// grid dimension, and an expert's rows within 31 bits.
+constexpr int kMaxFp8Cols = 1 << 22, kMaxFp8Rows = 1 << 24, kMaxFp8Experts = 4096;
+constexpr int64_t kMaxPairs = (int64_t)1 << 30;
+constexpr int kMaxCombineCols = 1 << 26;
 
 constexpr int kGemvTokensForGemm = 32;   // cq_gemm: up to this many tokens run the batched GEMV kernel
 
@@ -501,6 +508,97 @@ int cq_codebook_fit(const double *samples, int64_t n, int levels, int iters, dou
   const int rc = current_device(&cus);
   if (rc) return rc;
   return status_of(launch_codebook_fit(samples, n, levels, iters, raw, table, (hipStream_t)stream));
+}
+
+int fp8_quant(const void *x, int dtype, int m, int k, int64_t x_stride, int swiglu, uint8_t *q, float *scale,
+              bqm_stream_t stream) {
+  if (!x || !q || !scale || m < 1 || k < 1 || !known_dtype(dtype)) return BQM_EINVAL;
+  if (m > 1 && x_stride < (int64_t)k * (swiglu ? 2 : 1)) return BQM_EINVAL;
+  if (k > kMaxFp8Cols) return BQM_ENOTSUP;
+  if (!aligned16(q) || ((uintptr_t)scale & 3u) || ((uintptr_t)x & (unsigned)(elem_size(dtype) - 1))) return BQM_EALIGN;
+  int cus;
+  const int rc = current_device(&cus);
+  if (rc) return rc;
+  return status_of(launch_fp8_quant(x, dtype, m, k, x_stride, swiglu != 0, q, scale, (hipStream_t)stream));
+}
+
+int fp8_pack(const void *w, int dtype, int experts, int rows, int cols, uint8_t *q, float *scale,
+             bqm_stream_t stream) {
+  if (!w || !q || !scale || experts < 1 || rows < 1 || cols < 1 || !known_dtype(dtype)) return BQM_EINVAL;
+  if (experts > kMaxFp8Experts || cols > kMaxFp8Cols || rows > kMaxFp8Rows) return BQM_ENOTSUP;
+  if (!aligned16(q) || ((uintptr_t)scale & 3u) || ((uintptr_t)w & (unsigned)(elem_size(dtype) - 1))) return BQM_EALIGN;
+  int cus;
+  const int rc = current_device(&cus);
+  if (rc) return rc;
+  return status_of(launch_fp8_pack(w, dtype, experts, rows, cols, q, scale, (hipStream_t)stream));
+}
+
+int fp8_gemm(const uint8_t *w, const float *w_scale, int rows, int cols, const uint8_t *q, const float *q_scale,
+             int m, void *y, int ydtype, bqm_stream_t stream) {
+  if (!w || !w_scale || !q || !q_scale || !y || rows < 1 || cols < 1 || m < 1 || !known_dtype(ydtype))
+    return BQM_EINVAL;
+  if (cols > kMaxFp8Cols || rows > kMaxFp8Rows) return BQM_ENOTSUP;
+  if (!aligned16(w) || !aligned16(q) || ((uintptr_t)w_scale & 3u) || ((uintptr_t)q_scale & 3u) ||
+      ((uintptr_t)y & (unsigned)(elem_size(ydtype) - 1)))
+    return BQM_EALIGN;
+  int cus;
+  const int rc = current_device(&cus);
+  if (rc) return rc;
+  return status_of(launch_fp8_gemm(w, w_scale, rows, cols, q, q_scale, m, y, ydtype, cus, (hipStream_t)stream));
+}
+
+int fp8_gemm_grouped(const uint8_t *w, const float *w_scale, int experts, int rows, int cols, const uint8_t *q,
+                     const float *q_scale, int m, const int32_t *offsets, const int32_t *row_ids, int slots, void *y,
+                     int ydtype, bqm_stream_t stream) {
+  if (!w || !w_scale || !q || !q_scale || !offsets || !y || experts < 1 || rows < 1 || cols < 1 || m < 1 ||
+      slots < 1 || !known_dtype(ydtype) || (!row_ids && slots > m))
+    return BQM_EINVAL;
+  if (experts > kMaxFp8Experts || cols > kMaxFp8Cols || rows > kMaxFp8Rows) return BQM_ENOTSUP;
+  if (!aligned16(w) || !aligned16(q) || ((uintptr_t)w_scale & 3u) || ((uintptr_t)q_scale & 3u) ||
+      ((uintptr_t)offsets & 3u) || ((uintptr_t)row_ids & 3u) || ((uintptr_t)y & (unsigned)(elem_size(ydtype) - 1)))
+    return BQM_EALIGN;
+  int cus;
+  const int rc = current_device(&cus);
+  if (rc) return rc;
+  return status_of(launch_fp8_gemm_grouped(w, w_scale, experts, rows, cols, q, q_scale, m, offsets, row_ids, slots, y,
+                                           ydtype, cus, (hipStream_t)stream));
+}
+
+int moe_route_workspace(int tokens, int experts, int top, int64_t *bytes) {
+  if (!bytes || tokens < 1 || experts < 1 || top < 1 || top > experts) return BQM_EINVAL;
+  if (!moe_route_supported(experts, top) || (int64_t)tokens * top > kMaxPairs) return BQM_ENOTSUP;
+  *bytes = moe_route_scratch(tokens, experts);
+  return BQM_OK;
+}
+
+int moe_route(const void *logits, int dtype, int tokens, int experts, int64_t stride, int top, int renorm,
+              int32_t *ids, float *weights, int32_t *offsets, int32_t *row_ids, int32_t *slots, void *workspace,
+              int64_t workspace_bytes, bqm_stream_t stream) {
+  if (!logits || !ids || !weights || !offsets || !row_ids || !slots || !known_dtype(dtype)) return BQM_EINVAL;
+  int64_t need = 0;
+  const int rw = moe_route_workspace(tokens, experts, top, &need);
+  if (rw) return rw;
+  if ((tokens > 1 && stride < experts) || workspace_bytes < need || (need && !workspace)) return BQM_EINVAL;
+  const uintptr_t all4 = (uintptr_t)ids | (uintptr_t)weights | (uintptr_t)offsets | (uintptr_t)row_ids |
+                         (uintptr_t)slots | (uintptr_t)workspace;
+  if ((all4 & 3u) || ((uintptr_t)logits & (unsigned)(elem_size(dtype) - 1))) return BQM_EALIGN;
+  int cus;
+  const int rc = current_device(&cus);
+  if (rc) return rc;
+  return status_of(launch_moe_route(logits, dtype, tokens, experts, stride, top, renorm != 0, ids, weights, offsets,
+                                    row_ids, slots, workspace, (hipStream_t)stream));
+}
+
+int moe_combine(const void *y, int dtype, int64_t y_rows, int d, const int32_t *slots, const float *weights,
+                int tokens, int top, void *out, bqm_stream_t stream) {
+  if (!y || !slots || !weights || !out || y_rows < 1 || d < 1 || tokens < 1 || top < 1 || !known_dtype(dtype))
+    return BQM_EINVAL;
+  if (d > kMaxCombineCols) return BQM_ENOTSUP;
+  if (!aligned16(y) || !aligned16(out) || ((uintptr_t)slots & 3u) || ((uintptr_t)weights & 3u)) return BQM_EALIGN;
+  int cus;
+  const int rc = current_device(&cus);
+  if (rc) return rc;
+  return status_of(launch_moe_combine(y, dtype, y_rows, d, slots, weights, tokens, top, out, (hipStream_t)stream));
 }
 
 const char *bqm_strerror(int code) {

@@ -155,6 +155,23 @@ hipError_t launch_q4_0_gemm(const uint8_t *blocks, int rows, int cols, const flo
 hipError_t launch_cq_pack(const float *w, const bqm_cq_layout &L, const LevelTable &T,
                           uint8_t *blob, int32_t *status, hipStream_t s);
 hipError_t launch_q4_0_pack(const float *w, int rows, int cols, uint8_t *blocks, hipStream_t s);
+hipError_t launch_fp8_quant(const void *x, int dtype, int m, int k, int64_t stride, bool swiglu, uint8_t *q,
+                            float *scale, hipStream_t s);
+hipError_t launch_fp8_pack(const void *w, int dtype, int experts, int rows, int cols, uint8_t *q, float *scale,
+                           hipStream_t s);
+hipError_t launch_fp8_gemm(const uint8_t *w, const float *ws, int rows, int cols, const uint8_t *q, const float *qs,
+                           int m, void *y, int ydtype, int num_cus, hipStream_t s);
+hipError_t launch_fp8_gemm_grouped(const uint8_t *w, const float *ws, int experts, int rows, int cols,
+                                   const uint8_t *q, const float *qs, int m, const int32_t *offsets,
+                                   const int32_t *row_ids, int slots, void *y, int ydtype, int num_cus,
+                                   hipStream_t s);
+bool moe_route_supported(int experts, int top);
+int64_t moe_route_scratch(int tokens, int experts);
+hipError_t launch_moe_route(const void *logits, int dtype, int tokens, int experts, int64_t stride, int top,
+                            bool renorm, int32_t *ids, float *weights, int32_t *offsets, int32_t *row_ids,
+                            int32_t *slots, void *scratch, hipStream_t s);
+hipError_t launch_moe_combine(const void *y, int dtype, int64_t rows, int d, const int32_t *slots,
+                              const float *weights, int tokens, int top, void *out, hipStream_t s);
 hipError_t launch_codebook_fit(const double *samples, int64_t n, int levels, int iters,
                                double *raw, float *table, hipStream_t s);
 

@@ -1,0 +1,49 @@
+// Element types of the 8-bit float and mixture-of-experts operators: the
+// 16- and 32-bit types of their inputs and results, and E4M3 codes.
+#pragma once
+
+#include "bqm_common.h"
+
+namespace bqm {
+
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+inline int elem_size(int dtype) { return dtype == BQM_F32 ? 4 : 2; }
+inline bool known_dtype(int dtype) { return dtype == BQM_F32 || dtype == BQM_BF16 || dtype == BQM_F16; }
+
+// fp32 value of an element, and the element nearest to an fp32 value (half to even)
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__bf16 v) { return (float)v; }
+__device__ __forceinline__ float to_f32(_Float16 v) { return (float)v; }
+template <typename T> __device__ __forceinline__ T from_f32(float v) { return (T)v; }
+
+// N consecutive elements as fp32, with 16-byte loads: p is aligned to 16 bytes.
+template <int N>
+__device__ __forceinline__ void load_vec(const float *p, float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const f32x4_t a = *reinterpret_cast<const f32x4_t *>(p + i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[i + j] = a[j];
+  }
+}
+template <int N, typename T>
+__device__ __forceinline__ void load_vec(const T *p, float (&v)[N]) {
+  typedef T tx8 __attribute__((ext_vector_type(8)));
+#pragma unroll
+  for (int i = 0; i < N; i += 8) {
+    const tx8 a = *reinterpret_cast<const tx8 *>(p + i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i + j] = to_f32(a[j]);
+  }
+}
+
+// Two E4M3 codes of a and b (half to even) in the low 16 bits; |a|, |b| <= 448
+// or NaN (whose code is 0x7F or 0xFF).
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false) & 0xFFFFu;
+}
+
+}  // namespace bqm

@@ -375,6 +375,90 @@ int kmcu_upload(const void *file, uint64_t size, const bqm_kmcu_tensor *tensor, 
 int kmcu_upload_data(const void *file, uint64_t size, void *dst, uint64_t dst_bytes,
                      bqm_stream_t stream);
 
+/* ---- 8-bit floating point products with a scale for each block of 128 ----
+ * Codes are OCP E4M3 (finite, largest value 448).  kb = ceil(cols / 128) blocks
+ * a row; rows of codes are 128 kb bytes, the columns past `cols` hold code 0.
+ *   activations: codes [m, 128 kb], scales [kb, m] (one a token and 128 columns);
+ *   weights:     codes [rows, 128 kb], scales [ceil(rows / 128), kb] (one a
+ *                128 x 128 block); of several experts, one after another.
+ * Scales are arbitrary fp32 values.  Element types of inputs and results: */
+enum { BQM_F32 = 0, BQM_BF16 = 1, BQM_F16 = 2 };
+
+/* Quantize activations (8-bit activations with a scale a group: Needle article,
+ * section 1, there with integer codes).  x [device] `dtype` [m, k] with rows
+ * x_stride elements apart; with swiglu != 0 the rows are [gate | up] of 2 k
+ * elements and v = gate / (1 + exp(-gate)) * up is quantized, else v = x.
+ * Per token and block, a = max |v|:
+ *   s = max(RN(a / 448), 2^-126), 1 if a = 0, NaN if a is not finite;
+ *   q = E4M3(clamp(RN(v / s), -448, 448)), half to even.
+ * A block that holds a NaN or an infinity gets a NaN scale and NaN codes.
+ * q [device] uint8 [m, 128 kb], 16-byte aligned; scale [device] fp32 [kb, m].
+ * x needs its element's alignment only (16-byte aligned rows are read faster).
+ * BQM_EINVAL for x_stride below the row's length; k <= 2^22. */
+int fp8_quant(const void *x, int dtype, int m, int k, int64_t x_stride, int swiglu, uint8_t *q, float *scale,
+              bqm_stream_t stream);
+
+/* Quantize weights the same way, a block being 128 x 128.  w [device] `dtype`
+ * [experts, rows, cols] contiguous; q [device] uint8 [experts, rows, 128 kb],
+ * 16-byte aligned; scale [device] fp32 [experts, ceil(rows / 128), kb].
+ * experts <= 4096, rows <= 2^24, cols <= 2^22. */
+int fp8_pack(const void *w, int dtype, int experts, int rows, int cols, uint8_t *q, float *scale,
+             bqm_stream_t stream);
+
+/* y[t, r] = sum_b q_scale[b, t] w_scale[r / 128, b] sum_{j < 128} q[t, 128 b + j] w[r, 128 b + j]
+ * on the matrix cores: a block's products are exact and summed in fp32, the sum
+ * is scaled in fp32, the blocks are added in fp32 and y [device] `ydtype`
+ * [m, rows] is rounded once.  w and q 16-byte aligned.  Codes 0x7F and 0xFF are
+ * NaN and make the sums that read them NaN.  Any m >= 1. */
+int fp8_gemm(const uint8_t *w, const float *w_scale, int rows, int cols, const uint8_t *q, const float *q_scale,
+             int m, void *y, int ydtype, bqm_stream_t stream);
+
+/* The same sum with a matrix for each expert and ragged groups of rows: row p of
+ * y with offsets[e] <= p < offsets[e + 1] is the product of expert e's matrix
+ * and activation row row_ids[p] (row p when row_ids is NULL).
+ * w [device] [experts, rows, 128 kb]; offsets [device] int32 [experts + 1],
+ * ascending, offsets[experts] <= slots; row_ids [device] int32 [slots] or NULL;
+ * q [device] [m, 128 kb]; y [device] `ydtype` [slots, rows], of which the rows
+ * below offsets[0] or from offsets[experts] on are not written.  The offsets stay
+ * on the device: the launch is sized from `slots` and `experts` alone.  Experts
+ * without rows cost nothing but their offsets.  Offsets outside [0, slots] are
+ * taken as the nearer end and row numbers outside [0, m) as an end of it, so
+ * that no index leaves its buffer.  Without row_ids slots <= m (BQM_EINVAL). */
+int fp8_gemm_grouped(const uint8_t *w, const float *w_scale, int experts, int rows, int cols, const uint8_t *q,
+                     const float *q_scale, int m, const int32_t *offsets, const int32_t *row_ids, int slots, void *y,
+                     int ydtype, bqm_stream_t stream);
+
+/* ---- mixture of experts: routing and combination ----
+ * Bytes of device workspace that moe_route needs (0 for few tokens).  Host only.
+ * BQM_ENOTSUP past 1024 experts, top > 32 or tokens * top > 2^30. */
+int moe_route_workspace(int tokens, int experts, int top, int64_t *bytes);
+
+/* Choose each token's `top` experts and sort the (token, expert) pairs.
+ * logits [device] `dtype` [tokens, experts], rows `stride` elements apart.
+ * The largest logits win, the lower expert on ties; NaN counts as -inf; -inf
+ * is never chosen (a masked expert); +inf counts as the largest fp32 value.
+ *   ids [tokens, top] int32: the chosen experts, largest logit first, -1 where
+ *     fewer than `top` are left;
+ *   weights [tokens, top] fp32: softmax over the chosen logits (renorm != 0) or
+ *     over all the token's logits; 0 where the id is -1;
+ *   offsets [experts + 1] int32: the pairs of expert e are sorted pairs
+ *     offsets[e] .. offsets[e + 1] - 1, its tokens ascending;
+ *   row_ids [tokens * top] int32: the token of each sorted pair, -1 past the last;
+ *   slots [tokens, top] int32: where each pair went, -1 where the id is -1.
+ * All [device].  workspace [device, 4-byte aligned, may be NULL when none is
+ * needed] needs no clearing and may be reused by the next call on the stream.
+ * The result does not depend on the order of execution. */
+int moe_route(const void *logits, int dtype, int tokens, int experts, int64_t stride, int top, int renorm,
+              int32_t *ids, float *weights, int32_t *offsets, int32_t *row_ids, int32_t *slots, void *workspace,
+              int64_t workspace_bytes, bqm_stream_t stream);
+
+/* out[t] = sum_j weights[t, j] * y[slots[t, j]], j ascending, in fp32, rounded
+ * once; slots outside [0, y_rows) are left out (no row of y is read for them).
+ * y [device] `dtype` [y_rows, d] and out [device] `dtype` [tokens, d], 16-byte
+ * aligned; slots [device] int32 and weights [device] fp32 [tokens, top]. */
+int moe_combine(const void *y, int dtype, int64_t y_rows, int d, const int32_t *slots, const float *weights,
+                int tokens, int top, void *out, bqm_stream_t stream);
+
 /* Human-readable name of an error code (static string). */
 const char *bqm_strerror(int code);
 
