@@ -554,6 +554,8 @@ int fp8_gemm_grouped(const uint8_t *w, const float *w_scale, int experts, int ro
       slots < 1 || !known_dtype(ydtype) || (!row_ids && slots > m))
     return BQM_EINVAL;
   if (experts > kMaxFp8Experts || cols > kMaxFp8Cols || rows > kMaxFp8Rows) return BQM_ENOTSUP;
+  // gathered rows are addressed with 32-bit offsets from the first
+  if (row_ids && (int64_t)m * (((int64_t)cols + 127) / 128 * 128) >= (int64_t)1 << 32) return BQM_ENOTSUP;
   if (!aligned16(w) || !aligned16(q) || ((uintptr_t)w_scale & 3u) || ((uintptr_t)q_scale & 3u) ||
       ((uintptr_t)offsets & 3u) || ((uintptr_t)row_ids & 3u) || ((uintptr_t)y & (unsigned)(elem_size(ydtype) - 1)))
     return BQM_EALIGN;

@@ -423,7 +423,8 @@ int fp8_gemm(const uint8_t *w, const float *w_scale, int rows, int cols, const u
  * on the device: the launch is sized from `slots` and `experts` alone.  Experts
  * without rows cost nothing but their offsets.  Offsets outside [0, slots] are
  * taken as the nearer end and row numbers outside [0, m) as an end of it, so
- * that no index leaves its buffer.  Without row_ids slots <= m (BQM_EINVAL). */
+ * that no index leaves its buffer.  Without row_ids slots <= m (BQM_EINVAL); with
+ * them m * 128 kb < 2^32 (BQM_ENOTSUP: rows are found by 32-bit offsets). */
 int fp8_gemm_grouped(const uint8_t *w, const float *w_scale, int experts, int rows, int cols, const uint8_t *q,
                      const float *q_scale, int m, const int32_t *offsets, const int32_t *row_ids, int slots, void *y,
                      int ydtype, bqm_stream_t stream);

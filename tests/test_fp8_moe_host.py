@@ -72,6 +72,7 @@ def test_gemm_refuses(lib, args, code):
     ((P, P, 4, 8, 128, P, P, 1, P, P, 0, P, 0, None), EINVAL),
     ((P, P, 4, 8, 128, P, P, 7, P, None, 8, P, 0, None), EINVAL),      # without row_ids slots <= m
     ((P, P, 4097, 8, 128, P, P, 1, P, P, 8, P, 0, None), ENOTSUP),
+    ((P, P, 4, 8, 4096, P, P, 1 << 20, P, P, 8, P, 0, None), ENOTSUP),  # gathered rows of 2^32 bytes
     ((P, P, 4, 8, 128, P, P, 1, ODD, P, 8, P, 0, None), EALIGN),
     ((P, P, 4, 8, 128, P, P, 1, P, ODD, 8, P, 0, None), EALIGN),
 ])
