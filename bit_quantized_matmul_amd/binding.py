@@ -164,9 +164,15 @@ def _codebook_ptr(codebook, levels=None):
 
 # ---------------------------------------------------------------- device calls
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream():
@@ -531,30 +537,77 @@ def fp8_blocks(cols: int) -> int:
     return (cols + FP8_BLOCK - 1) // FP8_BLOCK
 
 
+_DTYPE_CODES = None
+
+
 def _dtype_code(dtype, name):
-    torch = _torch()
-    code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(dtype)
+    global _DTYPE_CODES
+    if _DTYPE_CODES is None:
+        torch = _torch()
+        _DTYPE_CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    code = _DTYPE_CODES.get(dtype)
     if code is None:
         raise ValueError(f"{name} must be float32, bfloat16 or float16, got {dtype}")
     return code
 
 
-def _row_strided(t, name):
-    """A 2-D tensor whose rows are contiguous: (pointer, dtype code, row stride)."""
+# The calls below take a few microseconds on the device for one token, so what
+# the host does for them counts: each operand is checked in one pass over its
+# attributes, and the messages are formed only when a check fails.
+
+def _current():
+    """(current device, its current stream as an integer)."""
+    c = _torch()._C
+    d = c._cuda_getDevice()
+    return d, c._cuda_getCurrentRawStream(d)
+
+
+def _operand(t, dtype, shape, device, name):
+    """The address of a contiguous `dtype` tensor of `shape` on the current device."""
+    try:
+        if t.get_device() == device and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _shape(t, shape, name)
+    _dev(t, dtype, name)
+    raise ValueError(f"{name} must be on the current device {device}, got {t.device}")
+
+
+def _row_strided(t, device, name):
+    """A 2-D tensor whose rows are contiguous: (address, dtype code, row stride)."""
     torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.ndim != 2:
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor, got {tuple(getattr(t, 'shape', ()))}")
     code = _dtype_code(t.dtype, name)
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA/HIP tensor")
-    if t.shape[0] < 1 or t.shape[1] < 1:
+    n, cols = t.shape
+    if n < 1 or cols < 1:
         raise ValueError(f"{name} must not be empty, got {tuple(t.shape)}")
-    rows, cols = t.stride()
-    if cols != 1 and t.shape[1] > 1:
+    row, col = t.stride()
+    if col != 1 and cols > 1:
         raise ValueError(f"{name}'s rows must be contiguous (stride {t.stride()})")
-    if t.shape[0] > 1 and rows < t.shape[1]:
+    if n > 1 and row < cols:
         raise ValueError(f"{name}'s rows must not overlap (stride {t.stride()})")
-    return ctypes.c_void_p(t.data_ptr()), code, rows
+    if t.get_device() != device:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA/HIP tensor")
+        raise ValueError(f"{name} must be on the current device {device}, got {t.device}")
+    return t.data_ptr(), code, row, n, cols
+
+
+def _result(y, dtype, shape, device, name="y"):
+    """y, or a new tensor, as (tensor, address)."""
+    if y is None:
+        y = _torch().empty(shape, dtype=dtype, device=device)
+        return y, y.data_ptr()
+    return y, _operand(y, dtype, shape, device, name)
+
+
+def _device_of(t, name):
+    """The current device and stream; refuses a host tensor before anything else is done."""
+    if not getattr(t, "is_cuda", False):
+        raise ValueError(f"{name} must be a CUDA/HIP tensor")
+    return _current()
 
 
 def fp8_quant(x, swiglu: bool = False, q=None, scale=None):
@@ -563,22 +616,21 @@ def fp8_quant(x, swiglu: bool = False, q=None, scale=None):
     ceil(k / 128).  With swiglu, x is [m, 2 k] = [gate | up] and silu(gate) * up
     is quantized."""
     torch = _torch()
-    xp, code, stride = _row_strided(x, "x")
-    m, k = x.shape
+    if getattr(x, "ndim", 0) != 2:
+        raise ValueError(f"x must be a 2-D tensor, got {tuple(getattr(x, 'shape', ()))}")
+    _dtype_code(x.dtype, "x")
+    dev, stream = _device_of(x, "x")
+    xp, code, stride, m, k = _row_strided(x, dev, "x")
     if swiglu:
         if k % 2:
             raise ValueError(f"x must hold gate and up columns, got {k}")
         k //= 2
-    kb = fp8_blocks(k)
-    if q is None:
-        q = torch.empty((m, kb * FP8_BLOCK), dtype=torch.float8_e4m3fn, device=x.device)
-    if scale is None:
-        scale = torch.empty((kb, m), dtype=torch.float32, device=x.device)
-    _shape(q, (m, kb * FP8_BLOCK), "q")
-    _shape(scale, (kb, m), "scale")
-    _check("fp8_quant", load_library().fp8_quant(
-        xp, code, m, k, stride, int(swiglu), _dev(q, torch.float8_e4m3fn, "q"),
-        _dev(scale, torch.float32, "scale"), _stream()))
+    kb = (k + 127) // 128
+    q, qp = _result(q, torch.float8_e4m3fn, (m, kb * FP8_BLOCK), dev, "q")
+    scale, sp = _result(scale, torch.float32, (kb, m), dev, "scale")
+    rc = load_library().fp8_quant(xp, code, m, k, stride, bool(swiglu), qp, sp, stream)
+    if rc:
+        _check("fp8_quant", rc)
     return q, scale
 
 
@@ -590,49 +642,58 @@ def fp8_pack(w, q=None, scale=None):
     if getattr(w, "ndim", 0) not in (2, 3) or w.numel() < 1:
         raise ValueError(f"w must be [rows, cols] or [experts, rows, cols], got {tuple(getattr(w, 'shape', ()))}")
     code = _dtype_code(w.dtype, "w")
+    dev, stream = _device_of(w, "w")
+    wp = _operand(w, w.dtype, w.shape, dev, "w")
     lead, (rows, cols) = tuple(w.shape[:-2]), w.shape[-2:]
     kb = fp8_blocks(cols)
-    if q is None:
-        q = torch.empty((*lead, rows, kb * FP8_BLOCK), dtype=torch.float8_e4m3fn, device=w.device)
-    if scale is None:
-        scale = torch.empty((*lead, fp8_blocks(rows), kb), dtype=torch.float32, device=w.device)
-    _shape(q, (*lead, rows, kb * FP8_BLOCK), "q")
-    _shape(scale, (*lead, fp8_blocks(rows), kb), "scale")
-    _check("fp8_pack", load_library().fp8_pack(
-        _dev(w, w.dtype, "w"), code, lead[0] if lead else 1, rows, cols,
-        _dev(q, torch.float8_e4m3fn, "q"), _dev(scale, torch.float32, "scale"), _stream()))
+    q, qp = _result(q, torch.float8_e4m3fn, (*lead, rows, kb * FP8_BLOCK), dev, "q")
+    scale, sp = _result(scale, torch.float32, (*lead, fp8_blocks(rows), kb), dev, "scale")
+    _check("fp8_pack", load_library().fp8_pack(wp, code, lead[0] if lead else 1, rows, cols, qp, sp, stream))
     return q, scale
 
 
-def _fp8_operands(w, w_scale, cols, q, q_scale, lead):
-    """Check a product's operands; returns (rows, m)."""
+def _result_type(y, dtype):
+    """The type of a product's result: the given tensor's, the one asked for, or bfloat16."""
+    if y is None:
+        return _torch().bfloat16 if dtype is None else dtype
+    if dtype is not None and y.dtype != dtype:
+        raise ValueError(f"y must be {dtype}, got {y.dtype}")
+    return y.dtype
+
+
+def _product_shapes(w, cols, q, lead):
+    """rows, m and the padded columns of a product, from its operands' shapes."""
     if cols < 1:
         raise ValueError(f"cols must be at least 1, got {cols}")
-    kb = fp8_blocks(cols)
-    if getattr(w, "ndim", 0) != lead + 2 or w.shape[-1] != kb * FP8_BLOCK or min(w.shape) < 1:
-        raise ValueError(f"w must have shape [{'experts, ' * lead}rows, {kb * FP8_BLOCK}], "
-                         f"got {tuple(getattr(w, 'shape', ()))}")
-    rows = int(w.shape[-2])
-    _shape(w_scale, (*w.shape[:-2], fp8_blocks(rows), kb), "w_scale")
-    m = _rows2d(q, kb * FP8_BLOCK, "q")
-    _shape(q_scale, (kb, m), "q_scale")
-    return rows, m
+    kp = (cols + 127) // 128 * 128
+    ws, qs = getattr(w, "shape", ()), getattr(q, "shape", ())
+    if len(ws) != lead + 2 or ws[-1] != kp or min(ws) < 1:
+        raise ValueError(f"w must have shape [{'experts, ' * lead}rows, {kp}], got {tuple(ws)}")
+    if len(qs) != 2 or qs[1] != kp or qs[0] < 1:
+        _rows2d(q, kp, "q")
+    return ws[-2], qs[0], kp
 
 
 def fp8_gemm(w, w_scale, cols: int, q, q_scale, dtype=None, y=None):
     """fp8_pack weights [rows, cols] x fp8_quant activations [m, cols] -> y [m, rows] of
     `dtype` (float32, bfloat16, the default, or float16)."""
     torch = _torch()
-    rows, m = _fp8_operands(w, w_scale, cols, q, q_scale, 0)
-    if y is None:
-        y = torch.empty((m, rows), dtype=dtype or torch.bfloat16, device=q.device)
-    elif dtype is not None and y.dtype != dtype:
-        raise ValueError(f"y must be {dtype}, got {y.dtype}")
-    _shape(y, (m, rows), "y")
     f8, f32 = torch.float8_e4m3fn, torch.float32
-    _check("fp8_gemm", load_library().fp8_gemm(
-        _dev(w, f8, "w"), _dev(w_scale, f32, "w_scale"), rows, cols, _dev(q, f8, "q"),
-        _dev(q_scale, f32, "q_scale"), m, _dev(y, y.dtype, "y"), _dtype_code(y.dtype, "y"), _stream()))
+    rows, m, kp = _product_shapes(w, cols, q, 0)
+    kb = kp // FP8_BLOCK
+    ydtype = _result_type(y, dtype)
+    _shape(w_scale, ((rows + 127) // 128, kb), "w_scale")
+    _shape(q_scale, (kb, m), "q_scale")
+    ycode = _dtype_code(ydtype, "y")
+    dev, stream = _device_of(q, "q")
+    wp = _operand(w, f8, (rows, kp), dev, "w")
+    wsp = _operand(w_scale, f32, ((rows + 127) // 128, kb), dev, "w_scale")
+    qp = _operand(q, f8, (m, kp), dev, "q")
+    qsp = _operand(q_scale, f32, (kb, m), dev, "q_scale")
+    y, yp = _result(y, ydtype, (m, rows), dev)
+    rc = load_library().fp8_gemm(wp, wsp, rows, cols, qp, qsp, m, yp, ycode, stream)
+    if rc:
+        _check("fp8_gemm", rc)
     return y
 
 
@@ -642,25 +703,28 @@ def fp8_gemm_grouped(w, w_scale, cols: int, q, q_scale, offsets, row_ids=None, d
     activation rows row_ids[p] (rows p without row_ids, and then slots = m).  Rows of
     y outside every expert's range are not written."""
     torch = _torch()
-    rows, m = _fp8_operands(w, w_scale, cols, q, q_scale, 1)
-    experts = int(w.shape[0])
+    f8, f32, i32 = torch.float8_e4m3fn, torch.float32, torch.int32
+    rows, m, kp = _product_shapes(w, cols, q, 1)
+    experts, kb = w.shape[0], kp // FP8_BLOCK
+    ydtype = _result_type(y, dtype)
+    ycode = _dtype_code(ydtype, "y")
     _shape(offsets, (experts + 1,), "offsets")
     slots = m
     if row_ids is not None:
         if getattr(row_ids, "ndim", 0) != 1 or row_ids.shape[0] < 1:
             raise ValueError(f"row_ids must have shape [slots], got {tuple(getattr(row_ids, 'shape', ()))}")
-        slots = int(row_ids.shape[0])
-    if y is None:
-        y = torch.empty((slots, rows), dtype=dtype or torch.bfloat16, device=q.device)
-    elif dtype is not None and y.dtype != dtype:
-        raise ValueError(f"y must be {dtype}, got {y.dtype}")
-    _shape(y, (slots, rows), "y")
-    f8, f32, i32 = torch.float8_e4m3fn, torch.float32, torch.int32
-    _check("fp8_gemm_grouped", load_library().fp8_gemm_grouped(
-        _dev(w, f8, "w"), _dev(w_scale, f32, "w_scale"), experts, rows, cols, _dev(q, f8, "q"),
-        _dev(q_scale, f32, "q_scale"), m, _dev(offsets, i32, "offsets"),
-        None if row_ids is None else _dev(row_ids, i32, "row_ids"), slots, _dev(y, y.dtype, "y"),
-        _dtype_code(y.dtype, "y"), _stream()))
+        slots = row_ids.shape[0]
+    dev, stream = _device_of(q, "q")
+    wp = _operand(w, f8, (experts, rows, kp), dev, "w")
+    wsp = _operand(w_scale, f32, (experts, (rows + 127) // 128, kb), dev, "w_scale")
+    qp = _operand(q, f8, (m, kp), dev, "q")
+    qsp = _operand(q_scale, f32, (kb, m), dev, "q_scale")
+    op = _operand(offsets, i32, (experts + 1,), dev, "offsets")
+    rp = None if row_ids is None else _operand(row_ids, i32, (slots,), dev, "row_ids")
+    y, yp = _result(y, ydtype, (slots, rows), dev)
+    rc = load_library().fp8_gemm_grouped(wp, wsp, experts, rows, cols, qp, qsp, m, op, rp, slots, yp, ycode, stream)
+    if rc:
+        _check("fp8_gemm_grouped", rc)
     return y
 
 
@@ -682,27 +746,31 @@ def moe_route_workspace(tokens: int, experts: int, top: int) -> int:
 def moe_route(logits, top: int, renorm: bool = True, workspace=None) -> MoeRoute:
     """logits [tokens, experts] -> MoeRoute: the `top` largest logits of each token, their
     softmax weights (over the chosen with renorm, else over all) and the pairs sorted
-    by expert."""
+    by expert.  The results share one allocation."""
     torch = _torch()
-    lp, code, stride = _row_strided(logits, "logits")
-    tokens, experts = logits.shape
+    if getattr(logits, "ndim", 0) != 2:
+        raise ValueError(f"logits must be a 2-D tensor, got {tuple(getattr(logits, 'shape', ()))}")
+    dev, stream = _device_of(logits, "logits")
+    lp, code, stride, tokens, experts = _row_strided(logits, dev, "logits")
     need = moe_route_workspace(tokens, experts, top)
-    dev, i32 = logits.device, torch.int32
     if workspace is None and need:
         workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    wp = None
     if workspace is not None:
         _at_least(workspace, need, "workspace")
+        wp = _operand(workspace, torch.uint8, workspace.shape, dev, "workspace")
     pairs = tokens * top
-    r = MoeRoute(torch.empty((tokens, top), dtype=i32, device=dev),
-                 torch.empty((tokens, top), dtype=torch.float32, device=dev),
-                 torch.empty((experts + 1,), dtype=i32, device=dev),
-                 torch.empty((pairs,), dtype=i32, device=dev),
-                 torch.empty((tokens, top), dtype=i32, device=dev))
-    _check("moe_route", load_library().moe_route(
-        lp, code, tokens, experts, stride, top, int(renorm), r.ids.data_ptr(), r.weights.data_ptr(),
-        r.offsets.data_ptr(), r.row_ids.data_ptr(), r.slots.data_ptr(),
-        None if workspace is None else _dev(workspace, torch.uint8, "workspace"), need, _stream()))
-    return r
+    # one buffer: ids, slots, row_ids, weights, offsets
+    base = torch.empty((4 * pairs + experts + 1,), dtype=torch.int32, device=dev)
+    p = base.data_ptr()
+    rc = load_library().moe_route(
+        lp, code, tokens, experts, stride, top, bool(renorm), p, p + 12 * pairs, p + 16 * pairs, p + 8 * pairs,
+        p + 4 * pairs, wp, need, stream)
+    if rc:
+        _check("moe_route", rc)
+    ids, slots, row_ids, weights, offsets = base.split((pairs, pairs, pairs, pairs, experts + 1))
+    return MoeRoute(ids.view(tokens, top), weights.view(torch.float32).view(tokens, top), offsets, row_ids,
+                    slots.view(tokens, top))
 
 
 def moe_combine(y, slots, weights, out=None):
@@ -715,11 +783,14 @@ def moe_combine(y, slots, weights, out=None):
         raise ValueError(f"slots must have shape [tokens, top], got {tuple(getattr(slots, 'shape', ()))}")
     code = _dtype_code(y.dtype, "y")
     tokens, top = slots.shape
+    rows, d = y.shape
     _shape(weights, (tokens, top), "weights")
-    if out is None:
-        out = torch.empty((tokens, y.shape[1]), dtype=y.dtype, device=y.device)
-    _shape(out, (tokens, y.shape[1]), "out")
-    _check("moe_combine", load_library().moe_combine(
-        _dev(y, y.dtype, "y"), code, y.shape[0], y.shape[1], _dev(slots, torch.int32, "slots"),
-        _dev(weights, torch.float32, "weights"), tokens, top, _dev(out, y.dtype, "out"), _stream()))
+    dev, stream = _device_of(y, "y")
+    yp = _operand(y, y.dtype, (rows, d), dev, "y")
+    sp = _operand(slots, torch.int32, (tokens, top), dev, "slots")
+    wp = _operand(weights, torch.float32, (tokens, top), dev, "weights")
+    out, op = _result(out, y.dtype, (tokens, d), dev, "out")
+    rc = load_library().moe_combine(yp, code, rows, d, sp, wp, tokens, top, op, stream)
+    if rc:
+        _check("moe_combine", rc)
     return out
