@@ -4,23 +4,17 @@
 //   y[t, r] = sum_b sx[b, t] * sw[r / 128, b] * sum_{j < 128} q[t, 128 b + j] * w[r, 128 b + j]
 //
 // The blocks' sums are scaled and added in fp32 and y is rounded once.  A block's own
-// sum is formed on the matrix cores in one of two ways:
+// sum is exact to fp32: the codes become fp16 in registers (E4M3 is exact there, two
+// codes an instruction) and the fp16 matrix instructions sum their products in fp32.
+// The 8-bit instructions are faster (a 4096 x 14336 x 4096 product 269 against 418 us) but
+// keep, of each 8 products, only the 13 bits below the largest one: measured, 4e-5
+// of the result's norm where a few columns are 30 times the others, which is how
+// activations are.  fp32 sums are 100 times nearer, so they are not used.
 //
-//  * exactly: the codes become fp16 in registers (E4M3 is exact there), and the fp16
-//    instruction sums products in fp32.  Results in fp32, few rows a matrix (bound by
-//    reading the weights, so the conversions are free) and short rows take this.
-//  * natively: v_mfma_f32_16x16x128_f8f6f4 spans a block in one instruction at four
-//    times the fp16 instruction's rate a byte.  It keeps, of each 8 products, only 13
-//    bits below the largest one: measured, 1.7e-5 of the result's norm.  That is 1 / 100
-//    of a bf16 result's rounding and 1 / 14 of an fp16 one's, so results in 16 bits
-//    take it, from 8 blocks on, where the errors of the blocks average out.
-//
-// The weights are the instruction's A operand (16 weight rows), the tokens its B
-// operand (16 tokens), so a lane's four results are four neighbouring rows of one
-// token: one scale a lane and block, and stores of four elements.  Any order of the 128
-// columns does, as long as both operands use the same one: lane group g holds the
-// 16-byte chunks g and g + 4 of a row, so that one load instruction reads 64
-// neighbouring bytes of each of 16 rows.
+// The weights are the instruction's A operand, the tokens its B operand, so a lane's
+// results are groups of four neighbouring rows of one token: one scale a lane and
+// block, and stores of four elements.  Any order of the 128 columns does, as long as both
+// operands use the same one.
 #include "lowp_types.h"
 
 namespace bqm {
@@ -28,7 +22,6 @@ namespace {
 
 constexpr int kBlk = 128;
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 struct Fp8Args {
@@ -41,46 +34,23 @@ struct Fp8Args {
   int experts, rows, kb, m, slots;
 };
 
-__device__ __forceinline__ f32x4_t mma(i32x8 w, i32x8 q) {
-  const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, q, zero, 0, 0, 0, 0, 0, 0);
-}
-
-// The block's sum with fp32's precision: the codes as fp16, in which E4M3 is exact,
-// on v_mfma_f32_16x16x32_f16, which keeps products and sums of them to fp32.
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-struct Halves {
-  f16x8 k[4];
-};
-
-__device__ __forceinline__ Halves widen(i32x8 c) {
-  Halves h;
+// Eight codes as fp16.
+__device__ __forceinline__ f16x8 widen(int lo, int hi) {
+  f16x8 h;
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[2 * s + i], 1.0f, false);
-      const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[2 * s + i], 1.0f, true);
-      h.k[s][4 * i] = a[0];
-      h.k[s][4 * i + 1] = a[1];
-      h.k[s][4 * i + 2] = b[0];
-      h.k[s][4 * i + 3] = b[1];
-    }
+  for (int i = 0; i < 2; ++i) {
+    const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(i ? hi : lo, 1.0f, false);
+    const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(i ? hi : lo, 1.0f, true);
+    h[4 * i] = a[0];
+    h[4 * i + 1] = a[1];
+    h[4 * i + 2] = b[0];
+    h[4 * i + 3] = b[1];
   }
   return h;
-}
-
-__device__ __forceinline__ f32x4_t mma(const Halves &w, const Halves &q) {
-  f32x4_t c = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_16x16x32_f16(w.k[s], q.k[s], c, 0, 0, 0);
-  return c;
-}
-
-__device__ __forceinline__ i32x8 join(i32x4 a, i32x4 b) {
-  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
 // A workgroup's part of y: rows [p0, p1) (at most BM) of expert e, weight rows from n0.
@@ -231,10 +201,16 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Args A, Y *__res
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
       if (b0 + d * NW < A.kb) {
-        const Halves wh = widen(join(wl[d][0], wl[d][1]));
+        f16x8 wh[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) wh[k] = widen(wl[d][k / 2][2 * (k & 1)], wl[d][k / 2][2 * (k & 1) + 1]);
 #pragma unroll
         for (int f = 0; f < MF; ++f) {
-          const f32x4_t part = mma(wh, widen(join(ql[d][f][0], ql[d][f][1])));
+          f32x4_t part = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            part = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                wh[k], widen(ql[d][f][k / 2][2 * (k & 1)], ql[d][f][k / 2][2 * (k & 1) + 1]), part, 0, 0, 0);
           const float s = sc[d][f] * sw[d];
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[f][i] = fmaf(part[i], s, acc[f][i]);
@@ -259,18 +235,48 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Args A, Y *__res
 // ------------------------------------------------------------------ tiles
 //
 // BM tokens x BN weight rows, WM x WN waves.  Per block of 128 columns both
-// operands' tiles go to LDS without passing through registers, into one of two
-// buffers while the other is multiplied.  A tile's rows are 128 bytes; chunk c of
-// row r is stored at chunk c ^ ((r >> 1) & 7), so that the 16 rows a fragment
-// load touches at one chunk lie in 16 different groups of four banks.
-template <typename Y, int BM, int BN, int WM, int WN, bool kExact>
-__global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args A, Y *__restrict__ y) {
+// operands' tiles and scales go to LDS without passing through registers, into one of
+// two buffers while the other is multiplied.  A tile's rows are 128 bytes; chunk c of
+// row r is stored at chunk c ^ ((r >> 1) & 7), so that the 16 rows a fragment load
+// touches at one chunk lie in 16 different groups of four banks.
+// Buffer loads, so that the next block costs one scalar addition instead of a 64-bit
+// vector one a load (441 against 443 us).
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void *base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, -1, 0x00020000);
+}
+
+// A wave's 1 KiB (8 rows of 128 bytes) of each of N loads, `step` bytes apart in LDS.
+template <int N>
+__device__ __forceinline__ void stage_rows(const uint8_t *base, const uint32_t *off, int add, uint8_t *to, int step) {
+  const __amdgpu_buffer_rsrc_t r = rsrc_of(base);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(to + i * step), 16, off[i], add, 0, 0);
+}
+
+// 64 scales, one a lane.
+__device__ __forceinline__ void stage_scales(const float *base, uint32_t off, uint8_t *to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc_of(base), (lds_void *)to, 4, off, 0, 0, 0);
+}
+
+// The wave's own loads to LDS have landed and its reads are done, then so are everyone's.
+__device__ __forceinline__ void wait_and_meet() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+template <typename Y, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args A, Y *__restrict__ y) {
   constexpr int NW = WM * WN;
-  constexpr int TM = BM / WM / 16, TN = BN / WN / 16;         // fragments a wave
-  constexpr int kRowsPerLoad = NW * 8;                         // rows all waves bring in one load
+  constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
+  constexpr int kRowsPerLoad = NW * 8;
   constexpr int LM = BM / kRowsPerLoad, LN = BN / kRowsPerLoad;
   static_assert(BM % kRowsPerLoad == 0 && BN % kRowsPerLoad == 0, "whole loads");
-  constexpr int kStage = (BM + BN) * kBlk;
+  static_assert(BN <= kBlk && kBlk % BN == 0 && BM % 64 == 0 && BM / 64 < NW, "one scale block of weights a tile");
+  constexpr int kScale = (BM + BN) * kBlk;                      // scales behind the codes
+  constexpr int kStage = kScale + (BM + 64) * 4;
   __shared__ __align__(1024) uint8_t lds[2 * kStage];
 
   Tile t;
@@ -278,12 +284,11 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args A, Y *__
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % WM, wn = wave / WM;
-  const int row = lane & 15, grp = lane >> 4;
+  const int row = lane & 31, half = lane >> 5;
   const int64_t kp = (int64_t)A.kb * kBlk;
 
-  // loads: wave w brings rows 8 w .. 8 w + 7 of every kRowsPerLoad.  Addresses are a
-  // uniform base and 32-bit offsets: from the tile's first row, or, for gathered rows,
-  // from the first activation.
+  // loads: wave w brings rows 8 w .. 8 w + 7 of every kRowsPerLoad, from a uniform base
+  // (the tile's first row, or, for gathered rows, the first activation) and 32-bit offsets
   const int lr = wave * 8 + (lane >> 3), slot = lane & 7;
   const uint32_t kp32 = (uint32_t)A.kb * kBlk;
   const uint8_t *qb = A.q + (A.row_ids ? 0 : t.p0 * kp);
@@ -299,108 +304,85 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args A, Y *__
     const int r = (i < LM ? i : i - LM) * kRowsPerLoad + lr;
     src[i] = (uint32_t)(i < LM ? q_row(r) : min(r, nmax)) * kp32 + ((slot ^ ((r >> 1) & 7)) << 4);
   }
-  auto load_stage = [&](int buf, int b) {
-    uint8_t *base = lds + buf * kStage + wave * 1024;
-#pragma unroll
-    for (int i = 0; i < LM + LN; ++i) {
-      const int off = i * kRowsPerLoad * kBlk;
-      const uint8_t *from = (i < LM ? qb : wb) + (int64_t)b * kBlk;
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(from + src[i]),
-                                       (__attribute__((address_space(3))) void *)(base + off), 16, 0, 0);
-    }
+  // scales: the first BM / 64 waves bring the tokens', the others the weights'
+  const bool token_wave = wave < BM / 64;
+  const int nblk = (A.rows + kBlk - 1) / kBlk;
+  const float *sb = token_wave ? A.qs + (A.row_ids ? 0 : t.p0) : A.ws + ((int64_t)t.e * nblk + t.n0 / kBlk) * A.kb;
+  const int64_t sstep = token_wave ? A.m : 1;
+  const uint32_t soff = token_wave ? (uint32_t)q_row(wave * 64 + lane) * 4 : 0;
+  const int sdst = kScale + (token_wave ? wave * 256 : BM * 4);
+  auto load_stage = [&](int at, int b) {
+    stage_rows<LM>(qb, src, b * kBlk, lds + at + wave * 1024, kRowsPerLoad * kBlk);
+    stage_rows<LN>(wb, src + LM, b * kBlk, lds + at + wave * 1024 + BM * kBlk, kRowsPerLoad * kBlk);
+    stage_scales(sb + b * sstep, soff, lds + at + sdst);
   };
 
-  uint32_t st[TM];
-  const float *qsb = A.qs + (A.row_ids ? 0 : t.p0);
-#pragma unroll
-  for (int f = 0; f < TM; ++f) st[f] = (uint32_t)q_row((wm * TM + f) * 16 + row);
-  const int nb = min((t.n0 + wn * TN * 16) / kBlk, (A.rows - 1) / kBlk);
-  uint32_t zero = 0;
-  asm volatile("v_mov_b32 %0, 0" : "=v"(zero));               // keeps the load below a vector load
-  const float *ws = A.ws + ((int64_t)t.e * ((A.rows + kBlk - 1) / kBlk) + nb) * A.kb;
-
-  f32x4_t acc[TN][TM] = {};
-  float sx[TM], sw;
+  f32x16 acc[TN][TM] = {};
   load_stage(0, 0);
-#pragma unroll
-  for (int f = 0; f < TM; ++f) sx[f] = qsb[st[f]];
-  sw = ws[zero];
-
-  // a fragment's two chunks: g and g + 4 at the swizzled places of its row
   const int sz = (row >> 1) & 7;
-  const int c0 = row * kBlk + ((grp ^ sz) << 4), c1 = row * kBlk + (((grp + 4) ^ sz) << 4);
+  int coff[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) coff[j] = row * kBlk + (((2 * j + half) ^ sz) << 4);
+  int at = 0;
   for (int b = 0; b < A.kb; ++b) {
-    __syncthreads();                                           // waits for this block's loads too
+    wait_and_meet();
+    if (b + 1 < A.kb) load_stage(kStage - at, b + 1);
+    const uint8_t *lq = lds + at + wm * TM * 32 * kBlk;
+    const uint8_t *lw = lds + at + BM * kBlk + wn * TN * 32 * kBlk;
+    const float *ls = reinterpret_cast<const float *>(lds + at + kScale);
+    i32x4 rq[TM][4], rw[TN][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      rw[0][j] = *reinterpret_cast<const i32x4 *>(lw + coff[j]);
+      rq[0][j] = *reinterpret_cast<const i32x4 *>(lq + coff[j]);
+    }
+#pragma unroll
+    for (int f = 1; f < TM; ++f)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) rq[f][j] = *reinterpret_cast<const i32x4 *>(lq + f * 32 * kBlk + coff[j]);
     float s[TM];
+    const float sw = ls[BM];
 #pragma unroll
-    for (int f = 0; f < TM; ++f) s[f] = sx[f] * sw;
-    if (b + 1 < A.kb) {
-      load_stage((b + 1) & 1, b + 1);
-      const float *next = qsb + (int64_t)(b + 1) * A.m;
+    for (int f = 0; f < TM; ++f) s[f] = ls[(wm * TM + f) * 32 + row] * sw;
+    // Chain c multiplies row fragment c / TM and token fragment c % TM, 8 steps of 16
+    // columns; between its steps the codes it is the first to use are widened and the sums
+    // of chain c - 1 scaled and added.
+    f16x8 qh[TM][8], wh[8];
+    f32x16 part[2];
 #pragma unroll
-      for (int f = 0; f < TM; ++f) sx[f] = next[st[f]];
-      sw = (ws + b + 1)[zero];
-    }
-    const uint8_t *lq = lds + (b & 1) * kStage + wm * TM * 16 * kBlk;
-    const uint8_t *lw = lds + (b & 1) * kStage + BM * kBlk + wn * TN * 16 * kBlk;
-    auto frag = [&](const uint8_t *p, int i) {
-      return join(*reinterpret_cast<const i32x4 *>(p + i * 16 * kBlk + c0),
-                  *reinterpret_cast<const i32x4 *>(p + i * 16 * kBlk + c1));
-    };
-    if constexpr (kExact) {
-      Halves qh[TM];
+    for (int c = 0; c <= TN * TM; ++c) {
+      const int g = c / TM, f = c % TM;
+      if (c < TN * TM && f == 0 && g + 1 < TN) {
 #pragma unroll
-      for (int f = 0; f < TM; ++f) qh[f] = widen(frag(lq, f));
+        for (int j = 0; j < 4; ++j) rw[g + 1][j] = *reinterpret_cast<const i32x4 *>(lw + (g + 1) * 32 * kBlk + coff[j]);
+      }
 #pragma unroll
-      for (int g = 0; g < TN; ++g) {
-        const Halves wh = widen(frag(lw, g));
-#pragma unroll
-        for (int f = 0; f < TM; ++f) {
-          const f32x4_t part = mma(wh, qh[f]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[g][f][i] = fmaf(part[i], s[f], acc[g][f][i]);
+      for (int k = 0; k < 8; ++k) {
+        if (c < TN * TM) {
+          if (f == 0) wh[k] = widen(rw[g][k / 2][2 * (k & 1)], rw[g][k / 2][2 * (k & 1) + 1]);
+          if (g == 0) qh[f][k] = widen(rq[f][k / 2][2 * (k & 1)], rq[f][k / 2][2 * (k & 1) + 1]);
+          const f32x16 zero = {};
+          part[c & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wh[k], qh[f][k], k ? part[c & 1] : zero, 0, 0, 0);
         }
-      }
-      continue;
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    i32x8 qf[TM], wf[2];
-    f32x4_t part[2][TM];
-    wf[0] = frag(lw, 0);
+        if (c > 0)
 #pragma unroll
-    for (int f = 0; f < TM; ++f) qf[f] = frag(lq, f);
-    // the products of row fragment g, while the sums of g - 1 are scaled and added
-#pragma unroll
-    for (int g = 0; g <= TN; ++g) {
-      if (g + 1 < TN) wf[(g + 1) & 1] = frag(lw, g + 1);
-#pragma unroll
-      for (int f = 0; f < TM; ++f) {
-        if (g < TN) part[g & 1][f] = mma(wf[g & 1], qf[f]);
-        if (g > 0)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            acc[g - 1][f][i] = fmaf(part[(g - 1) & 1][f][i], s[f], acc[g - 1][f][i]);
+          for (int i = 2 * k; i < 2 * k + 2; ++i)
+            acc[(c - 1) / TM][(c - 1) % TM][i] = fmaf(part[(c - 1) & 1][i], s[(c - 1) % TM], acc[(c - 1) / TM][(c - 1) % TM][i]);
       }
     }
-    // the order above, for the scheduler: reads ahead, then one product and four sums in turn
-    __builtin_amdgcn_sched_group_barrier(0x100, 2 + 2 * TM, 0);
-#pragma unroll
-    for (int g = 0; g <= TN; ++g) {
-      if (g + 1 < TN) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-#pragma unroll
-      for (int f = 0; f < TM; ++f) {
-        if (g < TN) __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-        if (g > 0) __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);
+    at = kStage - at;
   }
 #pragma unroll
   for (int f = 0; f < TM; ++f) {
-    const int p = t.p0 + (wm * TM + f) * 16 + row;
+    const int p = t.p0 + (wm * TM + f) * 32 + row;
     if (p >= t.p1) continue;
 #pragma unroll
-    for (int g = 0; g < TN; ++g) store4(y, A, p, t.n0 + (wn * TN + g) * 16 + grp * 4, acc[g][f]);
+    for (int g = 0; g < TN; ++g)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f32x4_t v = {acc[g][f][4 * i], acc[g][f][4 * i + 1], acc[g][f][4 * i + 2], acc[g][f][4 * i + 3]};
+        store4(y, A, p, t.n0 + (wn * TN + g) * 32 + 8 * i + 4 * half, v);
+      }
   }
 }
 
@@ -420,9 +402,9 @@ hipError_t stream(const Fp8Args &A, Y *y, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename Y, int BM, int BN, int WM, int WN, bool kExact>
+template <typename Y, int BM, int BN, int WM, int WN>
 hipError_t tile(const Fp8Args &A, Y *y, hipStream_t s) {
-  fp8_tile_kernel<Y, BM, BN, WM, WN, kExact><<<(unsigned)tiles(A, BM, BN), 64 * WM * WN, 0, s>>>(A, y);
+  fp8_tile_kernel<Y, BM, BN, WM, WN><<<(unsigned)tiles(A, BM, BN), 64 * WM * WN, 0, s>>>(A, y);
   return hipGetLastError();
 }
 
@@ -432,9 +414,8 @@ hipError_t run(const Fp8Args &A, Y *y, int num_cus, hipStream_t s) {
   const int per = A.offsets ? (A.slots + A.experts - 1) / A.experts : A.m;
   if (per <= 16) return A.kb >= 16 ? stream<Y, 1, 16, 2>(A, y, s) : stream<Y, 1, 4, 2>(A, y, s);
   if (per <= 32) return A.kb >= 16 ? stream<Y, 2, 16, 2>(A, y, s) : stream<Y, 2, 4, 2>(A, y, s);
-  if (tiles(A, 256, 256) >= num_cus) return tile<Y, 256, 256, 4, 2, true>(A, y, s);
-  if (tiles(A, 128, 128) >= num_cus) return tile<Y, 128, 128, 2, 2, true>(A, y, s);
-  return tile<Y, 64, 64, 2, 2, true>(A, y, s);
+  if (tiles(A, 128, 128) >= num_cus) return tile<Y, 128, 128, 2, 2>(A, y, s);
+  return tile<Y, 64, 64, 2, 2>(A, y, s);
 }
 
 hipError_t run_any(const Fp8Args &A, void *y, int ydtype, int num_cus, hipStream_t s) {
