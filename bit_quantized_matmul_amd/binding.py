@@ -628,7 +628,7 @@ def fp8_quant(x, swiglu: bool = False, q=None, scale=None):
     kb = (k + 127) // 128
     q, qp = _result(q, torch.float8_e4m3fn, (m, kb * FP8_BLOCK), dev, "q")
     scale, sp = _result(scale, torch.float32, (kb, m), dev, "scale")
-    rc = load_library().fp8_quant(xp, code, m, k, stride, bool(swiglu), qp, sp, stream)
+    rc = (_lib or load_library()).fp8_quant(xp, code, m, k, stride, bool(swiglu), qp, sp, stream)
     if rc:
         _check("fp8_quant", rc)
     return q, scale
@@ -682,16 +682,19 @@ def fp8_gemm(w, w_scale, cols: int, q, q_scale, dtype=None, y=None):
     rows, m, kp = _product_shapes(w, cols, q, 0)
     kb = kp // FP8_BLOCK
     ydtype = _result_type(y, dtype)
-    _shape(w_scale, ((rows + 127) // 128, kb), "w_scale")
-    _shape(q_scale, (kb, m), "q_scale")
     ycode = _dtype_code(ydtype, "y")
-    dev, stream = _device_of(q, "q")
+    nb = (rows + 127) // 128
+    if not q.is_cuda:
+        _shape(w_scale, (nb, kb), "w_scale")
+        _shape(q_scale, (kb, m), "q_scale")
+        raise ValueError("q must be a CUDA/HIP tensor")
+    dev, stream = _current()
     wp = _operand(w, f8, (rows, kp), dev, "w")
-    wsp = _operand(w_scale, f32, ((rows + 127) // 128, kb), dev, "w_scale")
+    wsp = _operand(w_scale, f32, (nb, kb), dev, "w_scale")
     qp = _operand(q, f8, (m, kp), dev, "q")
     qsp = _operand(q_scale, f32, (kb, m), dev, "q_scale")
     y, yp = _result(y, ydtype, (m, rows), dev)
-    rc = load_library().fp8_gemm(wp, wsp, rows, cols, qp, qsp, m, yp, ycode, stream)
+    rc = (_lib or load_library()).fp8_gemm(wp, wsp, rows, cols, qp, qsp, m, yp, ycode, stream)
     if rc:
         _check("fp8_gemm", rc)
     return y
@@ -708,7 +711,8 @@ def fp8_gemm_grouped(w, w_scale, cols: int, q, q_scale, offsets, row_ids=None, d
     experts, kb = w.shape[0], kp // FP8_BLOCK
     ydtype = _result_type(y, dtype)
     ycode = _dtype_code(ydtype, "y")
-    _shape(offsets, (experts + 1,), "offsets")
+    if not q.is_cuda:
+        _shape(offsets, (experts + 1,), "offsets")
     slots = m
     if row_ids is not None:
         if getattr(row_ids, "ndim", 0) != 1 or row_ids.shape[0] < 1:
@@ -722,7 +726,7 @@ def fp8_gemm_grouped(w, w_scale, cols: int, q, q_scale, offsets, row_ids=None, d
     op = _operand(offsets, i32, (experts + 1,), dev, "offsets")
     rp = None if row_ids is None else _operand(row_ids, i32, (slots,), dev, "row_ids")
     y, yp = _result(y, ydtype, (slots, rows), dev)
-    rc = load_library().fp8_gemm_grouped(wp, wsp, experts, rows, cols, qp, qsp, m, op, rp, slots, yp, ycode, stream)
+    rc = (_lib or load_library()).fp8_gemm_grouped(wp, wsp, experts, rows, cols, qp, qsp, m, op, rp, slots, yp, ycode, stream)
     if rc:
         _check("fp8_gemm_grouped", rc)
     return y
@@ -763,7 +767,7 @@ def moe_route(logits, top: int, renorm: bool = True, workspace=None) -> MoeRoute
     # one buffer: ids, slots, row_ids, weights, offsets
     base = torch.empty((4 * pairs + experts + 1,), dtype=torch.int32, device=dev)
     p = base.data_ptr()
-    rc = load_library().moe_route(
+    rc = (_lib or load_library()).moe_route(
         lp, code, tokens, experts, stride, top, bool(renorm), p, p + 12 * pairs, p + 16 * pairs, p + 8 * pairs,
         p + 4 * pairs, wp, need, stream)
     if rc:
@@ -784,13 +788,14 @@ def moe_combine(y, slots, weights, out=None):
     code = _dtype_code(y.dtype, "y")
     tokens, top = slots.shape
     rows, d = y.shape
-    _shape(weights, (tokens, top), "weights")
+    if not y.is_cuda:
+        _shape(weights, (tokens, top), "weights")
     dev, stream = _device_of(y, "y")
     yp = _operand(y, y.dtype, (rows, d), dev, "y")
     sp = _operand(slots, torch.int32, (tokens, top), dev, "slots")
     wp = _operand(weights, torch.float32, (tokens, top), dev, "weights")
     out, op = _result(out, y.dtype, (tokens, d), dev, "out")
-    rc = load_library().moe_combine(yp, code, rows, d, sp, wp, tokens, top, op, stream)
+    rc = (_lib or load_library()).moe_combine(yp, code, rows, d, sp, wp, tokens, top, op, stream)
     if rc:
         _check("moe_combine", rc)
     return out

@@ -162,11 +162,25 @@ template <typename Y, int MF, int NW, int kDepth>
 __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Args A, Y *__restrict__ y) {
   Tile t;
   if (!find_tile<16 * MF, 16>(A, blockIdx.x, &t)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = lane & 15, grp = lane >> 4;
   const int64_t kp = (int64_t)A.kb * kBlk;
   const uint8_t *w = A.w + ((int64_t)t.e * A.rows + min(t.n0 + row, A.rows - 1)) * kp + grp * 16;
   const float *ws = A.ws + ((int64_t)t.e * ((A.rows + kBlk - 1) / kBlk) + t.n0 / kBlk) * A.kb;
+  // the weights' addresses depend on the tile alone: they go out before the tokens are known
+  i32x4 wl[kDepth][2];
+  auto load_w = [&](int b0) {
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      const int b = b0 + d * NW;
+      if (b < A.kb) {
+        const uint8_t *p = w + (int64_t)b * kBlk;
+        wl[d][0] = __builtin_nontemporal_load(reinterpret_cast<const i32x4 *>(p));
+        wl[d][1] = __builtin_nontemporal_load(reinterpret_cast<const i32x4 *>(p + 64));
+      }
+    }
+  };
+  load_w(wave);
   const uint8_t *q[MF];
   const float *qs[MF];
 #pragma unroll
@@ -177,40 +191,38 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Args A, Y *__res
   }
   f32x4_t acc[MF] = {};
   for (int b0 = wave; b0 < A.kb; b0 += NW * kDepth) {
-    i32x4 wl[kDepth][2], ql[kDepth][MF][2];
+    i32x4 ql[kDepth][MF][2];
     float sc[kDepth][MF], sw[kDepth];
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
-      const int b = min(b0 + d * NW, A.kb - 1);
-      const uint8_t *p = w + (int64_t)b * kBlk;
-      wl[d][0] = __builtin_nontemporal_load(reinterpret_cast<const i32x4 *>(p));
-      wl[d][1] = __builtin_nontemporal_load(reinterpret_cast<const i32x4 *>(p + 64));
-    }
+      const int b = b0 + d * NW;
+      if (b < A.kb) {
+        sw[d] = ws[b];
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
-      const int b = min(b0 + d * NW, A.kb - 1);
-      sw[d] = ws[b];
-#pragma unroll
-      for (int f = 0; f < MF; ++f) {
-        const uint8_t *p = q[f] + (int64_t)b * kBlk;
-        ql[d][f][0] = *reinterpret_cast<const i32x4 *>(p);
-        ql[d][f][1] = *reinterpret_cast<const i32x4 *>(p + 64);
-        sc[d][f] = qs[f][(int64_t)b * A.m];
+        for (int f = 0; f < MF; ++f) {
+          const uint8_t *p = q[f] + (int64_t)b * kBlk;
+          ql[d][f][0] = *reinterpret_cast<const i32x4 *>(p);
+          ql[d][f][1] = *reinterpret_cast<const i32x4 *>(p + 64);
+          sc[d][f] = qs[f][(int64_t)b * A.m];
+        }
       }
     }
+    f16x8 wh[kDepth][4];
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) wh[d][k] = widen(wl[d][k / 2][2 * (k & 1)], wl[d][k / 2][2 * (k & 1) + 1]);
+    load_w(b0 + NW * kDepth);
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
       if (b0 + d * NW < A.kb) {
-        f16x8 wh[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) wh[k] = widen(wl[d][k / 2][2 * (k & 1)], wl[d][k / 2][2 * (k & 1) + 1]);
 #pragma unroll
         for (int f = 0; f < MF; ++f) {
           f32x4_t part = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             part = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                wh[k], widen(ql[d][f][k / 2][2 * (k & 1)], ql[d][f][k / 2][2 * (k & 1) + 1]), part, 0, 0, 0);
+                wh[d][k], widen(ql[d][f][k / 2][2 * (k & 1)], ql[d][f][k / 2][2 * (k & 1) + 1]), part, 0, 0, 0);
           const float s = sc[d][f] * sw[d];
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[f][i] = fmaf(part[i], s, acc[f][i]);
@@ -412,8 +424,11 @@ template <typename Y>
 hipError_t run(const Fp8Args &A, Y *y, int num_cus, hipStream_t s) {
   // rows a matrix has to multiply: exact for one matrix, the mean for experts
   const int per = A.offsets ? (A.slots + A.experts - 1) / A.experts : A.m;
-  if (per <= 16) return A.kb >= 16 ? stream<Y, 1, 16, 2>(A, y, s) : stream<Y, 1, 4, 2>(A, y, s);
-  if (per <= 32) return A.kb >= 16 ? stream<Y, 2, 16, 2>(A, y, s) : stream<Y, 2, 4, 2>(A, y, s);
+  // 8 waves a workgroup (one token, us with 4 / 8 / 16 waves: 4096x4096 7.9 / 6.2 / 6.0,
+  // 14336x4096 16.4 / 15.7 / 18.7, 4096x14336 23.7 / 15.9 / 17.8), 4 for short rows
+  // (1092x312 2.6 / 2.7 / 3.0)
+  if (per <= 16) return A.kb > 4 ? stream<Y, 1, 8, 2>(A, y, s) : stream<Y, 1, 4, 2>(A, y, s);
+  if (per <= 32) return A.kb > 4 ? stream<Y, 2, 8, 2>(A, y, s) : stream<Y, 2, 4, 2>(A, y, s);
   if (tiles(A, 128, 128) >= num_cus) return tile<Y, 128, 128, 2, 2>(A, y, s);
   return tile<Y, 64, 64, 2, 2>(A, y, s);
 }

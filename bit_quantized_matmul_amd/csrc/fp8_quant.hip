@@ -35,16 +35,27 @@ __device__ __forceinline__ float block_scale(float a) {
   return a > 0.0f ? fmaxf(__fdiv_rn(a, kE4M3Max), 1.17549435e-38f) : 1.0f;
 }
 
-__device__ __forceinline__ float code_value(float v, float s) {
-  const float r = __fdiv_rn(v, s);
-  return r != r ? r : fminf(fmaxf(r, -kE4M3Max), kE4M3Max);
-}
-
+// The codes of 8 values of a block with scale s.  RN(v / s) without a division an
+// element: with y = RN(1 / s) and q = v y, one step q + (v - q s) y is the correctly
+// rounded quotient (Markstein), as long as the remainder v - q s is no subnormal; tiny
+// scales divide.
 __device__ __forceinline__ u32x2_t codes8(const float (&v)[8], float s) {
+  if (s != s) return u32x2_t{0x7F7F7F7Fu, 0x7F7F7F7Fu};
+  const bool tiny = s < 0x1p-60f;
+  const float y = __fdiv_rn(1.0f, s);
   float c[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) c[j] = code_value(v[j], s);
+  for (int j = 0; j < 8; ++j) {
+    const float q = v[j] * y;
+    c[j] = fmaf(fmaf(-q, s, v[j]), y, q);
+  }
+  if (tiny) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = __fdiv_rn(v[j], s);
+  }
   u32x2_t p;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) c[j] = __builtin_amdgcn_fmed3f(c[j], -kE4M3Max, kE4M3Max);
 #pragma unroll
   for (int h = 0; h < 2; ++h) p[h] = e4m3_pair(c[4 * h], c[4 * h + 1]) | e4m3_pair(c[4 * h + 2], c[4 * h + 3]) << 16;
   return p;
@@ -61,7 +72,17 @@ __device__ __forceinline__ void load8(const T *row, int c, int k, float (&v)[8])
   }
 }
 
-__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+// g / d for d = 1 + exp(-g): the reciprocal refined once, then the quotient, within
+// 0.51 units; past 2^100 (g < -69) and for NaN the plain division.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  const float d = 1.0f + expf(-g);
+  float r = __builtin_amdgcn_rcpf(d);
+  r = fmaf(fmaf(-d, r, 1.0f), r, r);
+  float q = g * r;
+  q = fmaf(fmaf(-q, d, g), r, q);
+  if (!(d < 0x1p100f) || !(fabsf(g) < 0x1p100f)) q = g / d;
+  return q * u;
+}
 
 // 16 lanes hold a block; a workgroup of 256 takes `rows` tokens x 16 / rows blocks.
 template <typename T, bool kVec, bool kSwiglu>
@@ -70,8 +91,12 @@ __global__ __launch_bounds__(256) void fp8_quant_kernel(const T *__restrict__ x,
                                                         float *__restrict__ scale) {
   const int kb = (k + kBlk - 1) / kBlk;
   const int grp = threadIdx.x >> 4, sub = threadIdx.x & 15;
-  const int row = (int)blockIdx.x * rows + grp % rows;
-  const int b = (int)blockIdx.y * (16 / rows) + grp / rows;
+  // neighbouring workgroups take neighbouring blocks of the same rows: rows are often
+  // a multiple of 8 KiB apart, and one column of many of them lies in few memory channels
+  // (2048 x 14336 with SwiGLU 47 us with neighbouring rows)
+  const int per = 16 / rows, across = (kb + per - 1) / per;
+  const int row = (int)(blockIdx.x / across) * rows + grp % rows;
+  const int b = (int)(blockIdx.x % across) * per + grp / rows;
   if (row >= m || b >= kb) return;                 // whole 16-lane groups leave together
   const T *xr = x + (int64_t)row * stride;
   const int c = b * kBlk + sub * 8;
@@ -141,7 +166,7 @@ template <typename T>
 hipError_t quant_t(const T *x, int m, int k, int64_t stride, bool swiglu, uint8_t *q, float *scale, hipStream_t s) {
   const int kb = (k + kBlk - 1) / kBlk;
   const int rows = m >= 16 ? 16 : 1;
-  const dim3 grid((m + rows - 1) / rows, (kb + 16 / rows - 1) / (16 / rows));
+  const unsigned grid = (unsigned)((m + rows - 1) / rows) * (unsigned)((kb + 16 / rows - 1) / (16 / rows));
   // 16-byte loads where every row (and, with SwiGLU, its second half) starts on 16 bytes
   const int per = 16 / (int)sizeof(T);
   const bool vec = ((uintptr_t)x & 15u) == 0 && (m == 1 || stride % per == 0) && (!swiglu || k % per == 0);

@@ -6,12 +6,12 @@
 // ones go to the lower expert; NaN counts as -inf, which is never chosen, and
 // +inf as the largest fp32 value, so that exp(l - max) stays defined.
 //
-// The order is a counting sort over chunks of kChunkTokens tokens: the first
-// kernel chooses and counts each chunk's experts, the second adds up the counts
-// of the chunks before its own and places the chunk's pairs.  The counts are sums
-// of integers, so nothing depends on the order of atomics, and a pair's rank
-// among its chunk's is found 64 pairs at a time from ballots over the expert's
-// bits.  One chunk needs no second launch.
+// The order is a counting sort over chunks of neighbouring tokens: the first kernel
+// chooses and counts each chunk's experts, the second adds up the counts of the chunks
+// before its own and places the chunk's pairs.  The counts are sums of integers, so
+// nothing depends on the order of atomics, and a pair's rank among its chunk's is
+// found 64 pairs at a time from ballots over the expert's bits.  One chunk needs no
+// second launch.
 //
 // Combine.  out[t] = sum_j weights[t, j] * y[slots[t, j]] in fp32, j ascending.
 #include "lowp_types.h"
@@ -19,7 +19,8 @@
 namespace bqm {
 namespace {
 
-constexpr int kChunkTokens = 64;
+constexpr int kChunkTokens = 64;      // of a chunk, while there are at most kMaxChunks of them
+constexpr int kMaxChunks = 512;       // every chunk reads all chunks' counts
 constexpr int kMaxExperts = 1024, kMaxTop = 32;
 constexpr int kRouteThreads = 1024;
 constexpr float kHuge = 3.4028234663852886e38f;
@@ -31,46 +32,75 @@ struct RouteArgs {
   int32_t *ids;
   float *weights;
   int32_t *offsets, *row_ids, *slots;
-  int32_t *hist;             // [chunks, experts]
+  uint16_t *hist;            // [chunks, experts rounded up to even]
+  int chunk_tokens, chunks;
 };
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+// Reductions over 16 consecutive lanes (DPP row rotations) or the wave.
+template <int CTRL>
+__device__ __forceinline__ int row_move(int v) {
+  return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xF, 0xF, false);
+}
+
+template <int LANES, typename F>
+__device__ __forceinline__ int lanes_reduce(int v, F op) {
+  v = op(v, row_move<0x121>(v));                               // row_ror 1, 2, 4, 8
+  v = op(v, row_move<0x122>(v));
+  v = op(v, row_move<0x124>(v));
+  v = op(v, row_move<0x128>(v));
+  if constexpr (LANES == 64) {
+    v = op(v, __shfl_xor(v, 16, 64));
+    v = op(v, __shfl_xor(v, 32, 64));
+  }
   return v;
 }
 
-// Order-preserving integer of a logit that is no NaN and no -0.
-__device__ __forceinline__ int order_key(float v) {
-  const int b = __float_as_int(v);
-  return b >= 0 ? b : b ^ 0x7FFFFFFF;
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float v) {
+  return __int_as_float(lanes_reduce<LANES>(__float_as_int(v), [](int a, int b) {
+    return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b)));
+  }));
 }
 
-// One wave chooses one token's experts.  Lane l holds experts l, l + 64, ...
-template <typename T, int kPer>
-__device__ void choose(const RouteArgs &A, int token, int32_t *ids_lds) {
-  const int lane = threadIdx.x & 63;
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+  return __int_as_float(lanes_reduce<LANES>(__float_as_int(v), [](int a, int b) {
+    return __float_as_int(__int_as_float(a) + __int_as_float(b));
+  }));
+}
+
+template <int LANES>
+__device__ __forceinline__ int lanes_min(int v) {
+  return lanes_reduce<LANES>(v, [](int a, int b) { return min(a, b); });
+}
+
+// LANES lanes choose one token's experts; lane l of them holds experts l, l + LANES, ...
+// Every choice is one search for the largest logit left (largest of the lane's, then of
+// the lanes', then the lowest index that has it).  counts (LDS): the chunk's, by expert.
+template <typename T, int LANES, int kPer>
+__device__ void choose(const RouteArgs &A, int token, int32_t *ids_lds, int32_t *counts) {
+  const int lane = threadIdx.x & (LANES - 1);
   const T *x = reinterpret_cast<const T *>(A.logits) + (int64_t)token * A.stride;
   float v[kPer];
   float best = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int e = lane + 64 * i;
+    const int e = lane + LANES * i;
     float l = e < A.experts ? to_f32(x[e]) : -INFINITY;
-    l = l != l ? -INFINITY : fminf(l, kHuge) + 0.0f;          // -0 becomes +0
+    l = l != l ? -INFINITY : fminf(l, kHuge);
     v[i] = l;
     best = fmaxf(best, l);
   }
-  const float top = wave_max(best);
+  const float top = lanes_max<LANES>(best);
   const float ref = top > -INFINITY ? top : 0.0f;
   float total = 0.0f;
   if (!A.renorm) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) total += expf(v[i] - ref);
-    total = wave_sum(total);
+    total = lanes_sum<LANES>(total);
   }
-  float mine = 0.0f;                                           // lane j: the j-th choice
-  int my_id = -1;
+  float w0 = 0.0f, w1 = 0.0f;                                  // the choices lane and lane + LANES
+  int id0 = -1, id1 = -1;
   for (int j = 0; j < A.top; ++j) {
     float b = -INFINITY;
     int at = 0x7FFFFFFF;
@@ -78,35 +108,43 @@ __device__ void choose(const RouteArgs &A, int token, int32_t *ids_lds) {
     for (int i = 0; i < kPer; ++i)
       if (v[i] > b) {
         b = v[i];
-        at = lane + 64 * i;
+        at = lane + LANES * i;
       }
-    const float w = wave_max(b);
-    if (w == -INFINITY) break;
-    at = b == w ? at : 0x7FFFFFFF;
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) at = min(at, __shfl_xor(at, o, 64));
+    const float w = lanes_max<LANES>(b);
+    const int got = lanes_min<LANES>(b == w ? at : 0x7FFFFFFF);   // none left: all b are -inf
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (at == lane + 64 * i) v[i] = -INFINITY;
-    if (lane == j) {
-      mine = expf(w - ref);
-      my_id = at;
+      if (got == lane + LANES * i) v[i] = -INFINITY;
+    const float e = w > -INFINITY ? expf(w - ref) : 0.0f;
+    const int id = w > -INFINITY ? got : -1;
+    if (A.renorm) total += e;
+    if (j == lane) {
+      w0 = e;
+      id0 = id;
+    } else if (j == lane + LANES) {
+      w1 = e;
+      id1 = id;
     }
   }
-  if (A.renorm) total = wave_sum(mine);
-  if (lane < A.top) {
-    const int64_t o = (int64_t)token * A.top + lane;
-    A.ids[o] = my_id;
-    A.weights[o] = my_id >= 0 ? mine / total : 0.0f;
-    ids_lds[lane] = my_id;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int j = lane + h * LANES, id = h ? id1 : id0;
+    if (j < A.top) {
+      const int64_t o = (int64_t)token * A.top + j;
+      A.ids[o] = id;
+      A.weights[o] = id >= 0 ? (h ? w1 : w0) / total : 0.0f;
+      ids_lds[j] = id;
+      if (id >= 0) atomicAdd(&counts[id], 1);
+    }
   }
 }
 
 // Places a chunk's pairs; base[e]: the first slot of the chunk's pairs of
 // expert e (advanced here).  One wave.
-__device__ void place(const RouteArgs &A, int chunk, int pairs, const int32_t *ids, int32_t *base) {
+template <typename Ids>
+__device__ void place(const RouteArgs &A, int chunk, int pairs, Ids ids, int32_t *base) {
   const int lane = threadIdx.x & 63;
-  const int64_t first = (int64_t)chunk * kChunkTokens * A.top;
+  const int64_t first = (int64_t)chunk * A.chunk_tokens * A.top;
   for (int p0 = 0; p0 < pairs; p0 += 64) {
     const int p = p0 + lane;
     const int e = p < pairs ? ids[p] : -1;
@@ -120,7 +158,7 @@ __device__ void place(const RouteArgs &A, int chunk, int pairs, const int32_t *i
     int slot = -1;
     if (e >= 0) {
       slot = base[e] + rank;
-      A.row_ids[slot] = (int)((first + p) / A.top);
+      A.row_ids[slot] = chunk * A.chunk_tokens + p / A.top;
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");      // every lane has read base[e]
     if (e >= 0 && rank == 0) base[e] += __popcll(same);
@@ -130,9 +168,10 @@ __device__ void place(const RouteArgs &A, int chunk, int pairs, const int32_t *i
 }
 
 // From before[e] (pairs of e in earlier chunks) and total[e]: the offsets into
-// before (added) and, for the first chunk, into A.offsets; row_ids past the end.
-__device__ void finish(const RouteArgs &A, int chunk, int chunks, int pairs, const int32_t *ids, int32_t *before,
-                       int32_t *total) {
+// before (added) and, for the first chunk, into A.offsets; row_ids past the end; then the
+// chunk's pairs.
+template <typename Ids>
+__device__ void finish(const RouteArgs &A, int chunk, int pairs, Ids ids, int32_t *before, int32_t *total) {
   const int t = threadIdx.x;
   __shared__ int32_t wsum[kRouteThreads / 64];
   // exclusive prefix of total over the experts: thread t holds expert t
@@ -157,67 +196,86 @@ __device__ void finish(const RouteArgs &A, int chunk, int chunks, int pairs, con
   }
   if (chunk == 0 && t == 0) A.offsets[A.experts] = all;
   // row_ids past the last pair, the chunk's share of them by its own range
-  const int64_t lo = (int64_t)chunk * kChunkTokens * A.top;
+  const int64_t lo = (int64_t)chunk * A.chunk_tokens * A.top;
   for (int64_t p = lo + t; p < lo + pairs; p += kRouteThreads)
     if (p >= all) A.row_ids[p] = -1;
   __syncthreads();
   if (t < 64) place(A, chunk, pairs, ids, before);
 }
 
-template <typename T, int kPer>
-__global__ __launch_bounds__(kRouteThreads) void route_choose_kernel(RouteArgs A, int chunks) {
-  __shared__ int32_t ids[kChunkTokens * kMaxTop];
+template <typename T, int LANES, int kPer>
+__global__ __launch_bounds__(kRouteThreads) void route_choose_kernel(RouteArgs A) {
+  __shared__ int32_t ids[kChunkTokens * kMaxTop];              // read back where this is the only chunk
   __shared__ int32_t count[kMaxExperts], before[kMaxExperts];
   const int chunk = blockIdx.x, t = threadIdx.x;
   for (int e = t; e < A.experts; e += kRouteThreads) count[e] = before[e] = 0;
   __syncthreads();
-  const int t0 = chunk * kChunkTokens, n = min(kChunkTokens, A.tokens - t0);
-  for (int i = t >> 6; i < n; i += kRouteThreads / 64) choose<T, kPer>(A, t0 + i, ids + i * A.top);
+  const int t0 = chunk * A.chunk_tokens, n = min(A.chunk_tokens, A.tokens - t0);
+  for (int i = t / LANES; i < n; i += kRouteThreads / LANES)
+    choose<T, LANES, kPer>(A, t0 + i, ids + (i & (kChunkTokens - 1)) * A.top, count);
   __syncthreads();
-  for (int p = t; p < n * A.top; p += kRouteThreads)
-    if (ids[p] >= 0) atomicAdd(&count[ids[p]], 1);
-  __syncthreads();
-  if (chunks > 1) {
-    for (int e = t; e < A.experts; e += kRouteThreads) A.hist[(int64_t)chunk * A.experts + e] = count[e];
+  if (A.chunks > 1) {
+    const int ep = (A.experts + 1) & ~1;
+    for (int e = t; e < ep; e += kRouteThreads) A.hist[(int64_t)chunk * ep + e] = e < A.experts ? count[e] : 0;
     return;
   }
-  finish(A, chunk, chunks, n * A.top, ids, before, count);
+  finish(A, chunk, n * A.top, ids, before, count);
 }
 
-__global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs A, int chunks) {
-  __shared__ int32_t ids[kChunkTokens * kMaxTop];
+__global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs A) {
   __shared__ int32_t total[kMaxExperts], before[kMaxExperts];
   const int chunk = blockIdx.x, t = threadIdx.x;
-  const int t0 = chunk * kChunkTokens, n = min(kChunkTokens, A.tokens - t0);
+  const int t0 = chunk * A.chunk_tokens, n = min(A.chunk_tokens, A.tokens - t0);
   for (int e = t; e < A.experts; e += kRouteThreads) total[e] = before[e] = 0;
-  for (int p = t; p < n * A.top; p += kRouteThreads) ids[p] = A.ids[(int64_t)t0 * A.top + p];
   __syncthreads();
-  // every thread adds one expert's counts over every `step`-th chunk
-  const int step = kRouteThreads / A.experts;                  // >= 1
-  if (t < step * A.experts) {
-    const int e = t % A.experts;
-    int all = 0, pre = 0;
-    for (int c = t / A.experts; c < chunks; c += step) {
-      const int h = A.hist[(int64_t)c * A.experts + e];
-      all += h;
-      pre += c < chunk ? h : 0;
+  // every thread adds two experts' counts over every `step`-th chunk, eight loads at a time
+  const int half = (A.experts + 1) >> 1, step = kRouteThreads / half;
+  const uint32_t *hist = reinterpret_cast<const uint32_t *>(A.hist);
+  if (t < step * half) {
+    const int e = 2 * (t % half);
+    int all[2] = {0, 0}, pre[2] = {0, 0};
+    for (int c0 = t / half; c0 < A.chunks; c0 += 8 * step) {
+      uint32_t h[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int c = c0 + u * step;
+        h[u] = c < A.chunks ? hist[(int64_t)c * half + (e >> 1)] : 0u;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const uint32_t p = c0 + u * step < chunk ? h[u] : 0u;
+        all[0] += h[u] & 0xFFFFu;
+        all[1] += h[u] >> 16;
+        pre[0] += p & 0xFFFFu;
+        pre[1] += p >> 16;
+      }
     }
-    atomicAdd(&total[e], all);
-    atomicAdd(&before[e], pre);
+    atomicAdd(&total[e], all[0]);
+    atomicAdd(&before[e], pre[0]);
+    if (e + 1 < A.experts) {
+      atomicAdd(&total[e + 1], all[1]);
+      atomicAdd(&before[e + 1], pre[1]);
+    }
   }
   __syncthreads();
-  finish(A, chunk, chunks, n * A.top, ids, before, total);
+  finish(A, chunk, n * A.top, A.ids + (int64_t)t0 * A.top, before, total);
+}
+
+// Tokens of a chunk: at most kMaxChunks chunks, and counts that fit 16 bits.
+int chunk_tokens(int tokens) {
+  int c = kChunkTokens;
+  while ((int64_t)c * kMaxChunks < tokens && c < 32768) c *= 2;
+  return c;
 }
 
 template <typename T>
-hipError_t route_t(const RouteArgs &A, hipStream_t s) {
-  const int chunks = (A.tokens + kChunkTokens - 1) / kChunkTokens;
-  if (A.experts <= 64) route_choose_kernel<T, 1><<<chunks, kRouteThreads, 0, s>>>(A, chunks);
-  else if (A.experts <= 256) route_choose_kernel<T, 4><<<chunks, kRouteThreads, 0, s>>>(A, chunks);
-  else route_choose_kernel<T, 16><<<chunks, kRouteThreads, 0, s>>>(A, chunks);
+hipError_t route_t(RouteArgs A, hipStream_t s) {
+  if (A.experts <= 64) route_choose_kernel<T, 16, 4><<<A.chunks, kRouteThreads, 0, s>>>(A);
+  else if (A.experts <= 256) route_choose_kernel<T, 16, 16><<<A.chunks, kRouteThreads, 0, s>>>(A);
+  else route_choose_kernel<T, 64, 16><<<A.chunks, kRouteThreads, 0, s>>>(A);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || chunks == 1) return e;
-  route_place_kernel<<<chunks, kRouteThreads, 0, s>>>(A, chunks);
+  if (e != hipSuccess || A.chunks == 1) return e;
+  route_place_kernel<<<A.chunks, kRouteThreads, 0, s>>>(A);
   return hipGetLastError();
 }
 
@@ -266,15 +324,16 @@ hipError_t combine_t(const T *y, int64_t rows, int d, const int32_t *slots, cons
 bool moe_route_supported(int experts, int top) { return experts <= kMaxExperts && top <= kMaxTop; }
 
 int64_t moe_route_scratch(int tokens, int experts) {
-  const int64_t chunks = ((int64_t)tokens + kChunkTokens - 1) / kChunkTokens;
-  return chunks > 1 ? chunks * experts * 4 : 0;
+  const int64_t c = chunk_tokens(tokens), chunks = (tokens + c - 1) / c;
+  return chunks > 1 ? chunks * ((experts + 1) & ~1) * 2 : 0;
 }
 
 hipError_t launch_moe_route(const void *logits, int dtype, int tokens, int experts, int64_t stride, int top,
                             bool renorm, int32_t *ids, float *weights, int32_t *offsets, int32_t *row_ids,
                             int32_t *slots, void *scratch, hipStream_t s) {
+  const int c = chunk_tokens(tokens);
   const RouteArgs A{logits, stride, tokens, experts, top, renorm ? 1 : 0, ids, weights, offsets, row_ids, slots,
-                    (int32_t *)scratch};
+                    (uint16_t *)scratch, c, (int)(((int64_t)tokens + c - 1) / c)};
   if (dtype == BQM_F32) return route_t<float>(A, s);
   if (dtype == BQM_BF16) return route_t<__bf16>(A, s);
   return route_t<_Float16>(A, s);
