@@ -514,8 +514,7 @@ int fp8_quant(const void *x, int dtype, int m, int k, int64_t x_stride, int swig
               bqm_stream_t stream) {
   if (!x || !q || !scale || m < 1 || k < 1 || !known_dtype(dtype)) return BQM_EINVAL;
   if (m > 1 && x_stride < (int64_t)k * (swiglu ? 2 : 1)) return BQM_EINVAL;
-  // one launch's workgroups: 16 tokens and a block each
-  if (k > kMaxFp8Cols || ((int64_t)m + 15) / 16 * (((int64_t)k + 127) / 128) >= (int64_t)1 << 31) return BQM_ENOTSUP;
+  if (k > kMaxFp8Cols) return BQM_ENOTSUP;
   if (!aligned16(q) || ((uintptr_t)scale & 3u) || ((uintptr_t)x & (unsigned)(elem_size(dtype) - 1))) return BQM_EALIGN;
   int cus;
   const int rc = current_device(&cus);

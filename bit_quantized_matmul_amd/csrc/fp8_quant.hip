@@ -20,19 +20,33 @@ namespace {
 constexpr int kBlk = 128;
 constexpr float kE4M3Max = 448.0f;
 
-// max over 16 consecutive lanes; NaN if any is NaN
-__device__ __forceinline__ float max16_nan(float a) {
+// |v| as an integer: ordered as the values are, infinities and NaN above all others,
+// so an integer maximum finds a block's largest value and whether it is finite.
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_row_ror(uint32_t a) {
+  const uint32_t b = (uint32_t)__builtin_amdgcn_update_dpp((int)a, (int)a, CTRL, 0xF, 0xF, false);
+  return a > b ? a : b;
+}
+
+// max over 16 consecutive lanes
+__device__ __forceinline__ uint32_t max16(uint32_t a) {
+  return max_row_ror<0x128>(max_row_ror<0x124>(max_row_ror<0x122>(max_row_ror<0x121>(a))));
+}
+
+__device__ __forceinline__ uint32_t magnitude8(const float (&v)[8], uint32_t a) {
 #pragma unroll
-  for (int o = 8; o >= 1; o >>= 1) {
-    const float b = __shfl_xor(a, o, 16);
-    a = (a > b || a != a) ? a : b;
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t b = magnitude(v[j]);
+    a = a > b ? a : b;
   }
   return a;
 }
 
-__device__ __forceinline__ float block_scale(float a) {
-  if (!(a <= 3.4028234663852886e38f)) return __builtin_nanf("");
-  return a > 0.0f ? fmaxf(__fdiv_rn(a, kE4M3Max), 1.17549435e-38f) : 1.0f;
+__device__ __forceinline__ float block_scale(uint32_t a) {
+  if (a >= 0x7F800000u) return __builtin_nanf("");
+  return a ? fmaxf(__fdiv_rn(__uint_as_float(a), kE4M3Max), 0x1p-126f) : 1.0f;
 }
 
 // The codes of 8 values of a block with scale s.  RN(v / s) without a division an
@@ -40,16 +54,15 @@ __device__ __forceinline__ float block_scale(float a) {
 // rounded quotient (Markstein), as long as the remainder v - q s is no subnormal; tiny
 // scales divide.
 __device__ __forceinline__ u32x2_t codes8(const float (&v)[8], float s) {
-  if (s != s) return u32x2_t{0x7F7F7F7Fu, 0x7F7F7F7Fu};
-  const bool tiny = s < 0x1p-60f;
-  const float y = __fdiv_rn(1.0f, s);
   float c[8];
+  const float y = __fdiv_rn(1.0f, s);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float q = v[j] * y;
     c[j] = fmaf(fmaf(-q, s, v[j]), y, q);
   }
-  if (tiny) {
+  if (!(s >= 0x1p-60f)) {
+    if (s != s) return u32x2_t{0x7F7F7F7Fu, 0x7F7F7F7Fu};
 #pragma unroll
     for (int j = 0; j < 8; ++j) c[j] = __fdiv_rn(v[j], s);
   }
@@ -57,7 +70,7 @@ __device__ __forceinline__ u32x2_t codes8(const float (&v)[8], float s) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) c[j] = __builtin_amdgcn_fmed3f(c[j], -kE4M3Max, kE4M3Max);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) p[h] = e4m3_pair(c[4 * h], c[4 * h + 1]) | e4m3_pair(c[4 * h + 2], c[4 * h + 3]) << 16;
+  for (int h = 0; h < 2; ++h) p[h] = e4m3_quad(c[4 * h], c[4 * h + 1], c[4 * h + 2], c[4 * h + 3]);
   return p;
 }
 
@@ -72,55 +85,55 @@ __device__ __forceinline__ void load8(const T *row, int c, int k, float (&v)[8])
   }
 }
 
-// g / d for d = 1 + exp(-g): the reciprocal refined once, then the quotient, within
-// 0.51 units; past 2^100 (g < -69) and for NaN the plain division.
-__device__ __forceinline__ float silu_mul(float g, float u) {
-  const float d = 1.0f + expf(-g);
-  float r = __builtin_amdgcn_rcpf(d);
-  r = fmaf(fmaf(-d, r, 1.0f), r, r);
-  float q = g * r;
-  q = fmaf(fmaf(-q, d, g), r, q);
-  if (!(d < 0x1p100f) || !(fabsf(g) < 0x1p100f)) q = g / d;
-  return q * u;
-}
-
-// 16 lanes hold a block; a workgroup of 256 takes `rows` tokens x 16 / rows blocks.
-template <typename T, bool kVec, bool kSwiglu>
-__global__ __launch_bounds__(256) void fp8_quant_kernel(const T *__restrict__ x, int m, int k, int64_t stride,
-                                                        int rows, uint8_t *__restrict__ q,
-                                                        float *__restrict__ scale) {
-  const int kb = (k + kBlk - 1) / kBlk;
-  const int grp = threadIdx.x >> 4, sub = threadIdx.x & 15;
-  // neighbouring workgroups take neighbouring blocks of the same rows: rows are often
-  // a multiple of 8 KiB apart, and one column of many of them lies in few memory channels
-  // (2048 x 14336 with SwiGLU 47 us with neighbouring rows)
-  const int per = 16 / rows, across = (kb + per - 1) / per;
-  const int row = (int)(blockIdx.x / across) * rows + grp % rows;
-  const int b = (int)(blockIdx.x % across) * per + grp / rows;
-  if (row >= m || b >= kb) return;                 // whole 16-lane groups leave together
-  const T *xr = x + (int64_t)row * stride;
-  const int c = b * kBlk + sub * 8;
-  float v[8];
-  load8<T, kVec>(xr, c, k, v);
-  if constexpr (kSwiglu) {
-    float u[8];
-    if (kVec) {
-      load8<T, kVec>(xr + k, c, k, u);
-    } else {
-      load8<T, false>(xr + k, c, k, u);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = silu_mul(v[j], u[j]);
-  }
-  float a = 0.0f;
+// silu(g) u = g / (1 + exp(-g)) u.  exp(-g) = 2^p with p = -g log2(e) in two parts, the
+// rounded product and what it lost; the quotient is one step from g times the
+// approximate reciprocal.  Each of the three is within about a unit.  Where 1 + exp(-g)
+// nears the end of the range (g < -69) and for infinities and NaN: library calls.
+__device__ __forceinline__ void silu_mul8(float (&g)[8], const float (&u)[8]) {
+  constexpr float kL = 0x1.715476p+0f, kLlo = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;   // log2(e) = kL + kLlo
+  float q[8], far = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float w = fabsf(v[j]);
-    a = (a > w || a != a) ? a : w;
+    const float p = -g[j] * kL;
+    const float lost = fmaf(-g[j], kLlo, fmaf(-g[j], kL, -p));
+    const float d = 1.0f + __builtin_amdgcn_exp2f(p) * fmaf(lost, kLn2, 1.0f);
+    const float r = __builtin_amdgcn_rcpf(d);
+    const float a = g[j] * r;
+    q[j] = fmaf(fmaf(-a, d, g[j]), r, a);
+    far = fmaxf(far, fabsf(g[j]));
+    if (g[j] != g[j]) far = INFINITY;
   }
-  const float s = block_scale(max16_nan(a));
-  *reinterpret_cast<u32x2_t *>(q + ((int64_t)row * kb + b) * kBlk + sub * 8) = codes8(v, s);
-  if (sub == 0) scale[(int64_t)b * m + row] = s;
+  if (!(far < 69.0f)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = g[j] / (1.0f + expf(-g[j]));
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) g[j] = q[j] * u[j];
+}
+
+// 16 lanes hold a block; a workgroup of 256 takes kRows tokens x 16 / kRows blocks.
+// Neighbouring workgroups take neighbouring blocks of the same rows.
+template <typename T, bool kVec, bool kSwiglu, int kRows>
+__global__ __launch_bounds__(256) void fp8_quant_kernel(const T *__restrict__ x, int m, int k, int64_t stride,
+                                                        uint8_t *__restrict__ q, float *__restrict__ scale) {
+  const int kb = (k + kBlk - 1) / kBlk;
+  const int grp = threadIdx.x >> 4, sub = threadIdx.x & 15;
+  const int b = (int)blockIdx.x * (16 / kRows) + grp / kRows;
+  const int c = b * kBlk + sub * 8;
+  if (b >= kb) return;                               // whole 16-lane groups leave together
+  for (int64_t row = (int64_t)blockIdx.y * kRows + grp % kRows; row < m; row += (int64_t)gridDim.y * kRows) {
+    const T *xr = x + row * stride;
+    float v[8];
+    load8<T, kVec>(xr, c, k, v);
+    if constexpr (kSwiglu) {
+      float u[8];
+      load8<T, kVec>(xr + k, c, k, u);
+      silu_mul8(v, u);
+    }
+    const float s = block_scale(max16(magnitude8(v, 0)));
+    *reinterpret_cast<u32x2_t *>(q + (row * kb + b) * kBlk + sub * 8) = codes8(v, s);
+    if (sub == 0) scale[(int64_t)b * m + row] = s;
+  }
 }
 
 // One workgroup of 256 per 128 x 128 block: 16 lanes a row, 8 rows each.
@@ -134,24 +147,21 @@ __global__ __launch_bounds__(256) void fp8_pack_kernel(const T *__restrict__ w, 
   const T *we = w + e * rows * (int64_t)cols;
   const int c = b * kBlk + sub * 8;
   float v[8][8];
-  float a = 0.0f;
+  uint32_t a = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = rb * kBlk + i * 16 + grp;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 8; ++j)
       v[i][j] = r < rows && c + j < cols ? to_f32(we[(int64_t)r * cols + c + j]) : 0.0f;
-      const float x = fabsf(v[i][j]);
-      a = (a > x || a != a) ? a : x;
-    }
+    a = magnitude8(v[i], a);
   }
-  a = max16_nan(a);
-  __shared__ float red[16];
+  a = max16(a);
+  __shared__ uint32_t red[16];
   if (sub == 0) red[grp] = a;
   __syncthreads();
-  a = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) a = (a > red[i] || a != a) ? a : red[i];
+  for (int i = 0; i < 16; ++i) a = a > red[i] ? a : red[i];
   const float s = block_scale(a);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -162,22 +172,29 @@ __global__ __launch_bounds__(256) void fp8_pack_kernel(const T *__restrict__ w, 
   if (threadIdx.x == 0) scale[(e * nb + rb) * kb + b] = s;
 }
 
-template <typename T>
-hipError_t quant_t(const T *x, int m, int k, int64_t stride, bool swiglu, uint8_t *q, float *scale, hipStream_t s) {
+template <typename T, int kRows>
+hipError_t quant_rows(const T *x, int m, int k, int64_t stride, bool swiglu, uint8_t *q, float *scale, hipStream_t s) {
   const int kb = (k + kBlk - 1) / kBlk;
-  const int rows = m >= 16 ? 16 : 1;
-  const unsigned grid = (unsigned)((m + rows - 1) / rows) * (unsigned)((kb + 16 / rows - 1) / (16 / rows));
+  const int64_t tiles = ((int64_t)m + kRows - 1) / kRows;
+  const dim3 grid((kb + 16 / kRows - 1) / (16 / kRows), (unsigned)(tiles < 65535 ? tiles : 65535));
   // 16-byte loads where every row (and, with SwiGLU, its second half) starts on 16 bytes
   const int per = 16 / (int)sizeof(T);
   const bool vec = ((uintptr_t)x & 15u) == 0 && (m == 1 || stride % per == 0) && (!swiglu || k % per == 0);
   if (swiglu) {
-    if (vec) fp8_quant_kernel<T, true, true><<<grid, 256, 0, s>>>(x, m, k, stride, rows, q, scale);
-    else fp8_quant_kernel<T, false, true><<<grid, 256, 0, s>>>(x, m, k, stride, rows, q, scale);
+    if (vec) fp8_quant_kernel<T, true, true, kRows><<<grid, 256, 0, s>>>(x, m, k, stride, q, scale);
+    else fp8_quant_kernel<T, false, true, kRows><<<grid, 256, 0, s>>>(x, m, k, stride, q, scale);
   } else {
-    if (vec) fp8_quant_kernel<T, true, false><<<grid, 256, 0, s>>>(x, m, k, stride, rows, q, scale);
-    else fp8_quant_kernel<T, false, false><<<grid, 256, 0, s>>>(x, m, k, stride, rows, q, scale);
+    if (vec) fp8_quant_kernel<T, true, false, kRows><<<grid, 256, 0, s>>>(x, m, k, stride, q, scale);
+    else fp8_quant_kernel<T, false, false, kRows><<<grid, 256, 0, s>>>(x, m, k, stride, q, scale);
   }
   return hipGetLastError();
+}
+
+// 16 tokens a workgroup, so that it stores 16 neighbouring scales; few tokens: 16 blocks of one.
+template <typename T>
+hipError_t quant_t(const T *x, int m, int k, int64_t stride, bool swiglu, uint8_t *q, float *scale, hipStream_t s) {
+  return m >= 16 ? quant_rows<T, 16>(x, m, k, stride, swiglu, q, scale, s)
+                 : quant_rows<T, 1>(x, m, k, stride, swiglu, q, scale, s);
 }
 
 template <typename T>

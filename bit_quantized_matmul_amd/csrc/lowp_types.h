@@ -40,10 +40,10 @@ __device__ __forceinline__ void load_vec(const T *p, float (&v)[N]) {
   }
 }
 
-// Two E4M3 codes of a and b (half to even) in the low 16 bits; |a|, |b| <= 448
-// or NaN (whose code is 0x7F or 0xFF).
-__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false) & 0xFFFFu;
+// The E4M3 codes of four values (half to even), |value| <= 448.
+__device__ __forceinline__ uint32_t e4m3_quad(float a, float b, float c, float d) {
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true);
 }
 
 }  // namespace bqm

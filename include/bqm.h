@@ -394,8 +394,7 @@ enum { BQM_F32 = 0, BQM_BF16 = 1, BQM_F16 = 2 };
  * A block that holds a NaN or an infinity gets a NaN scale and NaN codes.
  * q [device] uint8 [m, 128 kb], 16-byte aligned; scale [device] fp32 [kb, m].
  * x needs its element's alignment only (16-byte aligned rows are read faster).
- * BQM_EINVAL for x_stride below the row's length; BQM_ENOTSUP for k > 2^22 or
- * ceil(m / 16) kb >= 2^31. */
+ * BQM_EINVAL for x_stride below the row's length; k <= 2^22. */
 int fp8_quant(const void *x, int dtype, int m, int k, int64_t x_stride, int swiglu, uint8_t *q, float *scale,
               bqm_stream_t stream);
 
