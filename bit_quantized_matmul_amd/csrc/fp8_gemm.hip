@@ -175,8 +175,8 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Args A, Y *__res
       const int b = b0 + d * NW;
       if (b < A.kb) {
         const uint8_t *p = w + (int64_t)b * kBlk;
-        wl[d][0] = __builtin_nontemporal_load(reinterpret_cast<const i32x4 *>(p));
-        wl[d][1] = __builtin_nontemporal_load(reinterpret_cast<const i32x4 *>(p + 64));
+        wl[d][0] = *reinterpret_cast<const i32x4 *>(p);
+        wl[d][1] = *reinterpret_cast<const i32x4 *>(p + 64);
       }
     }
   };
@@ -274,22 +274,24 @@ __device__ __forceinline__ void stage_scales(const float *base, uint32_t off, ui
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc_of(base), (lds_void *)to, 4, off, 0, 0, 0);
 }
 
-// The wave's own loads to LDS have landed and its reads are done, then so are everyone's.
+// All but the wave's last N loads to LDS have landed and its reads are done, then so
+// are everyone's.
+template <int N>
 __device__ __forceinline__ void wait_and_meet() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-template <typename Y, int BM, int BN, int WM, int WN>
+template <typename Y, int BM, int BN, int WM, int WN, int NS>
 __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args A, Y *__restrict__ y) {
   constexpr int NW = WM * WN;
   constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
   constexpr int kRowsPerLoad = NW * 8;
-  constexpr int LM = BM / kRowsPerLoad, LN = BN / kRowsPerLoad;
+  constexpr int LM = BM / kRowsPerLoad, LN = BN / kRowsPerLoad, kLoads = LM + LN + 1;
   static_assert(BM % kRowsPerLoad == 0 && BN % kRowsPerLoad == 0, "whole loads");
   static_assert(BN <= kBlk && kBlk % BN == 0 && BM % 64 == 0 && BM / 64 < NW, "one scale block of weights a tile");
   constexpr int kScale = (BM + BN) * kBlk;                      // scales behind the codes
   constexpr int kStage = kScale + (BM + 64) * 4;
-  __shared__ __align__(1024) uint8_t lds[2 * kStage];
+  __shared__ __align__(1024) uint8_t lds[NS * kStage];
 
   Tile t;
   if (!find_tile<BM, BN>(A, blockIdx.x, &t)) return;
@@ -330,18 +332,26 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args A, Y 
   };
 
   f32x16 acc[TN][TM] = {};
-  load_stage(0, 0);
+#pragma unroll
+  for (int i = 0; i < NS - 1; ++i)
+    if (i < A.kb) load_stage(i * kStage, i);
   const int sz = (row >> 1) & 7;
   int coff[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) coff[j] = row * kBlk + (((2 * j + half) ^ sz) << 4);
-  int at = 0;
+  const bool any_row = wm * TM * 32 <= pmax;
+  int at = 0, to = (NS - 1) * kStage;
   for (int b = 0; b < A.kb; ++b) {
-    wait_and_meet();
-    if (b + 1 < A.kb) load_stage(kStage - at, b + 1);
-    const uint8_t *lq = lds + at + wm * TM * 32 * kBlk;
-    const uint8_t *lw = lds + at + BM * kBlk + wn * TN * 32 * kBlk;
-    const float *ls = reinterpret_cast<const float *>(lds + at + kScale);
+    if (b + NS - 2 < A.kb) wait_and_meet<(NS - 2) * kLoads>();
+    else wait_and_meet<0>();
+    if (b + NS - 1 < A.kb) load_stage(to, b + NS - 1);
+    const int here = at;
+    at = at + kStage < NS * kStage ? at + kStage : 0;
+    to = to + kStage < NS * kStage ? to + kStage : 0;
+    if (!any_row) continue;                                    // only loads and meets
+    const uint8_t *lq = lds + here + wm * TM * 32 * kBlk;
+    const uint8_t *lw = lds + here + BM * kBlk + wn * TN * 32 * kBlk;
+    const float *ls = reinterpret_cast<const float *>(lds + here + kScale);
     i32x4 rq[TM][4], rw[TN][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -382,7 +392,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args A, Y 
             acc[(c - 1) / TM][(c - 1) % TM][i] = fmaf(part[(c - 1) & 1][i], s[(c - 1) % TM], acc[(c - 1) / TM][(c - 1) % TM][i]);
       }
     }
-    at = kStage - at;
   }
 #pragma unroll
   for (int f = 0; f < TM; ++f) {
@@ -414,23 +423,45 @@ hipError_t stream(const Fp8Args &A, Y *y, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename Y, int BM, int BN, int WM, int WN>
+template <typename Y, int BM, int BN, int WM, int WN, int NS>
 hipError_t tile(const Fp8Args &A, Y *y, hipStream_t s) {
-  fp8_tile_kernel<Y, BM, BN, WM, WN><<<(unsigned)tiles(A, BM, BN), 64 * WM * WN, 0, s>>>(A, y);
+  fp8_tile_kernel<Y, BM, BN, WM, WN, NS><<<(unsigned)tiles(A, BM, BN), 64 * WM * WN, 0, s>>>(A, y);
   return hipGetLastError();
+}
+
+// One fragment of tokens.  8 waves a workgroup, 4 where the rows are short and there are
+// workgroups enough (us with 4 / 8 waves, one token: 4096x4096 8.2 / 6.3, 14336x4096 16.2 /
+// 16.0, 4096x14336 24.3 / 17.3, 8 of 64 matrices of 2048x2048 11.8 / 13.4, 1092x312 2.6 / 2.7)
+template <typename Y>
+hipError_t stream1(const Fp8Args &A, Y *y, int num_cus, hipStream_t s) {
+  const bool four = A.kb <= 4 || (A.kb <= 16 && tiles(A, 16, 16) > 2 * num_cus);
+  return four ? stream<Y, 1, 4, 2>(A, y, s) : stream<Y, 1, 8, 2>(A, y, s);
 }
 
 template <typename Y>
 hipError_t run(const Fp8Args &A, Y *y, int num_cus, hipStream_t s) {
   // rows a matrix has to multiply: exact for one matrix, the mean for experts
   const int per = A.offsets ? (A.slots + A.experts - 1) / A.experts : A.m;
-  // 8 waves a workgroup (one token, us with 4 / 8 / 16 waves: 4096x4096 7.9 / 6.2 / 6.0,
-  // 14336x4096 16.4 / 15.7 / 18.7, 4096x14336 23.7 / 15.9 / 17.8), 4 for short rows
-  // (1092x312 2.6 / 2.7 / 3.0)
-  if (per <= 16) return A.kb > 4 ? stream<Y, 1, 8, 2>(A, y, s) : stream<Y, 1, 4, 2>(A, y, s);
-  if (per <= 32) return A.kb > 4 ? stream<Y, 2, 8, 2>(A, y, s) : stream<Y, 2, 4, 2>(A, y, s);
-  if (tiles(A, 128, 128) >= num_cus) return tile<Y, 128, 128, 2, 2>(A, y, s);
-  return tile<Y, 64, 64, 2, 2>(A, y, s);
+  // few tiles: the smallest token tile that leaves none of them waiting for a CU (us at 64
+  // tokens: 1024x4096 6.8 with 16 a tile, 4096x4096 12.5 with 64; 64 x 64 tiles 18.0, 19.8)
+  if (tiles(A, 16, 16) <= num_cus) return stream1(A, y, num_cus, s);
+  if (tiles(A, 32, 16) <= num_cus) return stream<Y, 2, 8, 1>(A, y, s);
+  if (tiles(A, 64, 16) <= num_cus) return stream<Y, 4, 8, 1>(A, y, s);
+  // many: 128 x 128 tiles, two workgroups a CU (us at 512 tokens, 14336x4096: 66, with 64 x 128
+  // tiles 77; 64 matrices of 2048x2048 with 128 rows each: 114 against 118, with 64: 87
+  // against 82)
+  if (per >= 96 && tiles(A, 128, 128) >= num_cus) return tile<Y, 128, 128, 2, 2, 2>(A, y, s);
+  // experts' matrices, and more than 8 tokens of one: 64 x 128 tiles (us, 64 matrices of
+  // 2048x2048 with 1 / 8 / 32 rows each: 45 / 55 / 64, reading 16 rows a workgroup 49 / 73 /
+  // 153; one matrix of 32768x4096, 1 token 37 against 30, 16 tokens 36 against 39)
+  if ((A.offsets || per > 8) && tiles(A, 64, 128) >= num_cus) return tile<Y, 64, 128, 2, 2, 3>(A, y, s);
+  if (per <= 16) return stream1(A, y, num_cus, s);
+  // up to 32 tokens reading the weights once counts, until 64 x 64 tiles fill the CUs (us at
+  // 32: 4096x14336 16.6 against 59, 14336x4096 25.8 against 20.2)
+  if (per <= 32 && tiles(A, 64, 64) < num_cus * 3 / 4) return stream<Y, 2, 8, 1>(A, y, s);
+  // 64 x 64 tiles, four blocks deep (us at 256 tokens, 4096x4096: 19.0, two deep 25, 64 x 128
+  // tiles 24)
+  return tile<Y, 64, 64, 2, 2, 4>(A, y, s);
 }
 
 hipError_t run_any(const Fp8Args &A, void *y, int ydtype, int num_cus, hipStream_t s) {

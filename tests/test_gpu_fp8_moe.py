@@ -169,6 +169,22 @@ def test_gemm(m, n, k):
     check_product(y, ref, mag, k, torch.float32, "y given")
 
 
+# one size for each kernel that the sizes choose between, with rows shorter and longer than its pipeline
+ROUTES = [(3, 5000, 200), (16, 4800, 2300), (30, 4000, 700), (32, 6001, 128), (50, 4096, 300), (64, 4000, 2176),
+          (65, 5000, 640), (70, 5001, 100), (129, 4000, 384), (130, 9000, 256), (300, 8000, 130), (200, 12000, 520),
+          (1100, 4002, 200), (1025, 4000, 96), (1000, 4224, 1100)]
+
+
+@pytest.mark.parametrize("m,n,k", ROUTES)
+def test_gemm_routes(m, n, k):
+    rng = np.random.default_rng(m + n + k)
+    q, qs, w, ws = operands(rng, m, n, k)
+    ref, mag = of8.gemm(w, ws, q, qs)
+    for dtype in (torch.float32, torch.bfloat16):
+        y = B.fp8_gemm(dev(w, F8), dev(ws), k, dev(q, F8), dev(qs), dtype=dtype)
+        check_product(y, ref, mag, k, dtype, f"{m}x{n}x{k} {dtype}")
+
+
 @pytest.mark.parametrize("m,n,k", [(1, 100, 384), (20, 100, 384), (90, 200, 384), (300, 300, 384)])
 def test_gemm_scales_of_any_size_and_nan(m, n, k):
     """Scales from 2^-100 to 2^60, negative and zero ones; a NaN token poisons its row alone."""
@@ -194,6 +210,9 @@ GROUPED = [  # sizes of the experts' groups, n, k
     ([0, 300, 7, 130, 0, 65], 257, 384),
     ([16] * 20, 128, 129),
     ([2, 0, 513], 128, 256),
+    ([1, 0, 2, 33, 65, 5] * 12, 520, 300),              # 72 experts, 64 x 128 tiles
+    ([130, 0, 290, 257, 1, 128], 6000, 200),            # 128 x 128 tiles, whole and ragged
+    ([3] * 70, 300, 513),
 ]
 
 
