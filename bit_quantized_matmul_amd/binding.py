@@ -8,6 +8,7 @@ exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -565,7 +566,7 @@ def _current():
 def _operand(t, dtype, shape, device, name):
     """The address of a contiguous `dtype` tensor of `shape` on the current device."""
     try:
-        if t.get_device() == device and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+        if t.get_device() == device and t.dtype is dtype and t.shape == shape and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
@@ -598,7 +599,7 @@ def _row_strided(t, device, name):
 def _result(y, dtype, shape, device, name="y"):
     """y, or a new tensor, as (tensor, address)."""
     if y is None:
-        y = _torch().empty(shape, dtype=dtype, device=device)
+        y = _torch().empty(*shape, dtype=dtype, device=device)
         return y, y.data_ptr()
     return y, _operand(y, dtype, shape, device, name)
 
@@ -663,13 +664,13 @@ def _result_type(y, dtype):
 
 def _product_shapes(w, cols, q, lead):
     """rows, m and the padded columns of a product, from its operands' shapes."""
-    if cols < 1:
-        raise ValueError(f"cols must be at least 1, got {cols}")
     kp = (cols + 127) // 128 * 128
     ws, qs = getattr(w, "shape", ()), getattr(q, "shape", ())
-    if len(ws) != lead + 2 or ws[-1] != kp or min(ws) < 1:
-        raise ValueError(f"w must have shape [{'experts, ' * lead}rows, {kp}], got {tuple(ws)}")
-    if len(qs) != 2 or qs[1] != kp or qs[0] < 1:
+    if kp < 1 or len(ws) != lead + 2 or ws[-1] != kp or 0 in ws or len(qs) != 2 or qs[1] != kp or qs[0] < 1:
+        if cols < 1:
+            raise ValueError(f"cols must be at least 1, got {cols}")
+        if len(ws) != lead + 2 or ws[-1] != kp or 0 in ws:
+            raise ValueError(f"w must have shape [{'experts, ' * lead}rows, {kp}], got {tuple(ws)}")
         _rows2d(q, kp, "q")
     return ws[-2], qs[0], kp
 
@@ -680,10 +681,9 @@ def fp8_gemm(w, w_scale, cols: int, q, q_scale, dtype=None, y=None):
     torch = _torch()
     f8, f32 = torch.float8_e4m3fn, torch.float32
     rows, m, kp = _product_shapes(w, cols, q, 0)
-    kb = kp // FP8_BLOCK
+    kb, nb = kp // 128, (rows + 127) // 128
     ydtype = _result_type(y, dtype)
     ycode = _dtype_code(ydtype, "y")
-    nb = (rows + 127) // 128
     if not q.is_cuda:
         _shape(w_scale, (nb, kb), "w_scale")
         _shape(q_scale, (kb, m), "q_scale")
@@ -740,6 +740,7 @@ class MoeRoute(NamedTuple):
     slots: object      # int32 [tokens, top]: where each pair went, -1 for none
 
 
+@functools.lru_cache(maxsize=256)
 def moe_route_workspace(tokens: int, experts: int, top: int) -> int:
     """Bytes of device workspace moe_route needs."""
     n = ctypes.c_int64()
@@ -758,14 +759,14 @@ def moe_route(logits, top: int, renorm: bool = True, workspace=None) -> MoeRoute
     lp, code, stride, tokens, experts = _row_strided(logits, dev, "logits")
     need = moe_route_workspace(tokens, experts, top)
     if workspace is None and need:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     wp = None
     if workspace is not None:
         _at_least(workspace, need, "workspace")
         wp = _operand(workspace, torch.uint8, workspace.shape, dev, "workspace")
     pairs = tokens * top
     # one buffer: ids, slots, row_ids, weights, offsets
-    base = torch.empty((4 * pairs + experts + 1,), dtype=torch.int32, device=dev)
+    base = torch.empty(4 * pairs + experts + 1, dtype=torch.int32, device=dev)
     p = base.data_ptr()
     rc = (_lib or load_library()).moe_route(
         lp, code, tokens, experts, stride, top, bool(renorm), p, p + 12 * pairs, p + 16 * pairs, p + 8 * pairs,
