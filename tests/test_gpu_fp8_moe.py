@@ -376,3 +376,19 @@ def test_grouped_weights_past_32_bits():
     off = torch.tensor([0, 0, 0, 0, 1, 2], dtype=torch.int32, device=DEV)
     y = host(B.fp8_gemm_grouped(w.view(F8), ws, k, q, qs, off, dtype=torch.float32))
     assert np.all(y[0] == 0) and y[1, 0] == 2 and np.all(y[1, -3:] == 5) and np.all(y[1, 1:-3] == 0)
+
+
+@pytest.mark.parametrize("tokens", [1, 37])
+def test_example_layer(tokens):
+    """The example's layer against fp32: three roundings to E4M3 (activations, weights, the inner
+    activations; at most 2^-4 each, uniform over a step: about 2^-4 / sqrt(3) in the mean)
+    and the two products' two operands each: sqrt(4) x 0.036 = 0.072 at the most."""
+    import importlib.util
+    import os
+
+    from tests.conftest import ROOT
+    spec = importlib.util.spec_from_file_location("fp8_moe_ffn", os.path.join(ROOT, "examples", "fp8_moe_ffn.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    rel, us = example.run(tokens, 256, 192, 8, 2, replays=3)
+    assert rel < 0.072 and us > 0
