@@ -4,12 +4,21 @@
 //   y[t, r] = sum_b sx[b, t] * sw[r / 128, b] * sum_{j < 128} q[t, 128 b + j] * w[r, 128 b + j]
 //
 // The blocks' sums are scaled and added in fp32 and y is rounded once.  A block's own
-// sum is exact to fp32: the codes become fp16 in registers (E4M3 is exact there, two
-// codes an instruction) and the fp16 matrix instructions sum their products in fp32.
-// The 8-bit instructions are faster (a 4096 x 14336 x 4096 product 269 against 418 us) but
-// keep, of each 8 products, only the 13 bits below the largest one: measured, 4e-5
-// of the result's norm where a few columns are 30 times the others, which is how
-// activations are.  fp32 sums are 100 times nearer, so they are not used.
+// sum is formed in one of two ways:
+//
+//  * with fp32's precision: the codes become fp16 in registers (E4M3 is exact there, two
+//    codes an instruction) and the fp16 matrix instructions sum their products in fp32.
+//    Every result in fp32, every row of fewer than 32 blocks, every small product.
+//  * by the 8-bit matrix instructions, at twice the rate and without conversions
+//    (4096 x 14336 x 4096: 268 against 437 us).  They keep, of each 8 products, only the 13
+//    bits below the largest one: measured, 4e-5 of the result's norm where a few
+//    columns are 30 times the others, which is how activations are, and 2e-5 without.
+//    A result in 16 bits is rounded by 2^-9 (bf16) or 2^-12 (fp16) of itself, but one
+//    that nearly cancels shows the difference; it averages out over the blocks,
+//    and from 32 on the largest error is 1.1 to 1.3 times 2^-16 of the sum of the terms'
+//    magnitudes, the bound that fp32 sums of a block have (8 blocks: 3.3 times,
+//    112 blocks: 0.4 times).  So large products with 16-bit results take this from 32
+//    blocks on.
 //
 // The weights are the instruction's A operand, the tokens its B operand, so a lane's
 // results are groups of four neighbouring rows of one token: one scale a lane and
@@ -37,6 +46,7 @@ struct Fp8Args {
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // Eight codes as fp16.
 __device__ __forceinline__ f16x8 widen(int lo, int hi) {
@@ -281,7 +291,7 @@ __device__ __forceinline__ void wait_and_meet() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-template <typename Y, int BM, int BN, int WM, int WN, int NS>
+template <typename Y, int BM, int BN, int WM, int WN, int NS, bool kNative>
 __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args A, Y *__restrict__ y) {
   constexpr int NW = WM * WN;
   constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
@@ -367,10 +377,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args A, Y 
 #pragma unroll
     for (int f = 0; f < TM; ++f) s[f] = ls[(wm * TM + f) * 32 + row] * sw;
     // Chain c multiplies row fragment c / TM and token fragment c % TM, 8 steps of 16
-    // columns; between its steps the codes it is the first to use are widened and the sums
-    // of chain c - 1 scaled and added.
+    // columns (2 of 64 with the 8-bit instruction); between its steps the codes it is the
+    // first to use are widened and the sums of chain c - 1 scaled and added.
     f16x8 qh[TM][8], wh[8];
     f32x16 part[2];
+    auto quarter = [](const i32x4 (&r)[4], int k) {
+      return __builtin_shufflevector(r[2 * k], r[2 * k + 1], 0, 1, 2, 3, 4, 5, 6, 7);
+    };
 #pragma unroll
     for (int c = 0; c <= TN * TM; ++c) {
       const int g = c / TM, f = c % TM;
@@ -380,7 +393,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args A, Y 
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        if (c < TN * TM) {
+        if (kNative && c < TN * TM) {
+          if (k % 4 == 0) {
+            const f32x16 zero = {};
+            part[c & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                quarter(rw[g], k / 4), quarter(rq[f], k / 4), k ? part[c & 1] : zero, 0, 0, 0, 0, 0, 0);
+          }
+        } else if (c < TN * TM) {
           if (f == 0) wh[k] = widen(rw[g][k / 2][2 * (k & 1)], rw[g][k / 2][2 * (k & 1) + 1]);
           if (g == 0) qh[f][k] = widen(rq[f][k / 2][2 * (k & 1)], rq[f][k / 2][2 * (k & 1) + 1]);
           const f32x16 zero = {};
@@ -423,9 +442,9 @@ hipError_t stream(const Fp8Args &A, Y *y, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename Y, int BM, int BN, int WM, int WN, int NS>
+template <typename Y, int BM, int BN, int WM, int WN, int NS, bool kNative = false>
 hipError_t tile(const Fp8Args &A, Y *y, hipStream_t s) {
-  fp8_tile_kernel<Y, BM, BN, WM, WN, NS><<<(unsigned)tiles(A, BM, BN), 64 * WM * WN, 0, s>>>(A, y);
+  fp8_tile_kernel<Y, BM, BN, WM, WN, NS, kNative><<<(unsigned)tiles(A, BM, BN), 64 * WM * WN, 0, s>>>(A, y);
   return hipGetLastError();
 }
 
@@ -437,6 +456,8 @@ hipError_t stream1(const Fp8Args &A, Y *y, int num_cus, hipStream_t s) {
   const bool four = A.kb <= 4 || (A.kb <= 16 && tiles(A, 16, 16) > 2 * num_cus);
   return four ? stream<Y, 1, 4, 2>(A, y, s) : stream<Y, 1, 8, 2>(A, y, s);
 }
+
+constexpr int kMinNativeBlocks = 32;      // see the top
 
 template <typename Y>
 hipError_t run(const Fp8Args &A, Y *y, int num_cus, hipStream_t s) {
@@ -450,7 +471,11 @@ hipError_t run(const Fp8Args &A, Y *y, int num_cus, hipStream_t s) {
   // many: 128 x 128 tiles, two workgroups a CU (us at 512 tokens, 14336x4096: 66, with 64 x 128
   // tiles 77; 64 matrices of 2048x2048 with 128 rows each: 114 against 118, with 64: 87
   // against 82)
-  if (per >= 96 && tiles(A, 128, 128) >= num_cus) return tile<Y, 128, 128, 2, 2, 2>(A, y, s);
+  if (per >= 96 && tiles(A, 128, 128) >= num_cus) {
+    if constexpr (sizeof(Y) == 2)
+      if (A.kb >= kMinNativeBlocks) return tile<Y, 128, 128, 2, 2, 2, true>(A, y, s);
+    return tile<Y, 128, 128, 2, 2, 2>(A, y, s);
+  }
   // experts' matrices, and more than 8 tokens of one: 64 x 128 tiles (us, 64 matrices of
   // 2048x2048 with 1 / 8 / 32 rows each: 45 / 55 / 64, reading 16 rows a workgroup 49 / 73 /
   // 153; one matrix of 32768x4096, 1 token 37 against 30, 16 tokens 36 against 39)

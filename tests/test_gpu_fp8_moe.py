@@ -185,6 +185,47 @@ def test_gemm_routes(m, n, k):
         check_product(y, ref, mag, k, dtype, f"{m}x{n}x{k} {dtype}")
 
 
+@pytest.mark.parametrize("kind", ["dense", "grouped"])
+def test_native_sums(kind):
+    """Large products with 16-bit results and 32 blocks a row or more.  The 8-bit instructions: of each 8
+    neighbouring products the largest keeps its bits and the other 7 lose less than
+    2^-13 of it each; an eighth such loss stands for adding the groups.  So a sum is off
+    by less than 2^-10 of the largest product, over all groups of 8, and by what
+    gemm_tol counts.  The error's norm: 2^-13 of the result's, and the rounding to 16 bits,
+    uniform over half a step."""
+    rng = np.random.default_rng(11)
+    m, n, k = (260, 11000, 4096) if kind == "dense" else (280, 4000, 4100)
+    dtype = torch.bfloat16 if kind == "dense" else torch.float16
+    rows = np.sort(rng.choice(m, 24, replace=False))              # the rows that are checked
+    cols = rng.choice(n, 300, replace=False)
+    q, qs = of8.quant_act(acts(rng, m, k))
+    w, ws = of8.quant_weight((0.02 * rng.standard_normal((n, k))).astype(np.float32))
+    wd, sd, qd, qsd = dev(w, F8), dev(ws), dev(q, F8), dev(qs)
+    if kind == "dense":
+        y = B.fp8_gemm(wd, sd, k, qd, qsd, dtype=dtype)
+        exact = B.fp8_gemm(wd, sd, k, qd, qsd, dtype=torch.float32)
+    else:
+        off = dev(np.array([0, 130, m], dtype=np.int32))
+        two, s2 = torch.stack([wd.view(torch.uint8)] * 2).view(F8), torch.stack([sd] * 2)
+        y = B.fp8_gemm_grouped(two, s2, k, qd, qsd, off, dtype=dtype)
+        exact = B.fp8_gemm_grouped(two, s2, k, qd, qsd, off, dtype=torch.float32)
+    y, exact = host(y), host(exact)
+    full, mag = of8.gemm(w, ws, q[rows], qs[:, rows])
+    ref, mag = full[:, cols], mag[:, cols]
+    wide = np.repeat(ws, 128, axis=0)[:n][cols]                   # a scale row for each chosen weight row
+    a = np.abs(of8.act_values(q[rows], qs[:, rows])).reshape(len(rows), -1, 8)
+    b = np.abs(of8.decode(w[cols]) * np.repeat(wide.astype(np.float64), 128, axis=1)).reshape(len(cols), -1, 8)
+    lost = 2.0 ** -10 * np.stack([(a[t][None] * b).max(2).sum(1) for t in range(len(rows))])
+    half = torch.finfo(dtype).eps / 2
+    got = y[np.ix_(rows, cols)]
+    tol = lost + gemm_tol(k) * mag
+    assert np.all(np.abs(got - ref) <= tol + half * (np.abs(ref) + tol) + 2.0 ** -25)
+    e32 = exact[np.ix_(rows, cols)]
+    assert np.all(np.abs(e32 - ref) <= (gemm_tol(k) + 2.0 ** -24) * mag)      # fp32 results do not take it
+    rel = np.linalg.norm(got - ref) / np.linalg.norm(ref)
+    assert rel <= 2.0 ** -13 + half / math.sqrt(3)
+
+
 @pytest.mark.parametrize("m,n,k", [(1, 100, 384), (20, 100, 384), (90, 200, 384), (300, 300, 384)])
 def test_gemm_scales_of_any_size_and_nan(m, n, k):
     """Scales from 2^-100 to 2^60, negative and zero ones; a NaN token poisons its row alone."""
