@@ -24,6 +24,8 @@
 // results are groups of four neighbouring rows of one token: one scale a lane and
 // block, and stores of four elements.  Any order of the 128 columns does, as long as both
 // operands use the same one.
+#include <type_traits>
+
 #include "lowp_types.h"
 
 namespace bqm {
@@ -340,78 +342,141 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args A, Y 
     stage_rows<LN>(wb, src + LM, b * kBlk, lds + at + wave * 1024 + BM * kBlk, kRowsPerLoad * kBlk);
     stage_scales(sb + b * sstep, soff, lds + at + sdst);
   };
+  auto load_one = [&](int at, int b, int i) {                  // load i of load_stage's kLoads
+    uint8_t *to = lds + at + wave * 1024 + i * kRowsPerLoad * kBlk;
+    if (i < LM) stage_rows<1>(qb, src + i, b * kBlk, to, 0);
+    else if (i < LM + LN) stage_rows<1>(wb, src + i, b * kBlk, to, 0);
+    else if (i == LM + LN) stage_scales(sb + b * sstep, soff, lds + at + sdst);
+  };
 
-  f32x16 acc[TN][TM] = {};
-#pragma unroll
-  for (int i = 0; i < NS - 1; ++i)
-    if (i < A.kb) load_stage(i * kStage, i);
+  // The pipeline.  Chain c of a block multiplies row fragment c / TM and token fragment
+  // c % TM in 8 steps of 16 columns (2 of 64 with the 8-bit instruction).  By chain kMeet
+  // every wave has read the block's last fragments: there the waves meet, the next
+  // block's loads have landed, and the buffer takes the block NS ahead, the loads
+  // spread over the steps left: a compute unit's loads to LDS go 64 bytes a cycle, and a wave
+  // that issues all of them at once waits for its turns (8 of them held up the first
+  // chain by 500 of the block's 2600 cycles).  Between a chain's steps the next step's
+  // codes are widened, the sums of the chain before are scaled and added, and fragments and
+  // scales of the chains ahead are read, the next block's first ones during the last
+  // (4096 x 14336 x 4096 on the fp16 instructions: 438 us with loads and reads at
+  // the block's start, 406 so; 256 x 4096 x 4096 on 64 x 64 tiles 20.3, 17.0).
+  constexpr int C = TN * TM, kMeet = TN > 1 ? (TN - 2) * TM + 1 : 0;
+  constexpr int kEvery = 8 * (C - kMeet) / kLoads;           // steps a load
+  static_assert(kEvery >= 1, "every load has a step");
   const int sz = (row >> 1) & 7;
   int coff[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) coff[j] = row * kBlk + (((2 * j + half) ^ sz) << 4);
+  const int fq = wm * TM * 32 * kBlk, fw = BM * kBlk + wn * TN * 32 * kBlk;
+  auto chunk = [&](int at, int j) { return *reinterpret_cast<const i32x4 *>(lds + at + coff[j]); };
+  auto scale_of = [&](int at, int i) { return reinterpret_cast<const float *>(lds + at + kScale)[i]; };
+  f32x16 acc[TN][TM] = {}, last = {};
+  float s[TM], s_last = 0.0f;
+  i32x4 rw[TN][4], rq[TM][4];
+#pragma unroll
+  for (int i = 0; i < NS; ++i)
+    if (i < A.kb) load_stage(i * kStage, i);
+  if (NS <= A.kb) wait_and_meet<(NS - 1) * kLoads>();
+  else wait_and_meet<0>();
   const bool any_row = wm * TM * 32 <= pmax;
-  int at = 0, to = (NS - 1) * kStage;
-  for (int b = 0; b < A.kb; ++b) {
-    if (b + NS - 2 < A.kb) wait_and_meet<(NS - 2) * kLoads>();
-    else wait_and_meet<0>();
-    if (b + NS - 1 < A.kb) load_stage(to, b + NS - 1);
-    const int here = at;
-    at = at + kStage < NS * kStage ? at + kStage : 0;
-    to = to + kStage < NS * kStage ? to + kStage : 0;
-    if (!any_row) continue;                                    // only loads and meets
-    const uint8_t *lq = lds + here + wm * TM * 32 * kBlk;
-    const uint8_t *lw = lds + here + BM * kBlk + wn * TN * 32 * kBlk;
-    const float *ls = reinterpret_cast<const float *>(lds + here + kScale);
-    i32x4 rq[TM][4], rw[TN][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      rw[0][j] = *reinterpret_cast<const i32x4 *>(lw + coff[j]);
-      rq[0][j] = *reinterpret_cast<const i32x4 *>(lq + coff[j]);
+  for (int j = 0; j < 4; ++j) {
+    rw[0][j] = chunk(fw, j);
+    rq[0][j] = chunk(fq, j);
+  }
+#pragma unroll
+  for (int f = 0; f < TM; ++f) s[f] = scale_of(0, (wm * TM + f) * 32 + row) * scale_of(0, BM);
+  f16x8 qh[TM][8], wh[8];
+  auto half_of = [](const i32x4 (&r)[4], int k) {
+    return __builtin_shufflevector(r[2 * k], r[2 * k + 1], 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  auto eighth = [](const i32x4 (&r)[4], int k) { return widen(r[k / 2][2 * (k & 1)], r[k / 2][2 * (k & 1) + 1]); };
+  if constexpr (!kNative) {
+    wh[0] = eighth(rw[0], 0);
+    qh[0][0] = eighth(rq[0], 0);
+  }
+  if (!any_row) {                                              // only loads and meets
+    for (int b = 0, at = 0; b + 1 < A.kb; ++b) {
+      if (b + NS - 1 < A.kb) wait_and_meet<(NS - 2) * kLoads>();
+      else wait_and_meet<0>();
+      if (b + NS < A.kb) load_stage(at, b + NS);
+      at = at + kStage < NS * kStage ? at + kStage : 0;
     }
-#pragma unroll
-    for (int f = 1; f < TM; ++f)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) rq[f][j] = *reinterpret_cast<const i32x4 *>(lq + f * 32 * kBlk + coff[j]);
-    float s[TM];
-    const float sw = ls[BM];
-#pragma unroll
-    for (int f = 0; f < TM; ++f) s[f] = ls[(wm * TM + f) * 32 + row] * sw;
-    // Chain c multiplies row fragment c / TM and token fragment c % TM, 8 steps of 16
-    // columns (2 of 64 with the 8-bit instruction); between its steps the codes it is the
-    // first to use are widened and the sums of chain c - 1 scaled and added.
-    f16x8 qh[TM][8], wh[8];
+    return;
+  }
+  int at = 0;
+  // one block; kMore: with loads of the block NS ahead, kNext: with another block after it
+  auto block = [&](int b, auto more, auto next) __attribute__((always_inline)) {
+    constexpr bool kMore = decltype(more)::value, kNext = decltype(next)::value;
+    const int nx = at + kStage < NS * kStage ? at + kStage : 0;
+    i32x4 rwn[4], rqn[4];
+    float sn[TM], swn;
     f32x16 part[2];
-    auto quarter = [](const i32x4 (&r)[4], int k) {
-      return __builtin_shufflevector(r[2 * k], r[2 * k + 1], 0, 1, 2, 3, 4, 5, 6, 7);
-    };
 #pragma unroll
-    for (int c = 0; c <= TN * TM; ++c) {
+    for (int c = 0; c < C; ++c) {
       const int g = c / TM, f = c % TM;
-      if (c < TN * TM && f == 0 && g + 1 < TN) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) rw[g + 1][j] = *reinterpret_cast<const i32x4 *>(lw + (g + 1) * 32 * kBlk + coff[j]);
+      if (kNext && c == kMeet) {
+        if (kMore || b + NS - 1 < A.kb) wait_and_meet<(NS - 2) * kLoads>();
+        else wait_and_meet<0>();
       }
+      const int pc = c ? c - 1 : C - 1, pg = pc / TM, pf = pc % TM;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        if (kNative && c < TN * TM) {
-          if (k % 4 == 0) {
-            const f32x16 zero = {};
-            part[c & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                quarter(rw[g], k / 4), quarter(rq[f], k / 4), k ? part[c & 1] : zero, 0, 0, 0, 0, 0, 0);
+        const int step = (c - kMeet) * 8 + k;
+        if (kMore && step >= 0 && step % kEvery == 0 && step / kEvery < kLoads) load_one(at, b + NS, step / kEvery);
+        if (k < 4) {
+          if (g == 0 && f + 1 < TM) rq[f + 1][k] = chunk(at + fq + (f + 1) * 32 * kBlk, k);
+          if (f == 0 && g + 1 < TN) rw[g + 1][k] = chunk(at + fw + (g + 1) * 32 * kBlk, k);
+          if (kNext && c == C - 1) {
+            rwn[k] = chunk(nx + fw, k);
+            rqn[k] = chunk(nx + fq, k);
           }
-        } else if (c < TN * TM) {
-          if (f == 0) wh[k] = widen(rw[g][k / 2][2 * (k & 1)], rw[g][k / 2][2 * (k & 1) + 1]);
-          if (g == 0) qh[f][k] = widen(rq[f][k / 2][2 * (k & 1)], rq[f][k / 2][2 * (k & 1) + 1]);
-          const f32x16 zero = {};
-          part[c & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wh[k], qh[f][k], k ? part[c & 1] : zero, 0, 0, 0);
-        }
-        if (c > 0)
+        } else if (kNext && c == C - 1 && k == 4) {
 #pragma unroll
-          for (int i = 2 * k; i < 2 * k + 2; ++i)
-            acc[(c - 1) / TM][(c - 1) % TM][i] = fmaf(part[(c - 1) & 1][i], s[(c - 1) % TM], acc[(c - 1) / TM][(c - 1) % TM][i]);
+          for (int i = 0; i < TM; ++i) sn[i] = scale_of(nx, (wm * TM + i) * 32 + row);
+          swn = scale_of(nx, BM);
+        }
+        const f32x16 zero = {};
+        if constexpr (kNative) {
+          if (k % 4 == 0)
+            part[c & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                half_of(rw[g], k / 4), half_of(rq[f], k / 4), k ? part[c & 1] : zero, 0, 0, 0, 0, 0, 0);
+        } else {
+          part[c & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wh[k], qh[f][k], k ? part[c & 1] : zero, 0, 0, 0);
+          const int k1 = (k + 1) & 7, c1 = k == 7 ? c + 1 : c, g1 = c1 / TM, f1 = c1 % TM;
+          if (c1 < C) {
+            if (f1 == 0) wh[k1] = eighth(rw[g1], k1);
+            if (g1 == 0) qh[f1][k1] = eighth(rq[f1], k1);
+          } else if (kNext) {
+            wh[0] = eighth(rwn, 0);
+            qh[0][0] = eighth(rqn, 0);
+          }
+        }
+#pragma unroll
+        for (int i = 2 * k; i < 2 * k + 2; ++i)
+          acc[pg][pf][i] = fmaf(c ? part[(c - 1) & 1][i] : last[i], c ? s[pf] : s_last, acc[pg][pf][i]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
-  }
+    last = part[(C - 1) & 1];
+    s_last = s[TM - 1];
+    if constexpr (kNext) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        rw[0][j] = rwn[j];
+        rq[0][j] = rqn[j];
+      }
+#pragma unroll
+      for (int f = 0; f < TM; ++f) s[f] = sn[f] * swn;
+    }
+    at = nx;
+  };
+  int b = 0;
+  for (; b + NS < A.kb; ++b) block(b, std::true_type{}, std::true_type{});
+  for (; b + 1 < A.kb; ++b) block(b, std::false_type{}, std::true_type{});
+  block(b, std::false_type{}, std::false_type{});
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[TN - 1][TM - 1][i] = fmaf(last[i], s_last, acc[TN - 1][TM - 1][i]);
 #pragma unroll
   for (int f = 0; f < TM; ++f) {
     const int p = t.p0 + (wm * TM + f) * 32 + row;
