@@ -529,28 +529,32 @@ hipError_t run(const Fp8Args &A, Y *y, int num_cus, hipStream_t s) {
   // rows a matrix has to multiply: exact for one matrix, the mean for experts
   const int per = A.offsets ? (A.slots + A.experts - 1) / A.experts : A.m;
   // few tiles: the smallest token tile that leaves none of them waiting for a CU (us at 64
-  // tokens: 1024x4096 6.8 with 16 a tile, 4096x4096 12.5 with 64; 64 x 64 tiles 18.0, 19.8)
+  // tokens: 1024x4096 6.3 with 16 a tile, 4096x4096 12.4 with 64; 64 x 64 tiles 15.5, 16.1)
   if (tiles(A, 16, 16) <= num_cus) return stream1(A, y, num_cus, s);
   if (tiles(A, 32, 16) <= num_cus) return stream<Y, 2, 8, 1>(A, y, s);
   if (tiles(A, 64, 16) <= num_cus) return stream<Y, 4, 8, 1>(A, y, s);
-  // many: 128 x 128 tiles, two workgroups a CU (us at 512 tokens, 14336x4096: 66, with 64 x 128
-  // tiles 77; 64 matrices of 2048x2048 with 128 rows each: 114 against 118, with 64: 87
-  // against 82)
+  // many: 128 x 128 tiles, two workgroups a CU (us, 512 tokens of 14336x4096: 61, with 64 x 128
+  // tiles 70; 64 matrices of 2048x2048 with 128 rows each: 106 against 114, with 96: 97
+  // against 96)
   if (per >= 96 && tiles(A, 128, 128) >= num_cus) {
     if constexpr (sizeof(Y) == 2)
       if (A.kb >= kMinNativeBlocks) return tile<Y, 128, 128, 2, 2, 2, true>(A, y, s);
     return tile<Y, 128, 128, 2, 2, 2>(A, y, s);
   }
-  // experts' matrices, and more than 8 tokens of one: 64 x 128 tiles (us, 64 matrices of
-  // 2048x2048 with 1 / 8 / 32 rows each: 45 / 55 / 64, reading 16 rows a workgroup 49 / 73 /
-  // 153; one matrix of 32768x4096, 1 token 37 against 30, 16 tokens 36 against 39)
-  if ((A.offsets || per > 8) && tiles(A, 64, 128) >= num_cus) return tile<Y, 64, 128, 2, 2, 3>(A, y, s);
+  // experts' matrices, and more than 8 tokens of one, as soon as tiles fill most CUs: 64 x 128,
+  // three blocks deep, or 64 x 64, four deep (us, 64 matrices of 2048x2048 with 1/4, 2, 8 and
+  // 32 rows each: 64 x 128 15 / 43 / 54 / 61, 16 rows a workgroup 17 / 49 / 74 / 154; one matrix
+  // of 14336x4096 with 16, 32 and 128 tokens: 64 x 64 16.7 / 17.3 / 29.1, 64 x 128 21.2 / 21.6 /
+  // 24.6, 16 or 32 rows a workgroup 20.0 / 26.0 / 79; of 32768x4096 with 8: 35 / 37 / 34)
+  const int most = num_cus * 3 / 4;
+  if (A.offsets || per > 8) {
+    if (tiles(A, 64, 128) >= most) return tile<Y, 64, 128, 2, 2, 3>(A, y, s);
+    if (tiles(A, 64, 64) >= most && per > 8) return tile<Y, 64, 64, 2, 2, 4>(A, y, s);
+  }
   if (per <= 16) return stream1(A, y, num_cus, s);
-  // up to 32 tokens reading the weights once counts, until 64 x 64 tiles fill the CUs (us at
-  // 32: 4096x14336 16.6 against 59, 14336x4096 25.8 against 20.2)
-  if (per <= 32 && tiles(A, 64, 64) < num_cus * 3 / 4) return stream<Y, 2, 8, 1>(A, y, s);
-  // 64 x 64 tiles, four blocks deep (us at 256 tokens, 4096x4096: 19.0, two deep 25, 64 x 128
-  // tiles 24)
+  // too few tiles: up to 32 tokens reading the weights once counts (us at 32, 4096x14336: 16.6
+  // against 48)
+  if (per <= 32) return stream<Y, 2, 8, 1>(A, y, s);
   return tile<Y, 64, 64, 2, 2, 4>(A, y, s);
 }
 
