@@ -96,7 +96,8 @@ __device__ __forceinline__ void silu_mul8(float (&g)[8], const float (&u)[8]) {
   for (int j = 0; j < 8; ++j) {
     const float p = -g[j] * kL;
     const float lost = fmaf(-g[j], kLlo, fmaf(-g[j], kL, -p));
-    const float d = 1.0f + __builtin_amdgcn_exp2f(p) * fmaf(lost, kLn2, 1.0f);
+    const float e = __builtin_amdgcn_exp2f(p);
+    const float d = 1.0f + fmaf(e, lost * kLn2, e);
     const float r = __builtin_amdgcn_rcpf(d);
     const float a = g[j] * r;
     q[j] = fmaf(fmaf(-a, d, g[j]), r, a);
