@@ -165,14 +165,16 @@ def _codebook_ptr(codebook, levels=None):
 
 # ---------------------------------------------------------------- device calls
 
-_torch_module = None
+_torch_module = _get_device = _raw_stream = None
 
 
 def _torch():
-    global _torch_module
+    global _torch_module, _get_device, _raw_stream
     if _torch_module is None:
         import torch
         _torch_module = torch
+        # the current device's index and a device's current stream, as integers
+        _get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     return _torch_module
 
 
@@ -556,13 +558,6 @@ def _dtype_code(dtype, name):
 # the host does for them counts: each operand is checked in one pass over its
 # attributes, and the messages are formed only when a check fails.
 
-def _current():
-    """(current device, its current stream as an integer)."""
-    c = _torch()._C
-    d = c._cuda_getDevice()
-    return d, c._cuda_getCurrentRawStream(d)
-
-
 def _operand(t, dtype, shape, device, name):
     """The address of a contiguous `dtype` tensor of `shape` on the current device."""
     try:
@@ -575,40 +570,41 @@ def _operand(t, dtype, shape, device, name):
     raise ValueError(f"{name} must be on the current device {device}, got {t.device}")
 
 
-def _row_strided(t, device, name):
-    """A 2-D tensor whose rows are contiguous: (address, dtype code, row stride)."""
-    torch = _torch()
+def _row_strided(t, name):
+    """A 2-D device tensor whose rows are contiguous: (address, dtype code, row stride, rows,
+    columns, the current device)."""
+    torch = _torch_module or _torch()
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor, got {tuple(getattr(t, 'shape', ()))}")
     code = _dtype_code(t.dtype, name)
     n, cols = t.shape
+    row, col = t.stride()
     if n < 1 or cols < 1:
         raise ValueError(f"{name} must not be empty, got {tuple(t.shape)}")
-    row, col = t.stride()
     if col != 1 and cols > 1:
         raise ValueError(f"{name}'s rows must be contiguous (stride {t.stride()})")
-    if n > 1 and row < cols:
+    if row < cols and n > 1:
         raise ValueError(f"{name}'s rows must not overlap (stride {t.stride()})")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA/HIP tensor")
+    device = _get_device()
     if t.get_device() != device:
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA/HIP tensor")
         raise ValueError(f"{name} must be on the current device {device}, got {t.device}")
-    return t.data_ptr(), code, row, n, cols
+    return t.data_ptr(), code, row, n, cols, device
 
 
 def _result(y, dtype, shape, device, name="y"):
     """y, or a new tensor, as (tensor, address)."""
     if y is None:
-        y = _torch().empty(*shape, dtype=dtype, device=device)
+        y = _torch_module.empty(*shape, dtype=dtype, device=device)
         return y, y.data_ptr()
     return y, _operand(y, dtype, shape, device, name)
 
 
-def _device_of(t, name):
-    """The current device and stream; refuses a host tensor before anything else is done."""
+def _need_device(t, name):
+    """Refuses a host tensor, before the current device is asked for (there may be none)."""
     if not getattr(t, "is_cuda", False):
         raise ValueError(f"{name} must be a CUDA/HIP tensor")
-    return _current()
 
 
 def fp8_quant(x, swiglu: bool = False, q=None, scale=None):
@@ -616,20 +612,16 @@ def fp8_quant(x, swiglu: bool = False, q=None, scale=None):
     [m, 128 kb], scale fp32 [kb, m]), one scale a token and 128 columns, kb =
     ceil(k / 128).  With swiglu, x is [m, 2 k] = [gate | up] and silu(gate) * up
     is quantized."""
-    torch = _torch()
-    if getattr(x, "ndim", 0) != 2:
-        raise ValueError(f"x must be a 2-D tensor, got {tuple(getattr(x, 'shape', ()))}")
-    _dtype_code(x.dtype, "x")
-    dev, stream = _device_of(x, "x")
-    xp, code, stride, m, k = _row_strided(x, dev, "x")
+    xp, code, stride, m, k, dev = _row_strided(x, "x")
     if swiglu:
         if k % 2:
             raise ValueError(f"x must hold gate and up columns, got {k}")
         k //= 2
     kb = (k + 127) // 128
-    q, qp = _result(q, torch.float8_e4m3fn, (m, kb * FP8_BLOCK), dev, "q")
+    torch = _torch_module
+    q, qp = _result(q, torch.float8_e4m3fn, (m, kb * 128), dev, "q")
     scale, sp = _result(scale, torch.float32, (kb, m), dev, "scale")
-    rc = (_lib or load_library()).fp8_quant(xp, code, m, k, stride, bool(swiglu), qp, sp, stream)
+    rc = (_lib or load_library()).fp8_quant(xp, code, m, k, stride, 1 if swiglu else 0, qp, sp, _raw_stream(dev))
     if rc:
         _check("fp8_quant", rc)
     return q, scale
@@ -643,13 +635,14 @@ def fp8_pack(w, q=None, scale=None):
     if getattr(w, "ndim", 0) not in (2, 3) or w.numel() < 1:
         raise ValueError(f"w must be [rows, cols] or [experts, rows, cols], got {tuple(getattr(w, 'shape', ()))}")
     code = _dtype_code(w.dtype, "w")
-    dev, stream = _device_of(w, "w")
+    _need_device(w, "w")
+    dev = _get_device()
     wp = _operand(w, w.dtype, w.shape, dev, "w")
     lead, (rows, cols) = tuple(w.shape[:-2]), w.shape[-2:]
     kb = fp8_blocks(cols)
     q, qp = _result(q, torch.float8_e4m3fn, (*lead, rows, kb * FP8_BLOCK), dev, "q")
     scale, sp = _result(scale, torch.float32, (*lead, fp8_blocks(rows), kb), dev, "scale")
-    _check("fp8_pack", load_library().fp8_pack(wp, code, lead[0] if lead else 1, rows, cols, qp, sp, stream))
+    _check("fp8_pack", load_library().fp8_pack(wp, code, lead[0] if lead else 1, rows, cols, qp, sp, _raw_stream(dev)))
     return q, scale
 
 
@@ -688,13 +681,13 @@ def fp8_gemm(w, w_scale, cols: int, q, q_scale, dtype=None, y=None):
         _shape(w_scale, (nb, kb), "w_scale")
         _shape(q_scale, (kb, m), "q_scale")
         raise ValueError("q must be a CUDA/HIP tensor")
-    dev, stream = _current()
+    dev = _get_device()
     wp = _operand(w, f8, (rows, kp), dev, "w")
     wsp = _operand(w_scale, f32, (nb, kb), dev, "w_scale")
     qp = _operand(q, f8, (m, kp), dev, "q")
     qsp = _operand(q_scale, f32, (kb, m), dev, "q_scale")
     y, yp = _result(y, ydtype, (m, rows), dev)
-    rc = (_lib or load_library()).fp8_gemm(wp, wsp, rows, cols, qp, qsp, m, yp, ycode, stream)
+    rc = (_lib or load_library()).fp8_gemm(wp, wsp, rows, cols, qp, qsp, m, yp, ycode, _raw_stream(dev))
     if rc:
         _check("fp8_gemm", rc)
     return y
@@ -718,7 +711,8 @@ def fp8_gemm_grouped(w, w_scale, cols: int, q, q_scale, offsets, row_ids=None, d
         if getattr(row_ids, "ndim", 0) != 1 or row_ids.shape[0] < 1:
             raise ValueError(f"row_ids must have shape [slots], got {tuple(getattr(row_ids, 'shape', ()))}")
         slots = row_ids.shape[0]
-    dev, stream = _device_of(q, "q")
+    _need_device(q, "q")
+    dev = _get_device()
     wp = _operand(w, f8, (experts, rows, kp), dev, "w")
     wsp = _operand(w_scale, f32, (experts, (rows + 127) // 128, kb), dev, "w_scale")
     qp = _operand(q, f8, (m, kp), dev, "q")
@@ -726,7 +720,8 @@ def fp8_gemm_grouped(w, w_scale, cols: int, q, q_scale, offsets, row_ids=None, d
     op = _operand(offsets, i32, (experts + 1,), dev, "offsets")
     rp = None if row_ids is None else _operand(row_ids, i32, (slots,), dev, "row_ids")
     y, yp = _result(y, ydtype, (slots, rows), dev)
-    rc = (_lib or load_library()).fp8_gemm_grouped(wp, wsp, experts, rows, cols, qp, qsp, m, op, rp, slots, yp, ycode, stream)
+    rc = (_lib or load_library()).fp8_gemm_grouped(wp, wsp, experts, rows, cols, qp, qsp, m, op, rp, slots, yp, ycode,
+                                                   _raw_stream(dev))
     if rc:
         _check("fp8_gemm_grouped", rc)
     return y
@@ -752,11 +747,8 @@ def moe_route(logits, top: int, renorm: bool = True, workspace=None) -> MoeRoute
     """logits [tokens, experts] -> MoeRoute: the `top` largest logits of each token, their
     softmax weights (over the chosen with renorm, else over all) and the pairs sorted
     by expert.  The results share one allocation."""
-    torch = _torch()
-    if getattr(logits, "ndim", 0) != 2:
-        raise ValueError(f"logits must be a 2-D tensor, got {tuple(getattr(logits, 'shape', ()))}")
-    dev, stream = _device_of(logits, "logits")
-    lp, code, stride, tokens, experts = _row_strided(logits, dev, "logits")
+    lp, code, stride, tokens, experts, dev = _row_strided(logits, "logits")
+    torch = _torch_module
     need = moe_route_workspace(tokens, experts, top)
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
@@ -769,8 +761,8 @@ def moe_route(logits, top: int, renorm: bool = True, workspace=None) -> MoeRoute
     base = torch.empty(4 * pairs + experts + 1, dtype=torch.int32, device=dev)
     p = base.data_ptr()
     rc = (_lib or load_library()).moe_route(
-        lp, code, tokens, experts, stride, top, bool(renorm), p, p + 12 * pairs, p + 16 * pairs, p + 8 * pairs,
-        p + 4 * pairs, wp, need, stream)
+        lp, code, tokens, experts, stride, top, 1 if renorm else 0, p, p + 12 * pairs, p + 16 * pairs, p + 8 * pairs,
+        p + 4 * pairs, wp, need, _raw_stream(dev))
     if rc:
         _check("moe_route", rc)
     ids, slots, row_ids, weights, offsets = base.split((pairs, pairs, pairs, pairs, experts + 1))
@@ -791,12 +783,13 @@ def moe_combine(y, slots, weights, out=None):
     rows, d = y.shape
     if not y.is_cuda:
         _shape(weights, (tokens, top), "weights")
-    dev, stream = _device_of(y, "y")
+    _need_device(y, "y")
+    dev = _get_device()
     yp = _operand(y, y.dtype, (rows, d), dev, "y")
     sp = _operand(slots, torch.int32, (tokens, top), dev, "slots")
     wp = _operand(weights, torch.float32, (tokens, top), dev, "weights")
     out, op = _result(out, y.dtype, (tokens, d), dev, "out")
-    rc = (_lib or load_library()).moe_combine(yp, code, rows, d, sp, wp, tokens, top, op, stream)
+    rc = (_lib or load_library()).moe_combine(yp, code, rows, d, sp, wp, tokens, top, op, _raw_stream(dev))
     if rc:
         _check("moe_combine", rc)
     return out

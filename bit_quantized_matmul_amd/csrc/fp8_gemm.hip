@@ -180,7 +180,7 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Args A, Y *__res
   const uint8_t *w = A.w + ((int64_t)t.e * A.rows + min(t.n0 + row, A.rows - 1)) * kp + grp * 16;
   const float *ws = A.ws + ((int64_t)t.e * ((A.rows + kBlk - 1) / kBlk) + t.n0 / kBlk) * A.kb;
   // the weights' addresses depend on the tile alone: they go out before the tokens are known
-  i32x4 wl[kDepth][2];
+  i32x4 wl[kDepth][2] = {};
   auto load_w = [&](int b0) {
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
@@ -452,6 +452,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args A, Y 
             qh[0][0] = eighth(rqn, 0);
           }
         }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 2 * k; i < 2 * k + 2; ++i)
           acc[pg][pf][i] = fmaf(c ? part[(c - 1) & 1][i] : last[i], c ? s[pf] : s_last, acc[pg][pf][i]);

@@ -43,6 +43,7 @@ def test_quant_refuses(lib, args, code):
     ((P, 9, 1, 8, 128, P, P, None), EINVAL),
     ((P, 0, 4097, 8, 128, P, P, None), ENOTSUP),
     ((P, 0, 1, (1 << 24) + 1, 128, P, P, None), ENOTSUP),
+    ((P, 0, 1, 1 << 24, 1 << 22, P, P, None), ENOTSUP),                  # 2^32 blocks
     ((P, 0, 1, 8, 128, OFF8, P, None), EALIGN),
 ])
 def test_pack_refuses(lib, args, code):
@@ -57,6 +58,7 @@ def test_pack_refuses(lib, args, code):
     ((P, P, 8, 128, P, P, 0, P, 0, None), EINVAL),
     ((P, P, 8, 128, P, P, 1, P, 4, None), EINVAL),
     ((P, P, 8, (1 << 22) + 1, P, P, 1, P, 0, None), ENOTSUP),
+    ((P, P, 1 << 24, 128, P, P, 1 << 16, P, 0, None), ENOTSUP),         # 2^32 tiles
     ((OFF8, P, 8, 128, P, P, 1, P, 0, None), EALIGN),
     ((P, P, 8, 128, OFF8, P, 1, P, 0, None), EALIGN),
     ((P, ODD, 8, 128, P, P, 1, P, 0, None), EALIGN),

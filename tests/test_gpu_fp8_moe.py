@@ -292,6 +292,20 @@ def test_grouped_leaves_other_rows_alone(sizes, slots):
     assert np.all(np.abs(got[lo:hi] - ref[lo:hi]) <= (gemm_tol(k) + 2.0 ** -24) * mag[lo:hi])
 
 
+def test_native_sums_pass_nan_on():
+    """A NaN code in a large 16-bit product makes its token's row NaN and no other."""
+    rng = np.random.default_rng(12)
+    m, n, k = 300, 16000, 4096
+    q, qs = of8.quant_act(acts(rng, m, k))
+    w, ws = of8.quant_weight((0.02 * rng.standard_normal((n, k))).astype(np.float32))
+    wd, sd, qsd = dev(w, F8), dev(ws), dev(qs)
+    y = B.fp8_gemm(wd, sd, k, dev(q, F8), qsd)
+    q[77, 4000] = 0xFF
+    z = B.fp8_gemm(wd, sd, k, dev(q, F8), qsd)
+    assert bool(torch.isnan(z[77]).all()) and bool(torch.isfinite(y).all())
+    assert torch.equal(z[:77], y[:77]) and torch.equal(z[78:], y[78:])
+
+
 # ------------------------------------------------------------------ routing
 
 def check_route(r, x, top, renorm, label):
@@ -308,7 +322,7 @@ def check_route(r, x, top, renorm, label):
 
 @pytest.mark.parametrize("tokens,experts,top", [(1, 1, 1), (1, 64, 8), (4, 64, 8), (3, 12, 3), (63, 7, 7), (64, 65, 4),
                                                 (65, 64, 2), (200, 256, 8), (300, 257, 5), (129, 1024, 32),
-                                                (1000, 100, 1), (5000, 32, 6)])
+                                                (1000, 100, 1), (5000, 32, 6), (64, 64, 32), (40000, 9, 2)])
 def test_route(tokens, experts, top):
     rng = np.random.default_rng(tokens + experts)
     for dtype in TYPES:
