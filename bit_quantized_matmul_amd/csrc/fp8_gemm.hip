@@ -10,10 +10,10 @@
 //    codes an instruction) and the fp16 matrix instructions sum their products in fp32.
 //    Every result in fp32, every row of fewer than 32 blocks, every small product.
 //  * by the 8-bit matrix instructions, at twice the rate and without conversions
-//    (4096 x 14336 x 4096: 268 against 437 us).  They keep, of each 8 products, only the 13
+//    (4096 x 14336 x 4096: 268 against 403 us).  They keep, of each 8 products, only the 13
 //    bits below the largest one: measured, 4e-5 of the result's norm where a few
 //    columns are 30 times the others, which is how activations are, and 2e-5 without.
-//    A result in 16 bits is rounded by 2^-9 (bf16) or 2^-12 (fp16) of itself, but one
+//    A result in 16 bits is rounded by up to 2^-8 (bf16) or 2^-11 (fp16) of itself, but one
 //    that nearly cancels shows the difference; it averages out over the blocks,
 //    and from 32 on the largest error is 1.1 to 1.3 times 2^-16 of the sum of the terms'
 //    magnitudes, the bound that fp32 sums of a block have (8 blocks: 3.3 times,
@@ -126,6 +126,9 @@ __device__ __forceinline__ bool find_tile(const Fp8Args &A, int bid, Tile *t) {
         const int first = before + (at ? __builtin_amdgcn_readlane(inc, at - 1) : 0);
         const int p0 = __builtin_amdgcn_readlane(lo, at), p1 = __builtin_amdgcn_readlane(hi, at);
         place_tile(want - first * nt, (p1 - p0 + BM - 1) / BM, nt, &mi, &ni);
+        // ascending offsets always pass; others, whose counts may overflow, stay in their buffers
+        if (e0 + at >= A.experts || (unsigned)mi >= (unsigned)((p1 - p0 + BM - 1) / BM) || (unsigned)ni >= (unsigned)nt)
+          return false;
         *t = {e0 + at, p0 + mi * BM, min(p1, p0 + mi * BM + BM), ni * BN};
         return true;
       }
@@ -169,7 +172,10 @@ __device__ __forceinline__ void store4(Y *y, const Fp8Args &A, int p, int r, f32
 // The weights are read once and bound the time.  A workgroup takes 16 weight
 // rows and up to 16 MF tokens; its waves take every NW-th block of the columns and
 // load operands straight into the matrix cores' registers, kDepth blocks ahead; the
-// waves' sums meet in LDS.
+// waves' sums meet in LDS.  A lane loads the 16-byte chunks g and g + 4 of a row (g its
+// group of 16 lanes), so one load reads 64 neighbouring bytes of each of 16 rows.  One token
+// of 4096x4096: 6.2 us for 3.4 us of bytes, the rest an empty launch (1.7) and the chain
+// from tile to loads to sum; of 32768x4096: 30 us, 4.5 TB/s.
 template <typename Y, int MF, int NW, int kDepth>
 __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Args A, Y *__restrict__ y) {
   Tile t;
@@ -242,29 +248,28 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Args A, Y *__res
       }
     }
   }
-  if constexpr (NW > 1) {
-    __shared__ f32x4_t red[NW][MF][64];
+  static_assert(MF <= NW, "a wave for every fragment");
+  __shared__ f32x4_t red[NW][MF][64];
 #pragma unroll
-    for (int f = 0; f < MF; ++f) red[wave][f][lane] = acc[f];
-    __syncthreads();
-    if (wave >= MF) return;
-    f32x4_t sum = red[0][wave][lane];                 // wave f adds up and stores fragment f
+  for (int f = 0; f < MF; ++f) red[wave][f][lane] = acc[f];
+  __syncthreads();
+  if (wave >= MF) return;
+  f32x4_t sum = red[0][wave][lane];                   // wave f adds up and stores fragment f
 #pragma unroll
-    for (int v = 1; v < NW; ++v) sum += red[v][wave][lane];
-    const int p = t.p0 + wave * 16 + row;
-    if (p < t.p1) store4(y, A, p, t.n0 + grp * 4, sum);
-  }
+  for (int v = 1; v < NW; ++v) sum += red[v][wave][lane];
+  const int p = t.p0 + wave * 16 + row;
+  if (p < t.p1) store4(y, A, p, t.n0 + grp * 4, sum);
 }
 
 // ------------------------------------------------------------------ tiles
 //
 // BM tokens x BN weight rows, WM x WN waves.  Per block of 128 columns both
 // operands' tiles and scales go to LDS without passing through registers, into one of
-// two buffers while the other is multiplied.  A tile's rows are 128 bytes; chunk c of
+// NS buffers while others are multiplied.  A tile's rows are 128 bytes; chunk c of
 // row r is stored at chunk c ^ ((r >> 1) & 7), so that the 16 rows a fragment load
-// touches at one chunk lie in 16 different groups of four banks.
-// Buffer loads, so that the next block costs one scalar addition instead of a 64-bit
-// vector one a load (441 against 443 us).
+// touches at one chunk lie in 16 different groups of four banks (no conflicts counted).
+// They are buffer loads: the next block costs one scalar addition, where flat addresses
+// cost a 64-bit vector addition a load.
 
 typedef __attribute__((address_space(3))) void lds_void;
 
