@@ -8,13 +8,13 @@ exception is raised.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from typing import NamedTuple
 
 import numpy as np
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libbqm.so")
+_CALLS_PATH = os.path.join(os.path.dirname(_LIB_PATH), "_calls.so")
 
 BQM_OK, BQM_EINVAL, BQM_EALIGN, BQM_ENOTSUP, BQM_EDEVICE, BQM_ERANGE = 0, -1, -2, -3, -4, -5
 BINARY, B2, B3, B4, TERNARY, TERNARY_B3 = 1, 2, 3, 4, 5, 6
@@ -165,17 +165,9 @@ def _codebook_ptr(codebook, levels=None):
 
 # ---------------------------------------------------------------- device calls
 
-_torch_module = _get_device = _raw_stream = None
-
-
 def _torch():
-    global _torch_module, _get_device, _raw_stream
-    if _torch_module is None:
-        import torch
-        _torch_module = torch
-        # the current device's index and a device's current stream, as integers
-        _get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-    return _torch_module
+    import torch
+    return torch
 
 
 def _stream():
@@ -554,10 +546,6 @@ def _dtype_code(dtype, name):
     return code
 
 
-# The calls below take a few microseconds on the device for one token, so what
-# the host does for them counts: each operand is checked in one pass over its
-# attributes, and the messages are formed only when a check fails.
-
 def _operand(t, dtype, shape, device, name):
     """The address of a contiguous `dtype` tensor of `shape` on the current device."""
     try:
@@ -570,41 +558,32 @@ def _operand(t, dtype, shape, device, name):
     raise ValueError(f"{name} must be on the current device {device}, got {t.device}")
 
 
-def _row_strided(t, name):
-    """A 2-D device tensor whose rows are contiguous: (address, dtype code, row stride, rows,
-    columns, the current device)."""
-    torch = _torch_module or _torch()
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
-        raise ValueError(f"{name} must be a 2-D tensor, got {tuple(getattr(t, 'shape', ()))}")
-    code = _dtype_code(t.dtype, name)
-    n, cols = t.shape
-    row, col = t.stride()
-    if n < 1 or cols < 1:
-        raise ValueError(f"{name} must not be empty, got {tuple(t.shape)}")
-    if col != 1 and cols > 1:
-        raise ValueError(f"{name}'s rows must be contiguous (stride {t.stride()})")
-    if row < cols and n > 1:
-        raise ValueError(f"{name}'s rows must not overlap (stride {t.stride()})")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA/HIP tensor")
-    device = _get_device()
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be on the current device {device}, got {t.device}")
-    return t.data_ptr(), code, row, n, cols, device
-
-
 def _result(y, dtype, shape, device, name="y"):
     """y, or a new tensor, as (tensor, address)."""
     if y is None:
-        y = _torch_module.empty(*shape, dtype=dtype, device=device)
+        y = _torch().empty(shape, dtype=dtype, device=device)
         return y, y.data_ptr()
     return y, _operand(y, dtype, shape, device, name)
 
 
-def _need_device(t, name):
-    """Refuses a host tensor, before the current device is asked for (there may be none)."""
-    if not getattr(t, "is_cuda", False):
-        raise ValueError(f"{name} must be a CUDA/HIP tensor")
+_calls_module = None
+
+
+def _calls():
+    """The extension that makes the calls a model needs for every token (``csrc/calls.cpp``:
+    checks, results and the call of the library, without the interpreter)."""
+    global _calls_module
+    if _calls_module is None:
+        if not os.path.exists(_CALLS_PATH):
+            raise RuntimeError(f"{_CALLS_PATH} is missing: build it with "
+                               "`python -m bit_quantized_matmul_amd.build`")
+        torch, lib = _torch(), load_library()
+        from . import _calls as module
+        names = ("fp8_quant", "fp8_gemm", "fp8_gemm_grouped", "moe_route_workspace", "moe_route", "moe_combine")
+        module.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names},
+                    torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+        _calls_module = module
+    return _calls_module
 
 
 def fp8_quant(x, swiglu: bool = False, q=None, scale=None):
@@ -612,19 +591,10 @@ def fp8_quant(x, swiglu: bool = False, q=None, scale=None):
     [m, 128 kb], scale fp32 [kb, m]), one scale a token and 128 columns, kb =
     ceil(k / 128).  With swiglu, x is [m, 2 k] = [gate | up] and silu(gate) * up
     is quantized."""
-    xp, code, stride, m, k, dev = _row_strided(x, "x")
-    if swiglu:
-        if k % 2:
-            raise ValueError(f"x must hold gate and up columns, got {k}")
-        k //= 2
-    kb = (k + 127) // 128
-    torch = _torch_module
-    q, qp = _result(q, torch.float8_e4m3fn, (m, kb * 128), dev, "q")
-    scale, sp = _result(scale, torch.float32, (kb, m), dev, "scale")
-    rc = (_lib or load_library()).fp8_quant(xp, code, m, k, stride, 1 if swiglu else 0, qp, sp, _raw_stream(dev))
-    if rc:
-        _check("fp8_quant", rc)
-    return q, scale
+    r = (_calls_module or _calls()).fp8_quant(x, swiglu, q, scale)
+    if type(r) is int:
+        _check("fp8_quant", r)
+    return r
 
 
 def fp8_pack(w, q=None, scale=None):
@@ -635,62 +605,25 @@ def fp8_pack(w, q=None, scale=None):
     if getattr(w, "ndim", 0) not in (2, 3) or w.numel() < 1:
         raise ValueError(f"w must be [rows, cols] or [experts, rows, cols], got {tuple(getattr(w, 'shape', ()))}")
     code = _dtype_code(w.dtype, "w")
-    _need_device(w, "w")
-    dev = _get_device()
+    if not w.is_cuda:
+        raise ValueError("w must be a CUDA/HIP tensor")
+    dev = torch.cuda.current_device()
     wp = _operand(w, w.dtype, w.shape, dev, "w")
     lead, (rows, cols) = tuple(w.shape[:-2]), w.shape[-2:]
     kb = fp8_blocks(cols)
     q, qp = _result(q, torch.float8_e4m3fn, (*lead, rows, kb * FP8_BLOCK), dev, "q")
     scale, sp = _result(scale, torch.float32, (*lead, fp8_blocks(rows), kb), dev, "scale")
-    _check("fp8_pack", load_library().fp8_pack(wp, code, lead[0] if lead else 1, rows, cols, qp, sp, _raw_stream(dev)))
+    _check("fp8_pack", load_library().fp8_pack(wp, code, lead[0] if lead else 1, rows, cols, qp, sp, _stream()))
     return q, scale
-
-
-def _result_type(y, dtype):
-    """The type of a product's result: the given tensor's, the one asked for, or bfloat16."""
-    if y is None:
-        return _torch().bfloat16 if dtype is None else dtype
-    if dtype is not None and y.dtype != dtype:
-        raise ValueError(f"y must be {dtype}, got {y.dtype}")
-    return y.dtype
-
-
-def _product_shapes(w, cols, q, lead):
-    """rows, m and the padded columns of a product, from its operands' shapes."""
-    kp = (cols + 127) // 128 * 128
-    ws, qs = getattr(w, "shape", ()), getattr(q, "shape", ())
-    if kp < 1 or len(ws) != lead + 2 or ws[-1] != kp or 0 in ws or len(qs) != 2 or qs[1] != kp or qs[0] < 1:
-        if cols < 1:
-            raise ValueError(f"cols must be at least 1, got {cols}")
-        if len(ws) != lead + 2 or ws[-1] != kp or 0 in ws:
-            raise ValueError(f"w must have shape [{'experts, ' * lead}rows, {kp}], got {tuple(ws)}")
-        _rows2d(q, kp, "q")
-    return ws[-2], qs[0], kp
 
 
 def fp8_gemm(w, w_scale, cols: int, q, q_scale, dtype=None, y=None):
     """fp8_pack weights [rows, cols] x fp8_quant activations [m, cols] -> y [m, rows] of
     `dtype` (float32, bfloat16, the default, or float16)."""
-    torch = _torch()
-    f8, f32 = torch.float8_e4m3fn, torch.float32
-    rows, m, kp = _product_shapes(w, cols, q, 0)
-    kb, nb = kp // 128, (rows + 127) // 128
-    ydtype = _result_type(y, dtype)
-    ycode = _dtype_code(ydtype, "y")
-    if not q.is_cuda:
-        _shape(w_scale, (nb, kb), "w_scale")
-        _shape(q_scale, (kb, m), "q_scale")
-        raise ValueError("q must be a CUDA/HIP tensor")
-    dev = _get_device()
-    wp = _operand(w, f8, (rows, kp), dev, "w")
-    wsp = _operand(w_scale, f32, (nb, kb), dev, "w_scale")
-    qp = _operand(q, f8, (m, kp), dev, "q")
-    qsp = _operand(q_scale, f32, (kb, m), dev, "q_scale")
-    y, yp = _result(y, ydtype, (m, rows), dev)
-    rc = (_lib or load_library()).fp8_gemm(wp, wsp, rows, cols, qp, qsp, m, yp, ycode, _raw_stream(dev))
-    if rc:
-        _check("fp8_gemm", rc)
-    return y
+    r = (_calls_module or _calls()).fp8_gemm(w, w_scale, cols, q, q_scale, dtype, y)
+    if type(r) is int:
+        _check("fp8_gemm", r)
+    return r
 
 
 def fp8_gemm_grouped(w, w_scale, cols: int, q, q_scale, offsets, row_ids=None, dtype=None, y=None):
@@ -698,33 +631,10 @@ def fp8_gemm_grouped(w, w_scale, cols: int, q, q_scale, offsets, row_ids=None, d
     rows]: rows offsets[e] .. offsets[e + 1] - 1 of y are expert e's product with
     activation rows row_ids[p] (rows p without row_ids, and then slots = m).  Rows of
     y outside every expert's range are not written."""
-    torch = _torch()
-    f8, f32, i32 = torch.float8_e4m3fn, torch.float32, torch.int32
-    rows, m, kp = _product_shapes(w, cols, q, 1)
-    experts, kb = w.shape[0], kp // FP8_BLOCK
-    ydtype = _result_type(y, dtype)
-    ycode = _dtype_code(ydtype, "y")
-    if not q.is_cuda:
-        _shape(offsets, (experts + 1,), "offsets")
-    slots = m
-    if row_ids is not None:
-        if getattr(row_ids, "ndim", 0) != 1 or row_ids.shape[0] < 1:
-            raise ValueError(f"row_ids must have shape [slots], got {tuple(getattr(row_ids, 'shape', ()))}")
-        slots = row_ids.shape[0]
-    _need_device(q, "q")
-    dev = _get_device()
-    wp = _operand(w, f8, (experts, rows, kp), dev, "w")
-    wsp = _operand(w_scale, f32, (experts, (rows + 127) // 128, kb), dev, "w_scale")
-    qp = _operand(q, f8, (m, kp), dev, "q")
-    qsp = _operand(q_scale, f32, (kb, m), dev, "q_scale")
-    op = _operand(offsets, i32, (experts + 1,), dev, "offsets")
-    rp = None if row_ids is None else _operand(row_ids, i32, (slots,), dev, "row_ids")
-    y, yp = _result(y, ydtype, (slots, rows), dev)
-    rc = (_lib or load_library()).fp8_gemm_grouped(wp, wsp, experts, rows, cols, qp, qsp, m, op, rp, slots, yp, ycode,
-                                                   _raw_stream(dev))
-    if rc:
-        _check("fp8_gemm_grouped", rc)
-    return y
+    r = (_calls_module or _calls()).fp8_gemm_grouped(w, w_scale, cols, q, q_scale, offsets, row_ids, dtype, y)
+    if type(r) is int:
+        _check("fp8_gemm_grouped", r)
+    return r
 
 
 class MoeRoute(NamedTuple):
@@ -735,7 +645,6 @@ class MoeRoute(NamedTuple):
     slots: object      # int32 [tokens, top]: where each pair went, -1 for none
 
 
-@functools.lru_cache(maxsize=256)
 def moe_route_workspace(tokens: int, experts: int, top: int) -> int:
     """Bytes of device workspace moe_route needs."""
     n = ctypes.c_int64()
@@ -746,50 +655,17 @@ def moe_route_workspace(tokens: int, experts: int, top: int) -> int:
 def moe_route(logits, top: int, renorm: bool = True, workspace=None) -> MoeRoute:
     """logits [tokens, experts] -> MoeRoute: the `top` largest logits of each token, their
     softmax weights (over the chosen with renorm, else over all) and the pairs sorted
-    by expert.  The results share one allocation."""
-    lp, code, stride, tokens, experts, dev = _row_strided(logits, "logits")
-    torch = _torch_module
-    need = moe_route_workspace(tokens, experts, top)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    wp = None
-    if workspace is not None:
-        _at_least(workspace, need, "workspace")
-        wp = _operand(workspace, torch.uint8, workspace.shape, dev, "workspace")
-    pairs = tokens * top
-    # one buffer: ids, slots, row_ids, weights, offsets
-    base = torch.empty(4 * pairs + experts + 1, dtype=torch.int32, device=dev)
-    p = base.data_ptr()
-    rc = (_lib or load_library()).moe_route(
-        lp, code, tokens, experts, stride, top, 1 if renorm else 0, p, p + 12 * pairs, p + 16 * pairs, p + 8 * pairs,
-        p + 4 * pairs, wp, need, _raw_stream(dev))
-    if rc:
-        _check("moe_route", rc)
-    ids, slots, row_ids, weights, offsets = base.split((pairs, pairs, pairs, pairs, experts + 1))
-    return MoeRoute(ids.view(tokens, top), weights.view(torch.float32).view(tokens, top), offsets, row_ids,
-                    slots.view(tokens, top))
+    by expert."""
+    r = (_calls_module or _calls()).moe_route(logits, top, renorm, workspace)
+    if type(r) is int:
+        _check("moe_route", r)
+    return MoeRoute._make(r)
 
 
 def moe_combine(y, slots, weights, out=None):
     """out[t] = sum_j weights[t, j] * y[slots[t, j]] (slots below 0 are left out): y [rows, d],
     slots int32 and weights fp32 [tokens, top] -> out [tokens, d] of y's type."""
-    torch = _torch()
-    if getattr(y, "ndim", 0) != 2 or y.numel() < 1:
-        raise ValueError(f"y must have shape [rows, d], got {tuple(getattr(y, 'shape', ()))}")
-    if getattr(slots, "ndim", 0) != 2 or slots.numel() < 1:
-        raise ValueError(f"slots must have shape [tokens, top], got {tuple(getattr(slots, 'shape', ()))}")
-    code = _dtype_code(y.dtype, "y")
-    tokens, top = slots.shape
-    rows, d = y.shape
-    if not y.is_cuda:
-        _shape(weights, (tokens, top), "weights")
-    _need_device(y, "y")
-    dev = _get_device()
-    yp = _operand(y, y.dtype, (rows, d), dev, "y")
-    sp = _operand(slots, torch.int32, (tokens, top), dev, "slots")
-    wp = _operand(weights, torch.float32, (tokens, top), dev, "weights")
-    out, op = _result(out, y.dtype, (tokens, d), dev, "out")
-    rc = (_lib or load_library()).moe_combine(yp, code, rows, d, sp, wp, tokens, top, op, _raw_stream(dev))
-    if rc:
-        _check("moe_combine", rc)
-    return out
+    r = (_calls_module or _calls()).moe_combine(y, slots, weights, out)
+    if type(r) is int:
+        _check("moe_combine", r)
+    return r

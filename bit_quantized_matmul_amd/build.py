@@ -1,8 +1,10 @@
 """Build libbqm.so (the HIP kernels and the C ABI) for gfx950, in-tree.
 
 Usage: ``python -m bit_quantized_matmul_amd.build`` (also called by
-``__graft_entry__.build()``).  Every source under ``csrc/`` is compiled with
-hipcc for gfx950 only, then linked into ``bit_quantized_matmul_amd/libbqm.so``.
+``__graft_entry__.build()``).  Every HIP source under ``csrc/`` is compiled with
+hipcc for gfx950 only, then linked into ``bit_quantized_matmul_amd/libbqm.so``;
+``csrc/calls.cpp``, the binding's calls that are made for every token, is compiled
+with g++ against PyTorch's headers into ``bit_quantized_matmul_amd/_calls.so``.
 """
 from __future__ import annotations
 
@@ -10,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbqm.so")
+CALLS = os.path.join(PKG, "_calls.so")
 ARCH = "gfx950"
 
 COMMON = [
@@ -57,12 +61,29 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_calls() -> None:
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    tmp = CALLS + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{d}" for d in (INCLUDE, *include_paths(), sysconfig.get_paths()["include"])),
+           os.path.join(CSRC, "calls.cpp"), "-o", tmp, *(f"-L{d}" for d in library_paths()),
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on calls.cpp:\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sources()
     jobs = min(len(srcs), max(1, min(8, os.cpu_count() or 1)))
     with ThreadPoolExecutor(max_workers=jobs) as ex:
+        calls = ex.submit(_build_calls)
         objs = list(ex.map(_compile, srcs))
+        calls.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -153,3 +153,34 @@ def test_binding_refuses_shapes_types_and_devices():
         B.moe_combine(x, torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, 3))
     with pytest.raises(ValueError, match="CUDA"):
         B.moe_route(x, 2)
+
+
+def test_calls_fail_loudly_without_the_extension(monkeypatch, tmp_path):
+    monkeypatch.setattr(B, "_CALLS_PATH", str(tmp_path / "missing.so"))
+    monkeypatch.setattr(B, "_calls_module", None)
+    with pytest.raises(RuntimeError, match="missing"):
+        B.moe_route(torch.zeros(4, 8), 2)
+
+
+def test_calls_refuse_what_is_no_tensor_or_argument():
+    q, qs = torch.zeros(4, 256, dtype=torch.float8_e4m3fn), torch.zeros(2, 4)
+    with pytest.raises(ValueError, match="w must be"):
+        B.fp8_gemm(None, None, 256, q, qs)
+    with pytest.raises(ValueError, match="x must be"):
+        B.fp8_quant([1.0])
+    with pytest.raises(ValueError, match="cols must be at least 1"):
+        B.fp8_gemm(q, qs, 0, q, qs)
+    with pytest.raises(TypeError):
+        B.fp8_gemm(q, qs, "many", q, qs)
+    with pytest.raises(ValueError, match="out of range"):
+        B.fp8_gemm(q, qs, 1 << 40, q, qs)
+    with pytest.raises(ValueError, match="dtype must be a torch.dtype"):
+        B.fp8_gemm(torch.zeros(4, 256, dtype=torch.float8_e4m3fn), torch.zeros(1, 2), 256, q, qs, dtype=7)
+    with pytest.raises(ValueError, match="rows must be contiguous"):
+        B.fp8_quant(torch.zeros(8, 4).t())
+    with pytest.raises(ValueError, match="rows must not overlap"):
+        B.fp8_quant(torch.zeros(64).as_strided((4, 16), (8, 1)))
+    with pytest.raises(ValueError, match="must not be empty"):
+        B.fp8_quant(torch.zeros(0, 16))
+    with pytest.raises(ValueError, match="gate and up"):
+        B.fp8_quant(torch.zeros(2, 15), swiglu=True)
