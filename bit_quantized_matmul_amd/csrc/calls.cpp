@@ -80,7 +80,9 @@ int type_code(at::ScalarType s, const char *name) {
   }
 }
 
-int current_device() {
+// The current device, asked for only with a tensor on some device (there may be none).
+int current_device(const at::Tensor &t, const char *name) {
+  if (!t.is_cuda()) throw Refused{std::string(name) + " must be a CUDA/HIP tensor"};
   PyObject *r = PyObject_CallNoArgs(g_device);
   if (!r) throw python_error();
   const long d = PyLong_AsLong(r);
@@ -136,7 +138,6 @@ int64_t strided_rows(const at::Tensor &t, const char *name) {
   if (t.size(0) > 1 && t.stride(0) < t.size(1))
     throw Refused{std::string(name) + "'s rows must not overlap (strides " + shown(t.strides()) + ")"};
   if (t.size(0) > INT32_MAX || t.size(1) > INT32_MAX) throw Refused{std::string(name) + " is too large"};
-  if (!t.is_cuda()) throw Refused{std::string(name) + " must be a CUDA/HIP tensor"};
   return t.stride(0);
 }
 
@@ -148,7 +149,7 @@ PyObject *quant(PyObject *const *a) {
   const int64_t m = x.size(0), width = x.size(1);
   if (swiglu && width % 2) throw Refused{"x must hold gate and up columns, got " + std::to_string(width)};
   const int64_t k = swiglu ? width / 2 : width, kb = (k + 127) / 128;
-  const int dev = current_device();
+  const int dev = current_device(x, "x");
   on_device(x, dev, "x");
   const at::Tensor q = result(a[2], {m, kb * 128}, at::kFloat8_e4m3fn, dev, "q");
   const at::Tensor s = result(a[3], {kb, m}, at::kFloat, dev, "scale");
@@ -206,8 +207,7 @@ Product product(PyObject *const *a, bool grouped, PyObject *dtype, PyObject *y) 
 int operands(Product &p, PyObject *const *a) {
   const at::Tensor &w = THPVariable_Unpack(a[0]), &ws = THPVariable_Unpack(a[1]);
   const at::Tensor &q = THPVariable_Unpack(a[3]), &qs = THPVariable_Unpack(a[4]);
-  if (!q.is_cuda()) throw Refused{"q must be a CUDA/HIP tensor"};
-  const int dev = current_device();
+  const int dev = current_device(q, "q");
   p.w = address(w, at::kFloat8_e4m3fn, dev, "w");
   p.ws = address(ws, at::kFloat, dev, "w_scale");
   p.q = address(q, at::kFloat8_e4m3fn, dev, "q");
@@ -255,10 +255,10 @@ PyObject *route(PyObject *const *a) {
   const int64_t stride = strided_rows(x, "logits");
   const int64_t tokens = x.size(0), experts = x.size(1);
   const int top = integer(a[1], "top");
+  const int dev = current_device(x, "logits");
   int64_t need = 0;
   int rc = p_moe_route_workspace((int)tokens, (int)experts, top, &need);
   if (rc) return code(rc);
-  const int dev = current_device();
   on_device(x, dev, "logits");
   at::Tensor ws;
   if (a[3] != Py_None) {
@@ -291,8 +291,7 @@ PyObject *combine(PyObject *const *a) {
     throw Refused{"slots must have shape [tokens, top], got " + shown(slots.sizes())};
   shape(weights, slots.sizes(), "weights");
   const int type = type_code(y.scalar_type(), "y");
-  if (!y.is_cuda()) throw Refused{"y must be a CUDA/HIP tensor"};
-  const int dev = current_device();
+  const int dev = current_device(y, "y");
   const void *yp = address(y, y.scalar_type(), dev, "y"), *sp = address(slots, at::kInt, dev, "slots"),
              *wp = address(weights, at::kFloat, dev, "weights");
   const at::Tensor out = result(a[3], {slots.size(0), y.size(1)}, y.scalar_type(), dev, "out");
