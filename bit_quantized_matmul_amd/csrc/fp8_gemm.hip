@@ -150,12 +150,6 @@ __device__ __forceinline__ int token_of(const Fp8Args &A, int p) {
   return t < 0 ? 0 : t >= A.m ? A.m - 1 : t;
 }
 
-// 16 bytes of results.
-template <typename Y>
-struct Pack {
-  Y v[16 / sizeof(Y)];
-};
-
 // Four neighbouring results of row p from column r on.
 template <typename Y>
 __device__ __forceinline__ void store4(Y *y, const Fp8Args &A, int p, int r, f32x4_t v) {
@@ -302,6 +296,23 @@ __device__ __forceinline__ void stage_scales(const float *base, uint32_t off, ui
 template <int N>
 __device__ __forceinline__ void wait_and_meet() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// kTurn tokens' results from LDS (kRow bytes each, 16-byte piece c of token t at c ^ t) to
+// y's rows from p0 and columns from r0 on, a unit U a lane and neighbouring lanes side by
+// side; rows from p1 and columns past the matrix are left out.
+template <typename U, typename Y, int kTurn, int kRow>
+__device__ __forceinline__ void store_turned(const uint8_t *from, Y *y, const Fp8Args &A, int p0, int p1, int r0,
+                                             int lane) {
+  constexpr int kUnits = kRow / (int)sizeof(U), kPieces = kRow / 16;
+  static_assert(64 % kUnits == 0, "a wave stores whole tokens");
+#pragma unroll
+  for (int i = 0; i < kTurn * kUnits / 64; ++i) {
+    const int tt = i * (64 / kUnits) + lane / kUnits, byte = lane % kUnits * (int)sizeof(U);
+    const U v = *reinterpret_cast<const U *>(from + tt * kRow + (((byte >> 4) ^ (tt & (kPieces - 1))) << 4) + (byte & 15));
+    const int p = p0 + tt, r = r0 + byte / (int)sizeof(Y);
+    if (p < p1 && r < A.rows) *reinterpret_cast<U *>(y + (int64_t)p * A.rows + r) = v;
+  }
 }
 
 template <typename Y, int BM, int BN, int WM, int WN, int NS, bool kNative>
@@ -496,12 +507,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args A, Y 
   // whole stretches of TN x 32 rows, 16 bytes a lane.  Piece c of token t lies at c ^ t,
   // modulo the pieces.  (4096 x 4096 x 2048: 71.5 us stored as they are, 62.7 so; with
   // the 8-bit instructions 49.4 and 38.6.)
-  constexpr int kRow = TN * 32 * (int)sizeof(Y), kPieces = kRow / 16, kElems = 16 / (int)sizeof(Y);
+  constexpr int kRow = TN * 32 * (int)sizeof(Y), kPieces = kRow / 16;
   constexpr int kTurn = NW * 32 * kRow <= kStage ? 32 : 16;
   static_assert(NW * kTurn * kRow <= kStage, "a buffer holds every wave's tokens");
   typedef Y yx4 __attribute__((ext_vector_type(4)));
   uint8_t *mine = lds + at + wave * kTurn * kRow;
-  const bool whole = A.rows % kElems == 0 && ((uintptr_t)y & 15u) == 0;
+  // the widest unit that every row's start is a multiple of
+  const uint64_t align = (uint64_t)A.rows * sizeof(Y) | (uintptr_t)y;
+  const int unit = (align & 15u) == 0 ? 16 : (align & 3u) == 0 ? 4 : 2;
 #pragma unroll
   for (int h = 0; h < TM * 32 / kTurn; ++h) {
     const int f = h * kTurn / 32, first = h * kTurn % 32;        // tokens [first, first + kTurn) of fragment f
@@ -517,22 +530,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args A, Y 
         *reinterpret_cast<yx4 *>(mine + (row - first) * kRow + (((o >> 4) ^ (row & (kPieces - 1))) << 4) + (o & 15)) = v;
       }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-    for (int i = 0; i < kTurn * kPieces / 64; ++i) {
-      const int tt = i * (64 / kPieces) + lane / kPieces, c = lane % kPieces;
-      const u32x4_t v = *reinterpret_cast<const u32x4_t *>(mine + tt * kRow + ((c ^ (tt & (kPieces - 1))) << 4));
-      const int p = t.p0 + (wm * TM + f) * 32 + first + tt, r = t.n0 + wn * TN * 32 + c * kElems;
-      if (p >= t.p1 || r >= A.rows) continue;
-      Y *o = y + (int64_t)p * A.rows + r;
-      if (whole) {
-        *reinterpret_cast<u32x4_t *>(o) = v;
-      } else {
-        const auto e = __builtin_bit_cast(Pack<Y>, v);
-#pragma unroll
-        for (int j = 0; j < kElems; ++j)
-          if (r + j < A.rows) o[j] = e.v[j];
-      }
-    }
+    const int p0 = t.p0 + (wm * TM + f) * 32 + first, r0 = t.n0 + wn * TN * 32;
+    if (unit == 16) store_turned<u32x4_t, Y, kTurn, kRow>(mine, y, A, p0, t.p1, r0, lane);
+    else if (sizeof(Y) == 4 || unit == 4) store_turned<uint32_t, Y, kTurn, kRow>(mine, y, A, p0, t.p1, r0, lane);
+    else if constexpr (sizeof(Y) == 2) store_turned<uint16_t, Y, kTurn, kRow>(mine, y, A, p0, t.p1, r0, lane);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
 }
