@@ -92,6 +92,18 @@ __device__ __forceinline__ void place_tile(int l, int mt, int nt, int *mi, int *
   *ni = in / h;
 }
 
+// The sum of `v` over the lanes up to this one, by moves between lanes' registers: within
+// rows of 16, then a row's last lane to the row after it, then lane 31 to the upper half.
+__device__ __forceinline__ int wave_prefix(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);      // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);      // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);      // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);      // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);      // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);      // row_bcast:31
+  return v;
+}
+
 // The tile of workgroup `bid`; false past the last one.  Every wave searches the
 // expert for itself, 64 experts at a time.
 template <int BM, int BN>
@@ -114,11 +126,7 @@ __device__ __forceinline__ bool find_tile(const Fp8Args &A, int bid, Tile *t) {
         lo = e < A.experts ? clamp_off(A, e) : 0;
         hi = e < A.experts ? max(lo, clamp_off(A, e + 1)) : 0;
         inc = (hi - lo + BM - 1) / BM;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-          const int u = __shfl_up(inc, o, 64);
-          if (lane >= o) inc += u;
-        }
+        inc = wave_prefix(inc);
       }
       const int sum = __builtin_amdgcn_readlane(inc, 63);
       if (pass == 1 && want < (before + sum) * nt) {
