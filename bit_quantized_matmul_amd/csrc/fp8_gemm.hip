@@ -10,7 +10,7 @@
 //    codes an instruction) and the fp16 matrix instructions sum their products in fp32.
 //    Every result in fp32, every row of fewer than 32 blocks, every small product.
 //  * by the 8-bit matrix instructions, at twice the rate and without conversions
-//    (4096 x 14336 x 4096: 268 against 403 us).  They keep, of each 8 products, only the 13
+//    (4096 x 14336 x 4096: 256 against 400 us).  They keep, of each 8 products, only the 13
 //    bits below the largest one: measured, 4e-5 of the result's norm where a few
 //    columns are 30 times the others, which is how activations are, and 2e-5 without.
 //    A result in 16 bits is rounded by up to 2^-8 (bf16) or 2^-11 (fp16) of itself, but one
@@ -90,18 +90,6 @@ __device__ __forceinline__ void place_tile(int l, int mt, int nt, int *mi, int *
   const int in = l - band * 8 * nt;
   *mi = band * 8 + in % h;
   *ni = in / h;
-}
-
-// The sum of `v` over the lanes up to this one, by moves between lanes' registers: within
-// rows of 16, then a row's last lane to the row after it, then lane 31 to the upper half.
-__device__ __forceinline__ int wave_prefix(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);      // row_shr:1
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);      // row_shr:2
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);      // row_shr:4
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);      // row_shr:8
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);      // row_bcast:15
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);      // row_bcast:31
-  return v;
 }
 
 // The tile of workgroup `bid`; false past the last one.  Every wave searches the
@@ -275,7 +263,7 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Args A, Y *__res
 // operands' tiles and scales go to LDS without passing through registers, into one of
 // NS buffers while others are multiplied.  A tile's rows are 128 bytes; chunk c of
 // row r is stored at chunk c ^ ((r >> 1) & 7), so that the 16 rows a fragment load
-// touches at one chunk lie in 16 different groups of four banks (no conflicts counted).
+// touches at one chunk lie in 16 different groups of four banks (the loads counted none).
 // They are buffer loads: the next block costs one scalar addition, where flat addresses
 // cost a 64-bit vector addition a load.
 

@@ -239,12 +239,7 @@ __device__ void finish(const RouteArgs &A, int chunk, int pairs, Ids ids, int32_
   if (t < A.experts) counts[t] = u32x4_t{0, 0, 0, 0};
   // exclusive prefix of total over the experts: thread t holds expert t
   const int mine = t < A.experts ? total[t] : 0;
-  int inc = mine;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(inc, o, 64);
-    if (lane >= o) inc += u;
-  }
+  const int inc = wave_prefix(mine);
   if (lane == 63) wsum[wave] = inc;
   __syncthreads();
   int add = 0, all = 0;
