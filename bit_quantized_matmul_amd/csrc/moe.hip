@@ -34,7 +34,7 @@ struct RouteArgs {
   int chunk_tokens, chunks;
 };
 
-// Reductions over 16 consecutive lanes (DPP row rotations) or the wave.
+// Reductions over 16 consecutive lanes (DPP row rotations) or the wave (then swaps of rows).
 template <int CTRL>
 __device__ __forceinline__ int row_move(int v) {
   return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xF, 0xF, false);
@@ -47,8 +47,10 @@ __device__ __forceinline__ int lanes_reduce(int v, F op) {
   v = op(v, row_move<0x124>(v));
   v = op(v, row_move<0x128>(v));
   if constexpr (LANES == 64) {
-    v = op(v, __shfl_xor(v, 16, 64));
-    v = op(v, __shfl_xor(v, 32, 64));
+    auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);     // rows 0, 0, 2, 2 and 1, 1, 3, 3
+    v = op((int)s[0], (int)s[1]);
+    s = __builtin_amdgcn_permlane32_swap(v, v, false, false);          // the lower half twice, the upper twice
+    v = op((int)s[0], (int)s[1]);
   }
   return v;
 }
@@ -72,7 +74,7 @@ __device__ __forceinline__ int lanes_min(int v) {
   return lanes_reduce<LANES>(v, [](int a, int b) { return min(a, b); });
 }
 
-// Sorts N = 4 or 16 keys, largest first: Batcher's odd-even merge sort.
+// Sorts N = 4, 8 or 16 keys, largest first: Batcher's odd-even merge sort.
 template <int N>
 __device__ __forceinline__ void sort_keys(uint32_t (&k)[N]) {
 #pragma unroll
@@ -357,17 +359,23 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs A)
   finish(A, chunk, n * A.top, A.ids + (int64_t)t0 * A.top, before, total);
 }
 
-// Tokens of a chunk: at most kMaxChunks chunks, and counts that fit 16 bits.
-int chunk_tokens(int tokens) {
-  int c = kChunkTokens;
-  while ((int64_t)c * kMaxChunks < tokens && c < 32768) c *= 2;
+// Tokens of a chunk: at most kMaxChunks chunks, and counts that fit 16 bits.  Past 256 experts
+// a wave chooses for one token at a time, a chunk is one token a wave, and half as many
+// chunks read all counts, which are longer (us, 4096 tokens of 512, 10 each: 38 with 64 tokens a
+// chunk, 22 with 16).
+int chunk_tokens(int tokens, int experts) {
+  const bool wide = experts > 256;
+  int c = wide ? kRouteThreads / 64 : kChunkTokens;
+  while ((int64_t)c * (wide ? kMaxChunks / 2 : kMaxChunks) < tokens && c < 32768) c *= 2;
   return c;
 }
 
 template <typename T>
 hipError_t route_t(RouteArgs A, hipStream_t s) {
   if (A.experts <= 64) route_choose_kernel<T, 16, 4><<<A.chunks, kRouteThreads, 0, s>>>(A);
+  else if (A.experts <= 128) route_choose_kernel<T, 16, 8><<<A.chunks, kRouteThreads, 0, s>>>(A);
   else if (A.experts <= 256) route_choose_kernel<T, 16, 16><<<A.chunks, kRouteThreads, 0, s>>>(A);
+  else if (A.experts <= 512) route_choose_kernel<T, 64, 8><<<A.chunks, kRouteThreads, 0, s>>>(A);
   else route_choose_kernel<T, 64, 16><<<A.chunks, kRouteThreads, 0, s>>>(A);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || A.chunks == 1) return e;
@@ -420,14 +428,14 @@ hipError_t combine_t(const T *y, int64_t rows, int d, const int32_t *slots, cons
 bool moe_route_supported(int experts, int top) { return experts <= kMaxExperts && top <= kMaxTop; }
 
 int64_t moe_route_scratch(int tokens, int experts) {
-  const int64_t c = chunk_tokens(tokens), chunks = (tokens + c - 1) / c;
+  const int64_t c = chunk_tokens(tokens, experts), chunks = (tokens + c - 1) / c;
   return chunks > 1 ? chunks * ((experts + 1) & ~1) * 2 : 0;
 }
 
 hipError_t launch_moe_route(const void *logits, int dtype, int tokens, int experts, int64_t stride, int top,
                             bool renorm, int32_t *ids, float *weights, int32_t *offsets, int32_t *row_ids,
                             int32_t *slots, void *scratch, hipStream_t s) {
-  const int c = chunk_tokens(tokens);
+  const int c = chunk_tokens(tokens, experts);
   const RouteArgs A{logits, stride, tokens, experts, top, renorm ? 1 : 0, ids, weights, offsets, row_ids, slots,
                     (uint16_t *)scratch, c, (int)(((int64_t)tokens + c - 1) / c)};
   if (dtype == BQM_F32) return route_t<float>(A, s);

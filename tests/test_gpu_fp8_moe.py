@@ -333,6 +333,13 @@ def test_route(tokens, experts, top):
                         f"{tokens}x{experts} top {top} {dtype}")
 
 
+# each number of logits a lane, and chunks of one token a wave, of two, and the last one ragged
+@pytest.mark.parametrize("tokens,experts,top", [(16, 512, 10), (17, 512, 10), (4097, 513, 6), (4096, 384, 12), (700, 128, 8),
+                                                (700, 129, 8)])
+def test_route_many_experts(tokens, experts, top):
+    test_route(tokens, experts, top)
+
+
 @pytest.mark.parametrize("tokens", [6, 130])
 def test_route_masks_ties_and_extremes(tokens):
     rng = np.random.default_rng(tokens)
