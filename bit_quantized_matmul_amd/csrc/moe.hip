@@ -414,13 +414,22 @@ __global__ __launch_bounds__(256) void combine_kernel(const T *__restrict__ y, i
     if (kVec || c + i < d) o[i] = from_f32<T>(acc[i]);
 }
 
+// A grid of 2^32 threads or more wraps, without an error: 2^23 tokens a launch.
 template <typename T>
 hipError_t combine_t(const T *y, int64_t rows, int d, const int32_t *slots, const float *weights, int tokens,
                      int top, T *out, hipStream_t s) {
-  const dim3 grid(tokens, (d + 2047) / 2048);
-  if (d % 8 == 0) combine_kernel<T, true><<<grid, 256, 0, s>>>(y, rows, d, slots, weights, top, out);
-  else combine_kernel<T, false><<<grid, 256, 0, s>>>(y, rows, d, slots, weights, top, out);
-  return hipGetLastError();
+  constexpr int kTokens = 1 << 23;
+  for (int64_t t = 0; t < tokens; t += kTokens) {
+    const dim3 grid((unsigned)(tokens - t < kTokens ? tokens - t : kTokens), (d + 2047) / 2048);
+    const int32_t *sl = slots + t * top;
+    const float *w = weights + t * top;
+    T *o = out + t * d;
+    if (d % 8 == 0) combine_kernel<T, true><<<grid, 256, 0, s>>>(y, rows, d, sl, w, top, o);
+    else combine_kernel<T, false><<<grid, 256, 0, s>>>(y, rows, d, sl, w, top, o);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace

@@ -91,3 +91,19 @@ def test_large_products_sum_in_fp32(sizes, n, k, signs):
             z = product(dtype)
             off = int((z != y.to(dtype)).sum())
             assert off == 0, f"{dtype}, gather {gather}: {off} of {z.numel()} are not the fp32 result rounded"
+
+# ------------------------------------------------------------------ tokens
+
+def test_combine_more_tokens_than_a_launch():
+    """2^24 tokens and a few: one workgroup each would be 2^32 threads."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    tokens, d, rows = (1 << 24) + 5, 8, 1000
+    y = torch.randn(rows, d, device=DEV, generator=g).bfloat16()
+    slots = torch.randint(-1, rows, (tokens, 1), device=DEV, generator=g, dtype=torch.int32)
+    weights = torch.rand(tokens, 1, device=DEV, generator=g)
+    out = B.moe_combine(y, slots, weights)
+    for t0 in range(0, tokens, 1 << 22):
+        s, w = slots[t0:t0 + (1 << 22), 0].long(), weights[t0:t0 + (1 << 22)]
+        want = torch.where(s[:, None] >= 0, y[s.clamp(min=0)].float() * w, 0.0).bfloat16()
+        assert torch.equal(out[t0:t0 + (1 << 22)], want)
