@@ -159,13 +159,9 @@ int check_layout(const bqm_cq_layout *L) {
 
 int status_of(hipError_t e) { return e == hipSuccess ? BQM_OK : BQM_EDEVICE; }
 
-// E4M3 products: block counts and tile rows stay within a launch's second
-// grid dimension, and an expert's rows within 31 bits.
+// E4M3 calls: a tile's codes are found by 32-bit offsets from its first row, and rows,
+// experts and blocks stay within what one launch covers.
 constexpr int kMaxFp8Cols = 1 << 22, kMaxFp8Rows = 1 << 24, kMaxFp8Experts = 4096;
-// The smallest tiles (16 x 16) of a product are counted with 32 bits.
-bool fp8_tiles_fit(int m, int experts, int rows) {
-  return ((int64_t)m / 16 + 1 + experts) * (((int64_t)rows + 15) / 16) < (int64_t)1 << 31;
-}
 
 constexpr int64_t kMaxPairs = (int64_t)1 << 30;
 constexpr int kMaxCombineCols = 1 << 26;
@@ -531,7 +527,7 @@ int fp8_pack(const void *w, int dtype, int experts, int rows, int cols, uint8_t 
              bqm_stream_t stream) {
   if (!w || !q || !scale || experts < 1 || rows < 1 || cols < 1 || !known_dtype(dtype)) return BQM_EINVAL;
   if (experts > kMaxFp8Experts || cols > kMaxFp8Cols || rows > kMaxFp8Rows ||
-      (((int64_t)rows + 127) / 128) * (((int64_t)cols + 127) / 128) >= (int64_t)1 << 31)
+      (((int64_t)rows + 127) / 128) * (((int64_t)cols + 127) / 128) >= kMaxGroups256)
     return BQM_ENOTSUP;
   if (!aligned16(q) || ((uintptr_t)scale & 3u) || ((uintptr_t)w & (unsigned)(elem_size(dtype) - 1))) return BQM_EALIGN;
   int cus;
@@ -544,7 +540,7 @@ int fp8_gemm(const uint8_t *w, const float *w_scale, int rows, int cols, const u
              int m, void *y, int ydtype, bqm_stream_t stream) {
   if (!w || !w_scale || !q || !q_scale || !y || rows < 1 || cols < 1 || m < 1 || !known_dtype(ydtype))
     return BQM_EINVAL;
-  if (cols > kMaxFp8Cols || rows > kMaxFp8Rows || !fp8_tiles_fit(m, 0, rows)) return BQM_ENOTSUP;
+  if (cols > kMaxFp8Cols || rows > kMaxFp8Rows || !fp8_gemm_fits(rows, m, 0)) return BQM_ENOTSUP;
   if (!aligned16(w) || !aligned16(q) || ((uintptr_t)w_scale & 3u) || ((uintptr_t)q_scale & 3u) ||
       ((uintptr_t)y & (unsigned)(elem_size(ydtype) - 1)))
     return BQM_EALIGN;
@@ -560,7 +556,7 @@ int fp8_gemm_grouped(const uint8_t *w, const float *w_scale, int experts, int ro
   if (!w || !w_scale || !q || !q_scale || !offsets || !y || experts < 1 || rows < 1 || cols < 1 || m < 1 ||
       slots < 1 || !known_dtype(ydtype) || (!row_ids && slots > m))
     return BQM_EINVAL;
-  if (experts > kMaxFp8Experts || cols > kMaxFp8Cols || rows > kMaxFp8Rows || !fp8_tiles_fit(slots, experts, rows))
+  if (experts > kMaxFp8Experts || cols > kMaxFp8Cols || rows > kMaxFp8Rows || !fp8_gemm_fits(rows, slots, experts))
     return BQM_ENOTSUP;
   // gathered rows are addressed with 32-bit offsets from the first
   if (row_ids && (int64_t)m * (((int64_t)cols + 127) / 128 * 128) >= (int64_t)1 << 32) return BQM_ENOTSUP;

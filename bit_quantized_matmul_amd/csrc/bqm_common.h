@@ -159,6 +159,10 @@ hipError_t launch_fp8_quant(const void *x, int dtype, int m, int k, int64_t stri
                             float *scale, hipStream_t s);
 hipError_t launch_fp8_pack(const void *w, int dtype, int experts, int rows, int cols, uint8_t *q, float *scale,
                            hipStream_t s);
+// Workgroups of 256 that one launch takes along a dimension: a grid of 2^32 threads or
+// more wraps, without an error.
+constexpr int64_t kMaxGroups256 = 1 << 24;
+bool fp8_gemm_fits(int rows, int slots, int experts);   // experts 0: one matrix
 hipError_t launch_fp8_gemm(const uint8_t *w, const float *ws, int rows, int cols, const uint8_t *q, const float *qs,
                            int m, void *y, int ydtype, int num_cus, hipStream_t s);
 hipError_t launch_fp8_gemm_grouped(const uint8_t *w, const float *ws, int experts, int rows, int cols,

@@ -520,11 +520,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args A, Y 
 
 // Workgroups that cover every tile whatever the offsets are: an expert's rows take
 // at most one tile more than they fill.
-int64_t tiles(const Fp8Args &A, int bm, int bn) {
-  const int64_t nt = (A.rows + bn - 1) / bn;
-  const int64_t mt = A.offsets ? A.slots / bm + (A.experts < A.slots ? A.experts : A.slots) : (A.m + bm - 1) / bm;
-  return mt * nt;
+int64_t tiles(int rows, int slots, int experts, int bm, int bn) {
+  const int64_t nt = ((int64_t)rows + bn - 1) / bn;
+  return nt * (experts ? slots / bm + (experts < slots ? experts : slots) : ((int64_t)slots + bm - 1) / bm);
 }
+int64_t tiles(const Fp8Args &A, int bm, int bn) { return tiles(A.rows, A.slots, A.offsets ? A.experts : 0, bm, bn); }
+
+// rows a matrix has to multiply: exact for one matrix, the mean for experts
+int rows_each(int slots, int experts) { return experts ? (int)(((int64_t)slots + experts - 1) / experts) : slots; }
+constexpr int kManyRows = 96;             // from here on 128 x 128 tiles, see run
 
 template <typename Y, int MF, int NW, int kDepth>
 hipError_t stream(const Fp8Args &A, Y *y, hipStream_t s) {
@@ -549,8 +553,7 @@ hipError_t stream1(const Fp8Args &A, Y *y, int num_cus, hipStream_t s) {
 
 template <typename Y>
 hipError_t run(const Fp8Args &A, Y *y, int num_cus, hipStream_t s) {
-  // rows a matrix has to multiply: exact for one matrix, the mean for experts
-  const int per = A.offsets ? (A.slots + A.experts - 1) / A.experts : A.m;
+  const int per = rows_each(A.slots, A.offsets ? A.experts : 0);
   // few tiles: the smallest token tile that leaves none of them waiting for a CU (us at 64
   // tokens: 1024x4096 6.3 with 16 a tile, 4096x4096 12.4 with 64; 64 x 64 tiles 15.5, 16.1)
   if (tiles(A, 16, 16) <= num_cus) return stream1(A, y, num_cus, s);
@@ -559,7 +562,7 @@ hipError_t run(const Fp8Args &A, Y *y, int num_cus, hipStream_t s) {
   // many: 128 x 128 tiles, two workgroups a CU (us, 512 tokens of 14336x4096: 61, with 64 x 128
   // tiles 70; 64 matrices of 2048x2048 with 128 rows each: 106 against 114, with 96: 97
   // against 96)
-  if (per >= 96 && tiles(A, 128, 128) >= num_cus) return tile<Y, 128, 128, 2, 2, 2>(A, y, s);
+  if (per >= kManyRows && tiles(A, 128, 128) >= num_cus) return tile<Y, 128, 128, 2, 2, 2>(A, y, s);
   // experts' matrices, and more than 8 tokens of one, as soon as tiles fill most CUs: 64 x 128,
   // three blocks deep, or 64 x 64, four deep (us, 64 matrices of 2048x2048 with 1/4, 2, 8 and
   // 32 rows each: 64 x 128 15 / 43 / 54 / 61, 16 rows a workgroup 17 / 49 / 74 / 154; one matrix
@@ -584,6 +587,12 @@ hipError_t run_any(const Fp8Args &A, void *y, int ydtype, int num_cus, hipStream
 }
 
 }  // namespace
+
+// The most workgroups that run may launch; its other choices are for few tiles.
+bool fp8_gemm_fits(int rows, int slots, int experts) {
+  const int bm = rows_each(slots, experts) >= kManyRows ? 128 : 64;
+  return tiles(rows, slots, experts, bm, 128) < kMaxGroups256;
+}
 
 hipError_t launch_fp8_gemm(const uint8_t *w, const float *ws, int rows, int cols, const uint8_t *q, const float *qs,
                            int m, void *y, int ydtype, int num_cus, hipStream_t s) {

@@ -414,11 +414,11 @@ __global__ __launch_bounds__(256) void combine_kernel(const T *__restrict__ y, i
     if (kVec || c + i < d) o[i] = from_f32<T>(acc[i]);
 }
 
-// A grid of 2^32 threads or more wraps, without an error: 2^23 tokens a launch.
+// More tokens than a launch takes: half of that a launch.
 template <typename T>
 hipError_t combine_t(const T *y, int64_t rows, int d, const int32_t *slots, const float *weights, int tokens,
                      int top, T *out, hipStream_t s) {
-  constexpr int kTokens = 1 << 23;
+  constexpr int64_t kTokens = kMaxGroups256 / 2;
   for (int64_t t = 0; t < tokens; t += kTokens) {
     const dim3 grid((unsigned)(tokens - t < kTokens ? tokens - t : kTokens), (d + 2047) / 2048);
     const int32_t *sl = slots + t * top;

@@ -401,7 +401,7 @@ int fp8_quant(const void *x, int dtype, int m, int k, int64_t x_stride, int swig
 /* Quantize weights the same way, a block being 128 x 128.  w [device] `dtype`
  * [experts, rows, cols] contiguous; q [device] uint8 [experts, rows, 128 kb],
  * 16-byte aligned; scale [device] fp32 [experts, ceil(rows / 128), kb].
- * experts <= 4096, rows <= 2^24, cols <= 2^22, fewer than 2^31 blocks of an
+ * experts <= 4096, rows <= 2^24, cols <= 2^22, fewer than 2^24 blocks of an
  * expert (BQM_ENOTSUP past them). */
 int fp8_pack(const void *w, int dtype, int experts, int rows, int cols, uint8_t *q, float *scale,
              bqm_stream_t stream);
@@ -411,7 +411,7 @@ int fp8_pack(const void *w, int dtype, int experts, int rows, int cols, uint8_t 
  * is scaled in fp32, the blocks are added in fp32 and y [device] `ydtype`
  * [m, rows] is rounded once: a 16-bit y is the fp32 one rounded.  w and q 16-byte
  * aligned.  Codes 0x7F and 0xFF are NaN and make the sums that read them NaN.
- * Any m >= 1 with (m / 16 + 1) ceil(rows / 16) < 2^31, and the limits of fp8_pack
+ * Any m >= 1 with ceil(m / 128) ceil(rows / 128) < 2^24, and the limits of fp8_pack
  * (BQM_ENOTSUP). */
 int fp8_gemm(const uint8_t *w, const float *w_scale, int rows, int cols, const uint8_t *q, const float *q_scale,
              int m, void *y, int ydtype, bqm_stream_t stream);
@@ -428,7 +428,8 @@ int fp8_gemm(const uint8_t *w, const float *w_scale, int rows, int cols, const u
  * taken as the nearer end and row numbers outside [0, m) as an end of it, so
  * that no index leaves its buffer.  Without row_ids slots <= m (BQM_EINVAL); with
  * them m * 128 kb < 2^32 (BQM_ENOTSUP: rows are found by 32-bit offsets).
- * (slots / 16 + 1 + experts) ceil(rows / 16) < 2^31 (BQM_ENOTSUP). */
+ * (slots / t + min(experts, slots)) ceil(rows / 128) < 2^24 with t = 128 where the
+ * experts have at least 96 rows in the mean, else 64 (BQM_ENOTSUP). */
 int fp8_gemm_grouped(const uint8_t *w, const float *w_scale, int experts, int rows, int cols, const uint8_t *q,
                      const float *q_scale, int m, const int32_t *offsets, const int32_t *row_ids, int slots, void *y,
                      int ydtype, bqm_stream_t stream);
