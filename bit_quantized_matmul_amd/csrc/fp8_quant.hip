@@ -87,8 +87,10 @@ __device__ __forceinline__ void load8(const T *row, int c, int k, float (&v)[8])
 
 // silu(g) u = g / (1 + exp(-g)) u.  exp(-g) = 2^p with p = -g log2(e) in two parts, the
 // rounded product and what it lost; the quotient is one step from g times the
-// approximate reciprocal.  Each of the three is within about a unit.  Where 1 + exp(-g)
-// nears the end of the range (g < -69) and for infinities and NaN: library calls.
+// approximate reciprocal.  Each of the three is within about a unit.  From 69 on the quotient
+// is g.  Below -69, where exp(-g) may overflow and the value does not vanish, 1 + exp(-g) is
+// exp(-g), and g exp(g) u = (g h u) h with h = exp(g / 2) leaves the range only where the
+// value does.
 __device__ __forceinline__ void silu_mul8(float (&g)[8], const float (&u)[8]) {
   constexpr float kL = 0x1.715476p+0f, kLlo = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;   // log2(e) = kL + kLlo
   float q[8], far = 0.0f;
@@ -106,7 +108,12 @@ __device__ __forceinline__ void silu_mul8(float (&g)[8], const float (&u)[8]) {
   }
   if (!(far < 69.0f)) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = g[j] / (1.0f + expf(-g[j]));
+    for (int j = 0; j < 8; ++j) {
+      const float h = expf(0.5f * g[j]);
+      const float near = (g[j] >= 69.0f ? g[j] : q[j]) * u[j];
+      g[j] = g[j] < -69.0f ? g[j] * h * u[j] * h : near;
+    }
+    return;
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) g[j] = q[j] * u[j];

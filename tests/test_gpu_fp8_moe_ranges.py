@@ -107,3 +107,27 @@ def test_combine_more_tokens_than_a_launch():
         s, w = slots[t0:t0 + (1 << 22), 0].long(), weights[t0:t0 + (1 << 22)]
         want = torch.where(s[:, None] >= 0, y[s.clamp(min=0)].float() * w, 0.0).bfloat16()
         assert torch.equal(out[t0:t0 + (1 << 22)], want)
+
+# ------------------------------------------------------------------ gates
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_swiglu_of_far_negative_gates(dtype):
+    """silu(g) u where exp(-g) leaves fp32's range but the value does not.  exp(g / 2) within a
+    unit (2^-23), twice, and three products (2^-24 each): 3.5 x 2^-23, on a scale one more
+    rounding; the code as near to the quotient as half a step and both allow."""
+    rng = np.random.default_rng(4)
+    m, k = 24, 300
+    g = np.linspace(-140.0, -60.0, m)[:, None] - rng.random((m, k))
+    u = rng.standard_normal((m, k)) * np.exp(np.clip(-g - 60.0, 0.0, 80.0))
+    x = torch.from_numpy(np.concatenate([g, u], 1).astype(np.float32)).to(dtype)
+    q, s = B.fp8_quant(x.to(DEV), swiglu=True)
+    x = x.double().numpy()
+    v = np.zeros((m, 3 * 128))
+    v[:, :k] = x[:, :k] * np.exp(x[:, :k]) / (1.0 + np.exp(x[:, :k])) * x[:, k:]
+    a = np.abs(v).reshape(m, 3, 128).max(2)
+    assert a.min() > 2.0 ** -117                    # every block's scale is a normal number
+    want = (a / 448.0).T
+    assert np.all(np.abs(host(s) - want) <= 4 * 2.0 ** -23 * want)
+    ideal = v / np.repeat(want.T, 128, axis=1)
+    err = np.abs(of8.decode(host(q)) - ideal)
+    assert np.all(err <= np.maximum(np.abs(ideal), 2.0 ** -6) * 2.0 ** -4 * (1 + 2.0 ** -20) + 8 * 2.0 ** -23 * np.abs(ideal))
