@@ -152,6 +152,71 @@ __device__ __forceinline__ void store4(Y *y, const Fp8Args &A, int p, int r, f32
   }
 }
 
+// ------------------------------------------------------------------ scales whose product is far
+//
+// The kernels multiply a block's two scales with each other and then with the block's sum.
+// Where the product is no normal number although both are numbers other than 0, it
+// overflows, or loses bits that the sum would bring back.  Rows that may hold such a product are
+// looked at after they are stored, and those that do are computed once more, one code after the
+// other.  How a wave knows: a tile keeps the largest past_normal of its products (two
+// instructions a token and block; at most 0.5% of the time); the stream kernel, where that cost 5%
+// to 8%, looks at its results: an overflow leaves an infinity or a NaN, and bits lost below
+// 2^-149 of a scale are at most 2^-125 a block, which is below the rounding of
+// results from 2^-100 on.  (Applying one scale after the other in every block cost 2% to 8%.)
+
+// 0xFE000000 and more for 0, subnormals, infinities and NaN.
+__device__ __forceinline__ uint32_t past_normal(float s) { return (__float_as_uint(s) << 1) - 0x01000000u; }
+constexpr uint32_t kPast = 0xFE000000u;
+
+__device__ __forceinline__ bool product_far(float a, float b) {
+  constexpr int kNumber = 0x198;                               // the classes of normal and subnormal numbers
+  return past_normal(a * b) >= kPast && __builtin_amdgcn_classf(a, kNumber) && __builtin_amdgcn_classf(b, kNumber);
+}
+
+// acc + sum a b.  The exponents of a and b are shared out: sum times 2^h is exact, and that
+// times s leaves fp32's range only where the sum of the three does; past 2^180 either
+// way every sum but 0 does.
+__device__ __forceinline__ float add_scaled(float sum, float a, float b, float acc) {
+  const int e = min(max(__builtin_amdgcn_frexp_expf(a) + __builtin_amdgcn_frexp_expf(b), -180), 180), h = e >> 1;
+  const float s = ldexpf(__builtin_amdgcn_frexp_mantf(a) * __builtin_amdgcn_frexp_mantf(b), e - h);
+  return fmaf(ldexpf(sum, h), s, acc);
+}
+
+// The wave's N rows of y from p0 on (below p1), columns r0 .. r0 + R - 1 (of one scale block).
+template <typename Y, int N, int R>
+__device__ __forceinline__ void redo_far(const Fp8Args &A, Y *y, int e, int p0, int p1, int r0, int lane) {
+  if (p0 >= p1) return;
+  const float *ws = A.ws + ((int64_t)e * ((A.rows + kBlk - 1) / kBlk) + r0 / kBlk) * A.kb;
+  const float *qs = A.qs + token_of(A, min(p0 + lane % N, p1 - 1));
+  bool far = false;
+  for (int b = lane / N; b < A.kb; b += 64 / N) far |= product_far(qs[(int64_t)b * A.m], ws[b]);
+  uint64_t rows = __ballot(far);                               // bit i of any N: row p0 + i
+#pragma unroll
+  for (int n = 32; n >= N; n /= 2) rows |= rows >> n;
+  __threadfence();                                             // the rows' first stores come first
+  const int64_t kp = (int64_t)A.kb * kBlk;
+  const int r = r0 + lane;
+  const uint32_t *w = reinterpret_cast<const uint32_t *>(A.w + ((int64_t)e * A.rows + min(r, A.rows - 1)) * kp);
+  for (int i = 0; i < N && p0 + i < p1; ++i) {
+    if (!(rows >> i & 1)) continue;
+    const int tok = token_of(A, p0 + i);
+    const uint32_t *q = reinterpret_cast<const uint32_t *>(A.q + tok * kp);
+    float acc = 0.0f;
+    for (int b = 0; b < A.kb; ++b) {
+      float sum = 0.0f;
+      for (int j = b * (kBlk / 4); j < (b + 1) * (kBlk / 4); ++j) {
+        const int u = (int)w[j], v = (int)q[j];
+        sum = fmaf(__builtin_amdgcn_cvt_f32_fp8(u, 0), __builtin_amdgcn_cvt_f32_fp8(v, 0), sum);
+        sum = fmaf(__builtin_amdgcn_cvt_f32_fp8(u, 1), __builtin_amdgcn_cvt_f32_fp8(v, 1), sum);
+        sum = fmaf(__builtin_amdgcn_cvt_f32_fp8(u, 2), __builtin_amdgcn_cvt_f32_fp8(v, 2), sum);
+        sum = fmaf(__builtin_amdgcn_cvt_f32_fp8(u, 3), __builtin_amdgcn_cvt_f32_fp8(v, 3), sum);
+      }
+      acc = add_scaled(sum, A.qs[(int64_t)b * A.m + tok], ws[b], acc);
+    }
+    if (lane < R && r < A.rows) y[(int64_t)(p0 + i) * A.rows + r] = from_f32<Y>(acc);
+  }
+}
+
 // ------------------------------------------------------------------ few rows a matrix
 //
 // The weights are read once and bound the time.  A workgroup takes 16 weight
@@ -244,6 +309,11 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Args A, Y *__res
   for (int v = 1; v < NW; ++v) sum += red[v][wave][lane];
   const int p = t.p0 + wave * 16 + row;
   if (p < t.p1) store4(y, A, p, t.n0 + grp * 4, sum);
+  bool look = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) look |= !(fabsf(sum[i]) >= 0x1p-100f && fabsf(sum[i]) < INFINITY);
+  if (__builtin_expect(__ballot(look) != 0, 0))
+    redo_far<Y, 16, 16>(A, y, t.e, t.p0 + wave * 16, t.p1, t.n0, lane);
 }
 
 // ------------------------------------------------------------------ tiles
@@ -378,6 +448,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args A, Y 
   auto scale_of = [&](int at, int i) { return reinterpret_cast<const float *>(lds + at + kScale)[i]; };
   f32x16 acc[TN][TM] = {}, last = {};
   float s[TM], s_last = 0.0f;
+  uint32_t past = 0;                                           // the largest past_normal of the scales' products
   i32x4 rw[TN][4], rq[TM][4];
 #pragma unroll
   for (int i = 0; i < NS; ++i)
@@ -391,7 +462,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args A, Y 
     rq[0][j] = chunk(fq, j);
   }
 #pragma unroll
-  for (int f = 0; f < TM; ++f) s[f] = scale_of(0, (wm * TM + f) * 32 + row) * scale_of(0, BM);
+  for (int f = 0; f < TM; ++f) {
+    s[f] = scale_of(0, (wm * TM + f) * 32 + row) * scale_of(0, BM);
+    past = max(past, past_normal(s[f]));
+  }
   f16x8 qh[TM][8], wh[8];
   auto eighth = [](const i32x4 (&r)[4], int k) { return widen(r[k / 2][2 * (k & 1)], r[k / 2][2 * (k & 1) + 1]); };
   wh[0] = eighth(rw[0], 0);
@@ -463,7 +537,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args A, Y 
         rq[0][j] = rqn[j];
       }
 #pragma unroll
-      for (int f = 0; f < TM; ++f) s[f] = sn[f] * swn;
+      for (int f = 0; f < TM; ++f) {
+        s[f] = sn[f] * swn;
+        past = max(past, past_normal(s[f]));
+      }
     }
     at = nx;
   };
@@ -513,6 +590,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args A, Y 
     else if (sizeof(Y) == 4 || unit == 4) store_turned<uint32_t, Y, kTurn, kRow>(mine, y, A, p0, t.p1, r0, lane);
     else if constexpr (sizeof(Y) == 2) store_turned<uint16_t, Y, kTurn, kRow>(mine, y, A, p0, t.p1, r0, lane);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+  if (__builtin_expect(__ballot(past >= kPast) != 0, 0)) {
+#pragma unroll 1
+    for (int f = 0; f < TM; ++f)
+      redo_far<Y, 32, TN * 32>(A, y, t.e, t.p0 + (wm * TM + f) * 32, t.p1, t.n0 + wn * TN * 32, lane);
   }
 }
 

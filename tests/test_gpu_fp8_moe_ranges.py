@@ -131,3 +131,66 @@ def test_swiglu_of_far_negative_gates(dtype):
     ideal = v / np.repeat(want.T, 128, axis=1)
     err = np.abs(of8.decode(host(q)) - ideal)
     assert np.all(err <= np.maximum(np.abs(ideal), 2.0 ** -6) * 2.0 ** -4 * (1 + 2.0 ** -20) + 8 * 2.0 ** -23 * np.abs(ideal))
+
+# ------------------------------------------------------------------ scales
+
+# every kernel that the sizes choose between: 1, 2 and 4 fragments of tokens, 64 x 64, 64 x 128 and
+# 128 x 128 tiles; rows shorter and longer than the tiles' pipelines
+SCALED = [(3, 300, 384), (20, 300, 1100), (300, 300, 384), (300, 500, 1152), (70, 5001, 384), (70, 5001, 1152),
+          (129, 9000, 384), (129, 9000, 700), (1000, 4224, 300), (1000, 4224, 1152)]
+
+
+@pytest.mark.parametrize("m,n,k", SCALED)
+def test_products_of_scales_past_the_range(m, n, k):
+    """Scales whose product overflows (2^132) where the block's sum is small or 0, and is
+    subnormal (2^-143) where the sum brings the result back: as if the three were
+    multiplied exactly.  Beside gemm_tol a rounding more for the scaling in two steps, and
+    half a subnormal step for each block."""
+    rng = np.random.default_rng(m + n + k)
+    kb, nb = of8.blocks(k), of8.blocks(n)
+    q, w = np.zeros((m, kb * 128), dtype=np.uint8), np.zeros((n, kb * 128), dtype=np.uint8)
+    q[:, :k], w[:, :k] = normal_codes(rng, (m, k), 100.0), normal_codes(rng, (n, k), 100.0)
+    # by block modulo 3: scales of tokens (modulo 3) and of weight rows (even and odd blocks of 128)
+    ex = np.array([[72, 5, -75], [60, 0, -75], [-2, 3, -75]])[np.arange(kb) % 3][:, np.arange(m) % 3]
+    ew = np.array([[60, -60, 0], [-68, -68, -68]])[np.arange(nb) % 2][:, np.arange(kb) % 3]
+    # codes of a high block are the type's subnormals, and every other weight row is 0 there
+    cols = np.repeat(np.arange(kb) % 3 == 0, 128)
+    q[:, cols] &= 0x87
+    w[:, cols] &= 0x87
+    w[np.ix_(np.arange(n) % 2 == 0, cols)] = 0
+    qs = (np.exp2(ex.astype(np.float64)) * rng.uniform(1, 2, ex.shape)).astype(np.float32)
+    ws = (np.exp2(ew.astype(np.float64)) * rng.uniform(1, 2, ew.shape) * rng.choice([-1.0, 1.0], ew.shape)).astype(np.float32)
+    qs[0, m // 2] = 0.0
+    ref, mag = of8.gemm(w, ws, q, qs)
+    assert np.abs(ref).max() < 3.4e38
+    got = host(B.fp8_gemm(dev(w, F8), dev(ws), k, dev(q, F8), dev(qs), dtype=torch.float32))
+    assert np.all(np.isfinite(got)), f"{int((~np.isfinite(got)).sum())} results are not finite"
+    bound = (gemm_tol(k) + 2.0 ** -23) * mag + kb * 2.0 ** -149
+    worst = np.max(np.abs(got - ref) / bound)
+    assert worst <= 1.0, f"{worst:.3g} of the bound"
+    # the same rows as two experts' and gathered
+    off = dev(np.array([0, m // 3, m], dtype=np.int32))
+    two = torch.stack([dev(w)] * 2).view(F8)
+    ids = rng.permutation(m).astype(np.int32)
+    got = host(B.fp8_gemm_grouped(two, torch.stack([dev(ws)] * 2), k, dev(q, F8), dev(qs), off, row_ids=dev(ids),
+                                  dtype=torch.float32))
+    assert np.all(np.abs(got - ref[ids]) <= bound[ids])
+
+
+@pytest.mark.parametrize("m,n", [(2, 130), (300, 300), (70, 5001), (1000, 4224)])
+def test_scales_that_are_no_numbers(m, n):
+    """An infinite scale makes its token's results infinite or, where the sum is 0, NaN; a NaN
+    scale makes them NaN; other tokens are untouched."""
+    rng = np.random.default_rng(m)
+    k = 256
+    q, w = normal_codes(rng, (m, k), 100.0), normal_codes(rng, (n, k), 100.0)
+    w[5, :128] = 0
+    qs, ws = np.ones((2, m), dtype=np.float32), np.ones((of8.blocks(n), 2), dtype=np.float32)
+    args = dev(w, F8), dev(ws), k, dev(q, F8)
+    clean = host(B.fp8_gemm(*args, dev(qs), dtype=torch.float32))
+    qs[0, 0], qs[1, 1] = np.inf, np.nan
+    y = host(B.fp8_gemm(*args, dev(qs), dtype=torch.float32))
+    part, _ = of8.gemm(w[:, :128], ws[:, :1], q[:1, :128], np.ones((1, 1)))
+    with np.errstate(invalid="ignore"):
+        assert np.array_equal(y[0], part[0] * np.inf, equal_nan=True)
+    assert np.all(np.isnan(y[1])) and np.array_equal(y[2:], clean[2:])
