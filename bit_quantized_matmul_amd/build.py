@@ -2,9 +2,11 @@
 
 Usage: ``python -m bit_quantized_matmul_amd.build`` (also called by
 ``__graft_entry__.build()``).  Every HIP source under ``csrc/`` is compiled with
-hipcc for gfx950 only, then linked into ``bit_quantized_matmul_amd/libbqm.so``;
-``csrc/calls.cpp``, the binding's calls that are made for every token, is compiled
-with g++ against PyTorch's headers into ``bit_quantized_matmul_amd/_calls.so``.
+hipcc for gfx950 only, then linked into ``bit_quantized_matmul_amd/libbqm.so``.  That
+needs nothing else.  Then ``csrc/calls.cpp``, the binding's calls that are made for
+every token, becomes ``bit_quantized_matmul_amd/_calls.so``, with g++ and PyTorch's
+headers: without PyTorch it is left out, and a failure there leaves the library
+in place.
 """
 from __future__ import annotations
 
@@ -61,8 +63,12 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _build_calls() -> None:
-    import torch
+def _compile_calls() -> str | None:
+    """The extension under a temporary name; None without PyTorch."""
+    try:
+        import torch
+    except ImportError:
+        return None
     from torch.utils.cpp_extension import include_paths, library_paths
     tmp = CALLS + ".tmp"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
@@ -73,7 +79,7 @@ def _build_calls() -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on calls.cpp:\n{r.stderr}")
-    os.replace(tmp, CALLS)
+    return tmp
 
 
 def build(verbose: bool = True) -> str:
@@ -81,9 +87,8 @@ def build(verbose: bool = True) -> str:
     srcs = sources()
     jobs = min(len(srcs), max(1, min(8, os.cpu_count() or 1)))
     with ThreadPoolExecutor(max_workers=jobs) as ex:
-        calls = ex.submit(_build_calls)
+        calls = ex.submit(_compile_calls)                        # beside the library's sources
         objs = list(ex.map(_compile, srcs))
-        calls.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -92,6 +97,13 @@ def build(verbose: bool = True) -> str:
     os.replace(tmp, LIB)
     if verbose:
         print(f"built {LIB} from {len(srcs)} sources", file=sys.stderr)
+    if os.path.exists(CALLS):
+        os.remove(CALLS)                                         # an earlier library's
+    tmp = calls.result()
+    if tmp:
+        os.replace(tmp, CALLS)
+    else:
+        print("PyTorch is not installed: the binding's extension is left out", file=sys.stderr)
     return LIB
 
 
