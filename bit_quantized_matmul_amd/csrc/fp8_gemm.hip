@@ -224,7 +224,7 @@ __device__ __forceinline__ void redo_far(const Fp8Args &A, Y *y, int e, int p0, 
 // load operands straight into the matrix cores' registers, kDepth blocks ahead; the
 // waves' sums meet in LDS.  A lane loads the 16-byte chunks g and g + 4 of a row (g its
 // group of 16 lanes), so one load reads 64 neighbouring bytes of each of 16 rows.  One token
-// of 4096x4096: 6.2 us for 3.4 us of bytes, the rest an empty launch (1.7) and the chain
+// of 4096x4096: 5.6 us for 3.4 us of bytes, the rest an empty launch (1.7) and the chain
 // from tile to loads to sum; of 32768x4096: 30 us, 4.5 TB/s.
 template <typename Y, int MF, int NW, int kDepth>
 __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Args A, Y *__restrict__ y) {
@@ -435,7 +435,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args A, Y 
   // chain by 500 of the block's 2600 cycles).  Between a chain's steps the next step's
   // codes are widened, the sums of the chain before are scaled and added, and fragments and
   // scales of the chains ahead are read, the next block's first ones during the last
-  // (4096 x 14336 x 4096: 438 us with loads and reads at the block's start, 406 so; 256 x 4096 x 4096 on 64 x 64 tiles 20.3, 17.0).
+  // (4096 x 14336 x 4096: 438 us with loads and reads at the block's start, 406 so;
+  // 256 x 4096 x 4096 on 64 x 64 tiles 20.3, 17.0).
   constexpr int C = TN * TM, kMeet = TN > 1 ? (TN - 2) * TM + 1 : 0;
   constexpr int kEvery = 8 * (C - kMeet) / kLoads;           // steps a load
   static_assert(kEvery >= 1, "every load has a step");
@@ -641,9 +642,9 @@ hipError_t run(const Fp8Args &A, Y *y, int num_cus, hipStream_t s) {
   if (tiles(A, 16, 16) <= num_cus) return stream1(A, y, num_cus, s);
   if (tiles(A, 32, 16) <= num_cus) return stream<Y, 2, 8, 1>(A, y, s);
   if (tiles(A, 64, 16) <= num_cus) return stream<Y, 4, 8, 1>(A, y, s);
-  // many: 128 x 128 tiles, two workgroups a CU (us, 512 tokens of 14336x4096: 61, with 64 x 128
-  // tiles 70; 64 matrices of 2048x2048 with 128 rows each: 106 against 114, with 96: 97
-  // against 96)
+  // many: 128 x 128 tiles, two workgroups a CU (us, 512 tokens of 14336x4096: 62, with 64 x 128
+  // tiles 73; 300 tokens 50, 51; 64 matrices of 2048x2048 with 128 rows each: 86 against 98, with
+  // 96: 77 against 87)
   if (per >= kManyRows && tiles(A, 128, 128) >= num_cus) return tile<Y, 128, 128, 2, 2, 2>(A, y, s);
   // experts' matrices, and more than 8 tokens of one, as soon as tiles fill most CUs: 64 x 128,
   // three blocks deep, or 64 x 64, four deep (us, 64 matrices of 2048x2048 with 1/4, 2, 8 and

@@ -359,7 +359,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs A)
   finish(A, chunk, n * A.top, A.ids + (int64_t)t0 * A.top, before, total);
 }
 
-// Tokens of a chunk: at most kMaxChunks chunks, and counts that fit 16 bits.  Past 256 experts
+// Tokens of a chunk: at most kMaxChunks chunks, until a chunk has 32768 tokens (counts are 16
+// bits) and their number grows (past 2^24 tokens, 2^23 of many experts).  Past 256 experts
 // a wave chooses for one token at a time, a chunk is one token a wave, and half as many
 // chunks read all counts, which are longer (us, 4096 tokens of 512, 10 each: 38 with 64 tokens a
 // chunk, 22 with 16).
