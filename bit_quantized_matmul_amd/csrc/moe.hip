@@ -384,7 +384,9 @@ hipError_t route_t(RouteArgs A, hipStream_t s) {
   return hipGetLastError();
 }
 
-// One workgroup of 256 a token and 2048 columns, 8 columns a thread.
+// One workgroup of 256 a token and 2048 columns, 8 columns a thread: with 16-byte loads where
+// rows are whole groups of 8, else by elements (us, 8192 tokens of 8, bf16: 4096 columns 121,
+// 4100 306).
 template <typename T, bool kVec>
 __global__ __launch_bounds__(256) void combine_kernel(const T *__restrict__ y, int64_t rows, int d,
                                                       const int32_t *__restrict__ slots,
