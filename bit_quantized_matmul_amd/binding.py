@@ -27,6 +27,7 @@ EXPORTED = (
     "kmcu_header", "kmcu_tensor", "kmcu_find", "kmcu_upload", "kmcu_upload_data", "cq_gemv_f32_noalloc",
     "q4_0_gemv_a8", "q4_0_gemm_a8", "cq_gemv_lut", "q4_0_gemv_a8_f32",
     "fp8_quant", "fp8_pack", "fp8_gemm", "fp8_gemm_grouped", "moe_route_workspace", "moe_route", "moe_combine",
+    "moe_ffn_workspace", "moe_ffn", "rope", "kv_append", "kv_attention_workspace", "kv_attention",
 )
 KMCU_F32, KMCU_Q4 = 1, 2
 
@@ -118,6 +119,14 @@ def load_library() -> ctypes.CDLL:
         "moe_route_workspace": ([I, I, I, ctypes.POINTER(I64)], I),
         "moe_route": ([P, I, I, I, I64, I, I, P, P, P, P, P, P, I64, P], I),
         "moe_combine": ([P, I, I64, I, P, P, I, I, P, P], I),
+        "moe_ffn_workspace": ([I, I, I, I, I, ctypes.POINTER(I64)], I),
+        "moe_ffn": ([P, I, I, I, I64, P, I, I64, I, I, I, P, P, P, P, I, P, P, I64, P], I),
+        "rope": ([P, I, I, I, I, I64, I64, P, P, I, I, ctypes.c_float, I, P, I64, I64, P], I),
+        "kv_append": ([P, P, I, I, I, I, I64, I64, I64, I64, P, P, I, P, I64, I, P, P, I, I, ctypes.c_float,
+                       P, P, P, P, I, P], I),
+        "kv_attention_workspace": ([I, I, I, I, I, I, ctypes.POINTER(I64)], I),
+        "kv_attention": ([P, I, I, I, I, I64, I64, P, P, I, P, I64, I, P, P, P, P, I, I, ctypes.c_float, I, P, P,
+                          I64, P], I),
     }
     for name, (args, ret) in sig.items():
         fn = getattr(lib, name)
@@ -579,7 +588,8 @@ def _calls():
                                "`python -m bit_quantized_matmul_amd.build`")
         torch, lib = _torch(), load_library()
         from . import _calls as module
-        names = ("fp8_quant", "fp8_gemm", "fp8_gemm_grouped", "moe_route_workspace", "moe_route", "moe_combine")
+        names = ("fp8_quant", "fp8_gemm", "fp8_gemm_grouped", "moe_route_workspace", "moe_route", "moe_combine",
+                 "rope", "kv_append", "kv_attention_workspace", "kv_attention", "moe_ffn_workspace", "moe_ffn")
         module.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names},
                     torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
         _calls_module = module
@@ -668,4 +678,125 @@ def moe_combine(y, slots, weights, out=None):
     r = (_calls_module or _calls()).moe_combine(y, slots, weights, out)
     if type(r) is int:
         _check("moe_combine", r)
+    return r
+
+
+def moe_ffn_workspace(tokens: int, experts: int, top: int, hidden: int, ffn: int) -> int:
+    """Bytes of device workspace moe_ffn needs."""
+    n = ctypes.c_int64()
+    _check("moe_ffn_workspace", load_library().moe_ffn_workspace(tokens, experts, top, hidden, ffn, ctypes.byref(n)))
+    return n.value
+
+
+def moe_ffn(x, w13, w13_scale, w2, w2_scale, logits, top: int, renorm: bool = True, out=None, workspace=None):
+    """The expert layer of up to 32 tokens in two launches: x [tokens, hidden] (float32, bfloat16 or float16), fp8_pack
+    weights w13 [experts, 2 ffn, hidden] (gate rows, then up rows) and w2 [experts, hidden, ffn], router logits
+    [tokens, experts] -> out [tokens, hidden] of x's type: each token's `top` experts' silu(gate) * up rows through w2,
+    weighted as moe_route weighs them.  x is not quantized."""
+    r = (_calls_module or _calls()).moe_ffn(x, w13, w13_scale, w2, w2_scale, logits, top, renorm, out, workspace)
+    if type(r) is int:
+        _check("moe_ffn", r)
+    return r
+
+
+# ------------------------------------------ rotary positions, the paged 8-bit cache
+
+KV_PAGE = 64
+
+
+def rope_freqs(rotary: int, theta: float = 10000.0, kind: str = "none", factor: float = 1.0, context: int = 0,
+               low: float = 1.0, high: float = 32.0):
+    """Radians a position of the rotary / 2 pairs: theta ** (-2 i / rotary), as a float64 numpy array.
+
+    For contexts `factor` times as long as the `context` positions a model was trained on:
+    ``linear`` divides all of them by factor; ``base`` raises theta so that the last pair turns factor times slower and the
+    first as before; ``turns`` keeps the pairs with more than `high` turns in `context` positions, divides those
+    with fewer than `low` by factor and goes linearly in the number of turns between; ``pairs`` does the same
+    linearly in the pair's index."""
+    if rotary < 2 or rotary % 2:
+        raise ValueError(f"rotary must be even and at least 2, got {rotary}")
+    if kind not in ("none", "linear", "base", "turns", "pairs"):
+        raise ValueError(f"kind must be none, linear, base, turns or pairs, got {kind!r}")
+    if not theta > 0 or not factor > 0:
+        raise ValueError(f"theta and factor must be positive, got {theta} and {factor}")
+    i = np.arange(rotary // 2, dtype=np.float64)
+    if kind == "base" and rotary > 2:
+        theta *= factor ** (rotary / (rotary - 2.0))
+    f = theta ** (-2.0 * i / rotary)
+    if kind == "linear":
+        return f / factor
+    if kind in ("turns", "pairs"):
+        if context < 1 or not high > low:
+            raise ValueError(f"{kind} needs context and low < high, got {context}, {low} and {high}")
+        turns = context * f / (2.0 * np.pi)
+        if kind == "turns":
+            keep = (turns - low) / (high - low)
+        else:
+            at = lambda n: rotary * np.log(context / (2.0 * np.pi * n)) / (2.0 * np.log(theta))  # noqa: E731
+            first, last = max(np.floor(at(high)), 0.0), min(np.ceil(at(low)), rotary // 2 - 1.0)
+            keep = 1.0 - (i - first) / max(last - first, 1e-3)
+        keep = np.clip(keep, 0.0, 1.0)
+        return f * keep + f / factor * (1.0 - keep)
+    return f
+
+
+def rope(x, positions, freqs, interleaved: bool = False, mscale: float = 1.0, backward: bool = False, out=None):
+    """Rotary positions: x [tokens, heads, dim] (float32, bfloat16 or float16, tokens and heads may be strided), positions
+    int32 [tokens], freqs float64 [rotary / 2] radians a position (rope_freqs, on the device) -> x with its first
+    rotary columns turned and scaled by mscale: pairs (i, i + rotary / 2), or (2 i, 2 i + 1) with interleaved.  With
+    backward the gradient of x for a gradient x of the result.  out may be x."""
+    r = (_calls_module or _calls()).rope(x, positions, freqs, interleaved, mscale, backward, out)
+    if type(r) is int:
+        _check("rope", r)
+    return r
+
+
+class KvCache(NamedTuple):
+    k: object          # float8_e4m3fn [pages, heads, 64, dp]
+    v: object          # float8_e4m3fn [pages, heads, dp, 64]
+    k_scale: object    # fp32 [pages, heads]
+    v_scale: object    # fp32 [pages, heads]
+
+
+def kv_padded_dim(dim: int) -> int:
+    """Columns a head of `dim` takes in the cache."""
+    if not 1 <= dim <= 256:
+        raise ValueError(f"dim must be 1 .. 256, got {dim}")
+    return (dim + 31) // 32 * 32 if dim <= 128 else (dim + 63) // 64 * 64
+
+
+def kv_cache(pages: int, heads: int, dim: int, device="cuda") -> KvCache:
+    """An empty cache of `pages` pages of 64 tokens."""
+    torch = _torch()
+    dp = kv_padded_dim(dim)
+    codes = lambda *s: torch.zeros(s, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)  # noqa: E731
+    return KvCache(codes(pages, heads, KV_PAGE, dp), codes(pages, heads, dp, KV_PAGE),
+                   torch.zeros((pages, heads), device=device), torch.zeros((pages, heads), device=device))
+
+
+def kv_append(cache: KvCache, k, v, pages, lens, offsets=None, positions=None, freqs=None, interleaved: bool = False,
+              mscale: float = 1.0) -> None:
+    """Writes the newest keys and values into the cache: k, v [tokens, heads, dim] (strided as rope's), pages int32
+    [seqs, width], lens int32 [seqs] (positions of each sequence with the new ones), offsets int32 [seqs + 1]
+    (each sequence's rows of k and v; None: one a sequence).  With positions and freqs, k is turned as by rope."""
+    r = (_calls_module or _calls()).kv_append(*cache, pages, lens, offsets, k, v, positions, freqs, interleaved, mscale)
+    if r:
+        _check("kv_append", r)
+
+
+def kv_attention_workspace(tokens: int, seqs: int, heads: int, kv_heads: int, dim: int, width: int) -> int:
+    """Bytes of device workspace kv_attention needs."""
+    n = ctypes.c_int64()
+    _check("kv_attention_workspace",
+           load_library().kv_attention_workspace(tokens, seqs, heads, kv_heads, dim, width, ctypes.byref(n)))
+    return n.value
+
+
+def kv_attention(q, cache: KvCache, pages, lens, offsets=None, scale=None, window: int = 0, out=None, workspace=None):
+    """Attention of the newest tokens q [tokens, heads, dim] over the cache, causal: pages, lens and offsets as for
+    kv_append, scale dim ** -0.5 if not given, each token attends to the last `window` positions up to its own (0: to
+    all) -> out [tokens, heads, dim] of q's type.  heads is a multiple of the cache's."""
+    r = (_calls_module or _calls()).kv_attention(*cache, pages, lens, offsets, q, scale, window, out, workspace)
+    if type(r) is int:
+        _check("kv_attention", r)
     return r

@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "bqm_common.h"
+#include "kv_common.h"
 #include "lowp_types.h"
 
 namespace bqm {
@@ -48,6 +49,27 @@ int current_device(int *num_cus) {
 }
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+
+// limits of the cache's calls and the expert layer
+constexpr int kMaxRopeDim = 1024, kMaxKvHeads = 65535;
+constexpr int kMaxKvWidth = (1 << 25) - 1;           // pages of a sequence: positions below 2^31
+constexpr int kMaxMoeCols = 1 << 16;
+
+bool rotary_fits(int rotary, int dim) { return rotary >= 0 && rotary % 2 == 0 && rotary <= dim; }
+
+// Rows of `dim` elements, tokens and heads these strides apart, that do not overlap.
+bool separate(int tokens, int64_t t, int heads, int64_t h, int dim) {
+  if (tokens > 1 && t < dim) return false;
+  if (heads > 1 && h < dim) return false;
+  return tokens <= 1 || heads <= 1 || t >= (__int128)(heads - 1) * h + dim || h >= (__int128)(tokens - 1) * t + dim;
+}
+
+int check_batch(const KvBatch &B) {
+  if (!B.lens || !B.pages || B.seqs < 1 || B.tokens < 1 || B.width < 1 || B.count < 1) return BQM_EINVAL;
+  if ((B.seqs > 1 && B.stride < B.width) || (!B.offsets && B.tokens != B.seqs)) return BQM_EINVAL;
+  if (B.width > kMaxKvWidth) return BQM_ENOTSUP;
+  return ((uintptr_t)B.offsets | (uintptr_t)B.lens | (uintptr_t)B.pages) & 3u ? BQM_EALIGN : BQM_OK;
+}
 
 int index_bits_of(int bits) {
   switch (bits) {
@@ -605,6 +627,118 @@ int moe_combine(const void *y, int dtype, int64_t y_rows, int d, const int32_t *
   const int rc = current_device(&cus);
   if (rc) return rc;
   return status_of(launch_moe_combine(y, dtype, y_rows, d, slots, weights, tokens, top, out, (hipStream_t)stream));
+}
+
+int rope(const void *x, int dtype, int tokens, int heads, int dim, int64_t x_token_stride, int64_t x_head_stride,
+         const int32_t *positions, const double *freqs, int rotary, int interleaved, float mscale, int backward, void *y,
+         int64_t y_token_stride, int64_t y_head_stride, bqm_stream_t stream) {
+  if (!x || !y || !positions || !freqs || tokens < 1 || heads < 1 || dim < 1 || !known_dtype(dtype) ||
+      !rotary_fits(rotary, dim) || rotary < 2)
+    return BQM_EINVAL;
+  if (!separate(tokens, x_token_stride, heads, x_head_stride, dim) ||
+      !separate(tokens, y_token_stride, heads, y_head_stride, dim))
+    return BQM_EINVAL;
+  if (x == y && ((tokens > 1 && x_token_stride != y_token_stride) || (heads > 1 && x_head_stride != y_head_stride)))
+    return BQM_EINVAL;
+  if (dim > kMaxRopeDim || heads > kMaxKvHeads || tokens >= kMaxGroups256) return BQM_ENOTSUP;
+  const unsigned el = (unsigned)(elem_size(dtype) - 1);
+  if ((((uintptr_t)x | (uintptr_t)y) & el) || ((uintptr_t)positions & 3u) || ((uintptr_t)freqs & 7u)) return BQM_EALIGN;
+  int cus;
+  const int rc = current_device(&cus);
+  if (rc) return rc;
+  return status_of(launch_rope(x, dtype, tokens, heads, dim, x_token_stride, x_head_stride, positions, freqs, rotary,
+                               interleaved != 0, mscale, backward != 0, y, y_token_stride, y_head_stride, (hipStream_t)stream));
+}
+
+int kv_append(const void *k, const void *v, int dtype, int tokens, int heads, int dim, int64_t k_token_stride,
+              int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride, const int32_t *offsets,
+              const int32_t *lens, int seqs, const int32_t *pages, int64_t pages_stride, int width,
+              const int32_t *positions, const double *freqs, int rotary, int interleaved, float mscale, uint8_t *k_codes,
+              uint8_t *v_codes, float *k_scale, float *v_scale, int count, bqm_stream_t stream) {
+  if (!k || !v || !k_codes || !v_codes || !k_scale || !v_scale || heads < 1 || dim < 1 || !known_dtype(dtype))
+    return BQM_EINVAL;
+  if (!rotary_fits(rotary, dim) || (rotary && (!positions || !freqs))) return BQM_EINVAL;
+  if (!separate(tokens, k_token_stride, heads, k_head_stride, dim) ||
+      !separate(tokens, v_token_stride, heads, v_head_stride, dim))
+    return BQM_EINVAL;
+  const KvBatch B{offsets, lens, pages, pages_stride, seqs, tokens, width, count};
+  int rc = check_batch(B);
+  if (rc) return rc;
+  if (dim > kMaxKvDim || heads > kMaxKvHeads || kv_append_jobs(tokens, seqs) >= kMaxGroups256) return BQM_ENOTSUP;
+  const unsigned el = (unsigned)(elem_size(dtype) - 1);
+  if (!aligned16(k_codes) || !aligned16(v_codes) || (((uintptr_t)k | (uintptr_t)v) & el) ||
+      (((uintptr_t)k_scale | (uintptr_t)v_scale | (uintptr_t)positions) & 3u) || ((uintptr_t)freqs & 7u))
+    return BQM_EALIGN;
+  int cus;
+  rc = current_device(&cus);
+  if (rc) return rc;
+  return status_of(launch_kv_append(B, k, v, dtype, heads, dim, k_token_stride, k_head_stride, v_token_stride,
+                                    v_head_stride, positions, freqs, rotary, interleaved != 0, mscale, k_codes, v_codes,
+                                    k_scale, v_scale, (hipStream_t)stream));
+}
+
+int kv_attention_workspace(int tokens, int seqs, int heads, int kv_heads, int dim, int width, int64_t *bytes) {
+  if (!bytes || tokens < 1 || seqs < 1 || heads < 1 || kv_heads < 1 || heads % kv_heads || dim < 1 || width < 1)
+    return BQM_EINVAL;
+  if (dim > kMaxKvDim || heads > kMaxKvHeads || width > kMaxKvWidth || (int64_t)tokens * heads >= kMaxGroups256)
+    return BQM_ENOTSUP;
+  *bytes = kv_attention_scratch(tokens, seqs, heads, kv_heads, dim, width);
+  return BQM_OK;
+}
+
+int kv_attention(const void *q, int dtype, int tokens, int heads, int dim, int64_t q_token_stride, int64_t q_head_stride,
+                 const int32_t *offsets, const int32_t *lens, int seqs, const int32_t *pages, int64_t pages_stride,
+                 int width, const uint8_t *k_codes, const uint8_t *v_codes, const float *k_scale, const float *v_scale,
+                 int count, int kv_heads, float scale, int window, void *out, void *workspace, int64_t workspace_bytes,
+                 bqm_stream_t stream) {
+  if (!q || !k_codes || !v_codes || !k_scale || !v_scale || !out || window < 0 || !known_dtype(dtype)) return BQM_EINVAL;
+  const KvBatch B{offsets, lens, pages, pages_stride, seqs, tokens, width, count};
+  int rc = check_batch(B);
+  if (rc) return rc;
+  int64_t need = 0;
+  rc = kv_attention_workspace(tokens, seqs, heads, kv_heads, dim, width, &need);
+  if (rc) return rc;
+  if (!separate(tokens, q_token_stride, heads, q_head_stride, dim) || workspace_bytes < need || (need && !workspace))
+    return BQM_EINVAL;
+  const unsigned el = (unsigned)(elem_size(dtype) - 1);
+  if (!aligned16(k_codes) || !aligned16(v_codes) || !aligned16(workspace) || (((uintptr_t)q | (uintptr_t)out) & el) ||
+      (((uintptr_t)k_scale | (uintptr_t)v_scale) & 3u))
+    return BQM_EALIGN;
+  int cus;
+  rc = current_device(&cus);
+  if (rc) return rc;
+  return status_of(launch_kv_attention(B, q, dtype, heads, dim, q_token_stride, q_head_stride, k_codes, v_codes, k_scale,
+                                       v_scale, kv_heads, scale, window, out, workspace, (hipStream_t)stream));
+}
+
+int moe_ffn_workspace(int tokens, int experts, int top, int hidden, int ffn, int64_t *bytes) {
+  if (!bytes || tokens < 1 || experts < 1 || top < 1 || top > experts || hidden < 1 || ffn < 1) return BQM_EINVAL;
+  if (tokens > kMoeFewTokens || !moe_route_supported(experts, top) || hidden > kMaxMoeCols || ffn > kMaxMoeCols)
+    return BQM_ENOTSUP;
+  *bytes = moe_ffn_scratch(tokens, experts, top, hidden, ffn);
+  return BQM_OK;
+}
+
+int moe_ffn(const void *x, int dtype, int tokens, int hidden, int64_t x_stride, const void *logits, int logits_dtype,
+            int64_t logits_stride, int experts, int top, int renorm, const uint8_t *w13, const float *w13_scale,
+            const uint8_t *w2, const float *w2_scale, int ffn, void *out, void *workspace, int64_t workspace_bytes,
+            bqm_stream_t stream) {
+  if (!x || !logits || !w13 || !w13_scale || !w2 || !w2_scale || !out || !known_dtype(dtype) || !known_dtype(logits_dtype))
+    return BQM_EINVAL;
+  int64_t need = 0;
+  int rc = moe_ffn_workspace(tokens, experts, top, hidden, ffn, &need);
+  if (rc) return rc;
+  if ((tokens > 1 && (x_stride < hidden || logits_stride < experts)) || workspace_bytes < need || (need && !workspace))
+    return BQM_EINVAL;
+  if (!aligned16(w13) || !aligned16(w2) || !aligned16(workspace) ||
+      (((uintptr_t)x | (uintptr_t)out) & (unsigned)(elem_size(dtype) - 1)) ||
+      ((uintptr_t)logits & (unsigned)(elem_size(logits_dtype) - 1)) || (((uintptr_t)w13_scale | (uintptr_t)w2_scale) & 3u))
+    return BQM_EALIGN;
+  int cus;
+  rc = current_device(&cus);
+  if (rc) return rc;
+  return status_of(launch_moe_ffn(x, dtype, tokens, hidden, x_stride, logits, logits_dtype, logits_stride, experts, top,
+                                  renorm != 0, w13, w13_scale, w2, w2_scale, ffn, out, workspace, (hipStream_t)stream));
 }
 
 const char *bqm_strerror(int code) {

@@ -176,6 +176,23 @@ hipError_t launch_moe_route(const void *logits, int dtype, int tokens, int exper
                             int32_t *slots, void *scratch, hipStream_t s);
 hipError_t launch_moe_combine(const void *y, int dtype, int64_t rows, int d, const int32_t *slots,
                               const float *weights, int tokens, int top, void *out, hipStream_t s);
+hipError_t launch_rope(const void *x, int dtype, int tokens, int heads, int dim, int64_t xt, int64_t xh,
+                       const int32_t *positions, const double *freqs, int rotary, bool interleaved, float mscale,
+                       bool backward, void *y, int64_t yt, int64_t yh, hipStream_t s);
+struct KvBatch;                                          // kv_common.h
+int64_t kv_append_jobs(int tokens, int seqs);            // workgroups of a launch and head
+hipError_t launch_kv_append(const KvBatch &B, const void *k, const void *v, int dtype, int heads, int dim, int64_t kt,
+                            int64_t kh, int64_t vt, int64_t vh, const int32_t *positions, const double *freqs, int rotary,
+                            bool interleaved, float mscale, uint8_t *kc, uint8_t *vc, float *ks, float *vs, hipStream_t s);
+int64_t kv_attention_scratch(int tokens, int seqs, int heads, int kv_heads, int dim, int width);
+hipError_t launch_kv_attention(const KvBatch &B, const void *q, int dtype, int heads, int dim, int64_t qt, int64_t qh,
+                               const uint8_t *kc, const uint8_t *vc, const float *ks, const float *vs, int kv_heads,
+                               float scale, int window, void *out, void *scratch, hipStream_t s);
+constexpr int kMoeFewTokens = 32;
+int64_t moe_ffn_scratch(int tokens, int experts, int top, int hidden, int ffn);
+hipError_t launch_moe_ffn(const void *x, int dtype, int tokens, int hidden, int64_t xs, const void *logits, int ltype,
+                          int64_t ls, int experts, int top, bool renorm, const uint8_t *w13, const float *s13,
+                          const uint8_t *w2, const float *s2, int ffn, void *out, void *scratch, hipStream_t s);
 hipError_t launch_codebook_fit(const double *samples, int64_t n, int levels, int iters,
                                double *raw, float *table, hipStream_t s);
 

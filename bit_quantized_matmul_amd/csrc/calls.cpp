@@ -12,6 +12,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 
+#include <cmath>
 #include <sstream>
 
 #include "bqm.h"
@@ -25,7 +26,8 @@ struct Refused {
 PyObject *g_device = nullptr, *g_stream = nullptr;   // torch._C._cuda_getDevice, _cuda_getCurrentRawStream
 
 // libbqm.so's functions, by the types that bqm.h declares
-#define FUNCTIONS(X) X(fp8_quant) X(fp8_gemm) X(fp8_gemm_grouped) X(moe_route_workspace) X(moe_route) X(moe_combine)
+#define FUNCTIONS(X) X(fp8_quant) X(fp8_gemm) X(fp8_gemm_grouped) X(moe_route_workspace) X(moe_route) X(moe_combine) \
+  X(rope) X(kv_append) X(kv_attention_workspace) X(kv_attention) X(moe_ffn_workspace) X(moe_ffn)
 #define DECLARE(f) decltype(&::f) p_##f = nullptr;
 FUNCTIONS(DECLARE)
 #undef DECLARE
@@ -300,6 +302,210 @@ PyObject *combine(PyObject *const *a) {
   return rc ? code(rc) : THPVariable_Wrap(out);
 }
 
+double number(PyObject *o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw python_error();
+  return v;
+}
+
+// A tensor [tokens, heads, dim] whose rows are contiguous, on the device
+struct Heads {
+  int tokens, heads, dim, type;
+  int64_t ts, hs;
+};
+Heads heads_of(const at::Tensor &t, const char *name) {
+  if (t.dim() != 3 || t.numel() < 1)
+    throw Refused{std::string(name) + " must have shape [tokens, heads, dim], got " + shown(t.sizes())};
+  if (t.size(0) > INT32_MAX || t.size(1) > INT32_MAX || t.size(2) > INT32_MAX) throw Refused{std::string(name) + " is too large"};
+  const int type = type_code(t.scalar_type(), name);
+  if (t.size(2) > 1 && t.stride(2) != 1)
+    throw Refused{std::string(name) + "'s rows must be contiguous (strides " + shown(t.strides()) + ")"};
+  return {(int)t.size(0), (int)t.size(1), (int)t.size(2), type, t.stride(0), t.stride(1)};
+}
+
+// freqs and positions of `tokens` tokens, or none of both
+struct Turns {
+  const at::Tensor *positions = nullptr, *freqs = nullptr;
+  int rotary = 0;
+  const int32_t *p = nullptr;
+  const double *f = nullptr;
+  Turns(PyObject *po, PyObject *fo, const Heads &x) {
+    if (fo == Py_None) {
+      if (po != Py_None) throw Refused{"positions come with freqs"};
+      return;
+    }
+    freqs = &tensor(fo, "freqs");
+    positions = &tensor(po, "positions");
+    if (freqs->dim() != 1 || freqs->numel() < 1 || 2 * freqs->numel() > x.dim)
+      throw Refused{"freqs must have shape [rotary / 2], rotary at most " + std::to_string(x.dim) + ", got " + shown(freqs->sizes())};
+    shape(*positions, {x.tokens}, "positions");
+    rotary = 2 * (int)freqs->numel();
+  }
+  void addresses(int dev) {
+    if (!freqs) return;
+    f = (const double *)address(*freqs, at::kDouble, dev, "freqs");
+    p = (const int32_t *)address(*positions, at::kInt, dev, "positions");
+  }
+};
+
+// x, positions, freqs, interleaved, mscale, backward, out -> out
+PyObject *rope_call(PyObject *const *a) {
+  const at::Tensor &x = tensor(a[0], "x");
+  const Heads h = heads_of(x, "x");
+  if (a[2] == Py_None) throw Refused{"freqs must be a CUDA/HIP tensor"};
+  Turns r(a[1], a[2], h);
+  const int dev = current_device(x, "x");
+  on_device(x, dev, "x");
+  r.addresses(dev);
+  at::Tensor y;
+  if (a[6] == Py_None) {
+    y = fresh(x.sizes(), x.scalar_type(), dev);
+  } else {
+    y = tensor(a[6], "out");
+    shape(y, x.sizes(), "out");
+    on_device(y, dev, "out");
+    if (y.scalar_type() != x.scalar_type())
+      throw Refused{"out must be " + type_name(x.scalar_type()) + ", got " + type_name(y.scalar_type())};
+  }
+  const Heads o = heads_of(y, "out");
+  const int rc = p_rope(x.data_ptr(), h.type, h.tokens, h.heads, h.dim, h.ts, h.hs, r.p, r.f, r.rotary, truth(a[3]),
+                        (float)number(a[4]), truth(a[5]), y.data_ptr(), o.ts, o.hs, current_stream(dev));
+  return rc ? code(rc) : THPVariable_Wrap(y);
+}
+
+// The cache's four tensors and the batch's: a = k, v, k_scale, v_scale; pages, lens, offsets
+struct Cache {
+  int64_t count, heads;
+  uint8_t *k, *v;
+  float *ks, *vs;
+  int seqs, width;
+  int64_t stride;
+  const int32_t *pages, *lens, *offsets = nullptr;
+  Cache(PyObject *const *a, PyObject *const *b, int64_t dim, int64_t tokens) {
+    const at::Tensor &kt = tensor(a[0], "cache.k"), &vt = tensor(a[1], "cache.v");
+    const int64_t dp = dim <= 128 ? (dim + 31) / 32 * 32 : (dim + 63) / 64 * 64;
+    if (kt.dim() != 4 || kt.size(2) != 64 || kt.size(3) != dp || kt.numel() < 1 || kt.size(0) > INT32_MAX || kt.size(1) > INT32_MAX)
+      throw Refused{"cache.k must have shape [pages, heads, 64, " + std::to_string(dp) + "], got " + shown(kt.sizes())};
+    count = kt.size(0);
+    heads = kt.size(1);
+    shape(vt, {count, heads, dp, 64}, "cache.v");
+    shape(tensor(a[2], "cache.k_scale"), {count, heads}, "cache.k_scale");
+    shape(tensor(a[3], "cache.v_scale"), {count, heads}, "cache.v_scale");
+    const at::Tensor &p = tensor(b[0], "pages");
+    if (p.dim() != 2 || p.numel() < 1 || p.size(0) > INT32_MAX || p.size(1) > INT32_MAX)
+      throw Refused{"pages must have shape [seqs, width], got " + shown(p.sizes())};
+    if (p.size(1) > 1 && p.stride(1) != 1) throw Refused{"pages's rows must be contiguous (strides " + shown(p.strides()) + ")"};
+    seqs = (int)p.size(0);
+    width = (int)p.size(1);
+    stride = p.stride(0);
+    shape(tensor(b[1], "lens"), {seqs}, "lens");
+    if (b[2] != Py_None) shape(tensor(b[2], "offsets"), {seqs + 1}, "offsets");
+    else if (tokens != seqs)
+      throw Refused{"without offsets there is one token a sequence: " + std::to_string(seqs) + " sequences, got " + std::to_string(tokens)};
+  }
+  void addresses(PyObject *const *a, PyObject *const *b, int dev) {
+    k = (uint8_t *)address(THPVariable_Unpack(a[0]), at::kFloat8_e4m3fn, dev, "cache.k");
+    v = (uint8_t *)address(THPVariable_Unpack(a[1]), at::kFloat8_e4m3fn, dev, "cache.v");
+    ks = (float *)address(THPVariable_Unpack(a[2]), at::kFloat, dev, "cache.k_scale");
+    vs = (float *)address(THPVariable_Unpack(a[3]), at::kFloat, dev, "cache.v_scale");
+    const at::Tensor &p = THPVariable_Unpack(b[0]);
+    on_device(p, dev, "pages");
+    if (p.scalar_type() != at::kInt) throw Refused{"pages must be Int, got " + type_name(p.scalar_type())};
+    pages = (const int32_t *)p.data_ptr();
+    lens = (const int32_t *)address(THPVariable_Unpack(b[1]), at::kInt, dev, "lens");
+    if (b[2] != Py_None) offsets = (const int32_t *)address(THPVariable_Unpack(b[2]), at::kInt, dev, "offsets");
+  }
+};
+
+// cache.k, cache.v, cache.k_scale, cache.v_scale, pages, lens, offsets, k, v, positions, freqs, interleaved, mscale
+PyObject *append(PyObject *const *a) {
+  const at::Tensor &k = tensor(a[7], "k"), &v = tensor(a[8], "v");
+  const Heads h = heads_of(k, "k");
+  shape(v, k.sizes(), "v");
+  const Heads g = heads_of(v, "v");
+  if (g.type != h.type) throw Refused{"v must be " + type_name(k.scalar_type()) + ", got " + type_name(v.scalar_type())};
+  Cache c(a, a + 4, h.dim, h.tokens);
+  if (c.heads != h.heads)
+    throw Refused{"k must have the cache's " + std::to_string(c.heads) + " heads, got " + shown(k.sizes())};
+  Turns r(a[9], a[10], h);
+  const int dev = current_device(k, "k");
+  on_device(k, dev, "k");
+  on_device(v, dev, "v");
+  r.addresses(dev);
+  c.addresses(a, a + 4, dev);
+  return code(p_kv_append(k.data_ptr(), v.data_ptr(), h.type, h.tokens, h.heads, h.dim, h.ts, h.hs, g.ts, g.hs, c.offsets,
+                          c.lens, c.seqs, c.pages, c.stride, c.width, r.p, r.f, r.rotary, truth(a[11]), (float)number(a[12]),
+                          c.k, c.v, c.ks, c.vs, (int)c.count, current_stream(dev)));
+}
+
+// The caller's workspace of at least `need` bytes, or a new one; nothing where none is needed.
+at::Tensor scratch(PyObject *o, int64_t need, int dev) {
+  if (o == Py_None) return need ? fresh({need}, at::kByte, dev) : at::Tensor();
+  const at::Tensor &ws = tensor(o, "workspace");
+  address(ws, at::kByte, dev, "workspace");
+  if (ws.numel() < need)
+    throw Refused{"workspace must hold at least " + std::to_string(need) + " bytes, got " + std::to_string(ws.numel())};
+  return ws;
+}
+
+// cache.k, cache.v, cache.k_scale, cache.v_scale, pages, lens, offsets, q, scale, window, out, workspace -> out
+PyObject *attention(PyObject *const *a) {
+  const at::Tensor &q = tensor(a[7], "q");
+  const Heads h = heads_of(q, "q");
+  Cache c(a, a + 4, h.dim, h.tokens);
+  if (h.heads % c.heads)
+    throw Refused{"q's heads must be a multiple of the cache's " + std::to_string(c.heads) + ", got " + std::to_string(h.heads)};
+  const int window = integer(a[9], "window");
+  if (window < 0) throw Refused{"window must be at least 0, got " + std::to_string(window)};
+  const float scale = a[8] == Py_None ? (float)(1.0 / std::sqrt((double)h.dim)) : (float)number(a[8]);
+  const int dev = current_device(q, "q");
+  on_device(q, dev, "q");
+  c.addresses(a, a + 4, dev);
+  int64_t need = 0;
+  int rc = p_kv_attention_workspace(h.tokens, c.seqs, h.heads, (int)c.heads, h.dim, c.width, &need);
+  if (rc) return code(rc);
+  const at::Tensor ws = scratch(a[11], need, dev);
+  const at::Tensor out = result(a[10], q.sizes(), q.scalar_type(), dev, "out");
+  rc = p_kv_attention(q.data_ptr(), h.type, h.tokens, h.heads, h.dim, h.ts, h.hs, c.offsets, c.lens, c.seqs, c.pages,
+                      c.stride, c.width, c.k, c.v, c.ks, c.vs, (int)c.count, (int)c.heads, scale, window, out.data_ptr(),
+                      ws.defined() ? ws.data_ptr() : nullptr, need, current_stream(dev));
+  return rc ? code(rc) : THPVariable_Wrap(out);
+}
+
+// x, w13, w13_scale, w2, w2_scale, logits, top, renorm, out, workspace -> out
+PyObject *few(PyObject *const *a) {
+  const at::Tensor &x = tensor(a[0], "x"), &logits = tensor(a[5], "logits");
+  const int64_t xs = strided_rows(x, "x"), ls = strided_rows(logits, "logits");
+  const int64_t tokens = x.size(0), hidden = x.size(1), experts = logits.size(1);
+  if (logits.size(0) != tokens)
+    throw Refused{"logits must have shape [" + std::to_string(tokens) + ", experts], got " + shown(logits.sizes())};
+  const at::Tensor &w13 = tensor(a[1], "w13"), &w2 = tensor(a[3], "w2");
+  const int64_t kb = (hidden + 127) / 128;
+  if (w13.dim() != 3 || w13.size(0) != experts || w13.size(1) % 2 || w13.size(2) != kb * 128 || w13.numel() < 1 || w13.size(1) > INT32_MAX)
+    throw Refused{"w13 must have shape [" + std::to_string(experts) + ", 2 ffn, " + std::to_string(kb * 128) + "], got " + shown(w13.sizes())};
+  const int64_t ffn = w13.size(1) / 2, fb = (ffn + 127) / 128;
+  shape(w2, {experts, hidden, fb * 128}, "w2");
+  const at::Tensor &s13 = tensor(a[2], "w13_scale"), &s2 = tensor(a[4], "w2_scale");
+  shape(s13, {experts, (2 * ffn + 127) / 128, kb}, "w13_scale");
+  shape(s2, {experts, kb, fb}, "w2_scale");
+  const int top = integer(a[6], "top");
+  const int dev = current_device(x, "x");
+  int64_t need = 0;
+  int rc = p_moe_ffn_workspace((int)tokens, (int)experts, top, (int)hidden, (int)ffn, &need);
+  if (rc) return code(rc);
+  on_device(x, dev, "x");
+  on_device(logits, dev, "logits");
+  const void *w13p = address(w13, at::kFloat8_e4m3fn, dev, "w13"), *w2p = address(w2, at::kFloat8_e4m3fn, dev, "w2"),
+             *s13p = address(s13, at::kFloat, dev, "w13_scale"), *s2p = address(s2, at::kFloat, dev, "w2_scale");
+  const at::Tensor ws = scratch(a[9], need, dev);
+  const at::Tensor out = result(a[8], x.sizes(), x.scalar_type(), dev, "out");
+  rc = p_moe_ffn(x.data_ptr(), type_code(x.scalar_type(), "x"), (int)tokens, (int)hidden, xs, logits.data_ptr(),
+                 type_code(logits.scalar_type(), "logits"), ls, (int)experts, top, truth(a[7]), (const uint8_t *)w13p,
+                 (const float *)s13p, (const uint8_t *)w2p, (const float *)s2p, (int)ffn, out.data_ptr(),
+                 ws.defined() ? ws.data_ptr() : nullptr, need, current_stream(dev));
+  return rc ? code(rc) : THPVariable_Wrap(out);
+}
+
 // No exception leaves a call: refusals become ValueError, torch's errors its own.
 template <PyObject *(*kCall)(PyObject *const *), int kArgs>
 PyObject *entry(PyObject *, PyObject *const *a, Py_ssize_t n) {
@@ -350,6 +556,10 @@ PyMethodDef methods[] = {
     {"fp8_gemm_grouped", FAST((&entry<grouped, 9>)), METH_FASTCALL, nullptr},
     {"moe_route", FAST((&entry<route, 4>)), METH_FASTCALL, nullptr},
     {"moe_combine", FAST((&entry<combine, 4>)), METH_FASTCALL, nullptr},
+    {"rope", FAST((&entry<rope_call, 7>)), METH_FASTCALL, nullptr},
+    {"kv_append", FAST((&entry<append, 13>)), METH_FASTCALL, nullptr},
+    {"kv_attention", FAST((&entry<attention, 12>)), METH_FASTCALL, nullptr},
+    {"moe_ffn", FAST((&entry<few, 10>)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,140 @@
+// The paged 8-bit cache and the rotation of positions, as their kernels share them.
+#pragma once
+
+#include "lowp_types.h"
+
+namespace bqm {
+
+constexpr int kPage = 64;                 // tokens of a page, the block of one scale a head
+constexpr int kMaxKvDim = 256;
+
+// Columns of a head in the cache: dim padded to a size that kernels are built for.
+inline int kv_padded_dim(int dim) { return dim <= 128 ? (dim + 31) / 32 * 32 : (dim + 63) / 64 * 64; }
+
+// Ragged sequences: rows [offsets[s], offsets[s + 1]) are the newest tokens of sequence s, of
+// which the cache holds lens[s] with them; without offsets row s is sequence s's one.
+struct KvBatch {
+  const int32_t *offsets, *lens, *pages;  // pages [seqs, width], rows `stride` apart
+  int64_t stride;
+  int seqs, tokens, width, count;         // count: pages of the cache
+};
+
+struct KvSeq {
+  int s, lo, n, len;
+  __device__ __forceinline__ int first() const { return len - n; }     // position of row lo; may be negative
+};
+
+__device__ __forceinline__ KvSeq kv_seq(const KvBatch &B, int s) {
+  KvSeq q{s, s, 1, max(0, B.lens[s])};
+  if (B.offsets) {
+    q.lo = min(max(0, B.offsets[s]), B.tokens);
+    q.n = max(0, min(B.offsets[s + 1], B.tokens) - q.lo);
+  }
+  return q;
+}
+
+// Positions that the sequence's row of the table has pages for.
+__device__ __forceinline__ int kv_limit(const KvBatch &B, const KvSeq &q) { return min(q.len, B.width * kPage); }
+
+// The page of positions 64 i .. 64 i + 63, -1 where the table names none of the cache's.
+__device__ __forceinline__ int kv_page(const KvBatch &B, const KvSeq &q, int i) {
+  const int p = B.pages[q.s * B.stride + i];
+  return (unsigned)p < (unsigned)B.count ? p : -1;
+}
+
+// Job `bid` of the sequences' jobs(seq) each, in order: its sequence and its place there.  Every
+// wave searches for itself, 64 sequences at a time.  Without offsets every sequence has
+// `each` places.  False past the last.
+template <typename F>
+__device__ __forceinline__ bool kv_find(const KvBatch &B, int bid, int each, F jobs, KvSeq *q, int *job) {
+  if (!B.offsets) {
+    const int s = bid / each;
+    if (s >= B.seqs) return false;
+    *q = kv_seq(B, s);
+    *job = bid - s * each;
+    return *job < jobs(*q);
+  }
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int s0 = 0; s0 < B.seqs; s0 += 64) {
+    const int mine = s0 + lane < B.seqs ? jobs(kv_seq(B, s0 + lane)) : 0;
+    const int inc = wave_prefix(mine);
+    const int sum = __builtin_amdgcn_readlane(inc, 63);
+    if (bid < before + sum) {
+      const int at = __popcll(__ballot(before + inc <= bid));
+      const int j = bid - before - (at ? __builtin_amdgcn_readlane(inc, at - 1) : 0);
+      // ascending offsets always pass; others, whose sums may overflow, stay in their buffers
+      if (at >= 64 || s0 + at >= B.seqs || j < 0 || j >= __builtin_amdgcn_readlane(mine, at)) return false;
+      *q = kv_seq(B, s0 + at);
+      *job = j;
+      return true;
+    }
+    before += sum;
+  }
+  return false;
+}
+
+// ------------------------------------------------------------------ rotation
+//
+// cos and sin of position p times f radians.  The angle is formed and reduced to an eighth of
+// a turn in 64 bits: in 32, position 2^20 would leave it 0.06 off.  The series' first terms left out are
+// below 2^-28.
+__device__ __forceinline__ void turn(int p, double f, float scale, float sign, float *c, float *s) {
+  const double t = (double)p * (f * 0.15915494309189535);               // in turns: f / (2 pi)
+  const double q4 = rint(4.0 * t);
+  const float x = (float)((t - 0.25 * q4) * 6.283185307179586);
+  const float x2 = x * x;
+  const float sn = x * fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), 1.0f);
+  const float cs = fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, -1.0f / 3628800, 1.0f / 40320), -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
+  const int q = (int)(q4 - 4.0 * rint(0.25 * q4)) & 3;                   // quarter turns, modulo 4
+  const float a = q & 1 ? sn : cs, b = q & 1 ? cs : sn;
+  *c = scale * (q == 1 || q == 2 ? -a : a);
+  *s = scale * sign * (q >= 2 ? -b : b);
+}
+
+struct Rope {
+  const int32_t *positions;
+  const double *freqs;                    // [rotary / 2]
+  int rotary, interleaved;
+  float mscale, sign;
+};
+
+// A unit is 2 N columns of a head: N from c1 on and N from c2 on.  The first rotary / (2 N)
+// are N pairs each, the rest follow in order.
+template <int N>
+__device__ __forceinline__ bool unit_columns(const Rope &R, int u, int *c1, int *c2) {
+  const int turned = R.rotary / (2 * N);
+  if (u < turned && !R.interleaved) {
+    *c1 = u * N;
+    *c2 = R.rotary / 2 + u * N;
+  } else {                                                               // also where c1 >= rotary
+    *c1 = u * 2 * N;
+    *c2 = *c1 + N;
+  }
+  return u < turned;
+}
+
+// cs: (cos, sin) of the unit's N pairs
+template <int N>
+__device__ __forceinline__ void unit_turn(const Rope &R, const float2 *cs, float (&a)[N], float (&b)[N]) {
+  if (N == 1 || !R.interleaved) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float x = a[i], y = b[i];
+      a[i] = fmaf(x, cs[i].x, -(y * cs[i].y));
+      b[i] = fmaf(x, cs[i].y, y * cs[i].x);
+    }
+  } else if constexpr (N > 1) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      float x = a[2 * i], y = a[2 * i + 1];
+      a[2 * i] = fmaf(x, cs[i].x, -(y * cs[i].y));
+      a[2 * i + 1] = fmaf(x, cs[i].y, y * cs[i].x);
+      x = b[2 * i], y = b[2 * i + 1];
+      b[2 * i] = fmaf(x, cs[N / 2 + i].x, -(y * cs[N / 2 + i].y));
+      b[2 * i + 1] = fmaf(x, cs[N / 2 + i].y, y * cs[N / 2 + i].x);
+    }
+  }
+}
+
+}  // namespace bqm

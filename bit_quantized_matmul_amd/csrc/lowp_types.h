@@ -19,6 +19,14 @@ __device__ __forceinline__ float to_f32(__bf16 v) { return (float)v; }
 __device__ __forceinline__ float to_f32(_Float16 v) { return (float)v; }
 template <typename T> __device__ __forceinline__ T from_f32(float v) { return (T)v; }
 
+// The same of a sum or product that was formed in fp32: left to itself, the compiler joins some elements' last
+// operation and their rounding to fp16 into one instruction, so that equal sums would give unequal elements.
+template <typename T>
+__device__ __forceinline__ T from_sum(float v) {
+  if constexpr (sizeof(T) == 2) asm("" : "+v"(v));
+  return from_f32<T>(v);
+}
+
 // N consecutive elements as fp32, with 16-byte loads: p is aligned to 16 bytes.
 template <int N>
 __device__ __forceinline__ void load_vec(const float *p, float (&v)[N]) {

@@ -465,6 +465,87 @@ int moe_route(const void *logits, int dtype, int tokens, int experts, int64_t st
 int moe_combine(const void *y, int dtype, int64_t y_rows, int d, const int32_t *slots, const float *weights,
                 int tokens, int top, void *out, bqm_stream_t stream);
 
+/* The layer of a few tokens (at most 32), from router logits to combined rows, in two
+ * launches that read each chosen expert's codes once:
+ *   out[t] = sum_j w[t, j] W2[e_j] (silu(G[e_j] x_t) * (U[e_j] x_t)),  W13 = [G | U],
+ * e_j and w[t, j] as moe_route gives them (the same ties, masks and renorm; a token without an
+ * expert has a row of zeros).  x is not quantized: the products of its elements and the codes are summed
+ * in fp32 (x and the hidden rows as one or, for an fp32 x, two fp16 terms of a power of two
+ * a row), and out is rounded once.  A row of x with a NaN or an infinity has a row of NaN.
+ * x [device] `dtype` [tokens, hidden], rows x_stride apart; logits [device] `logits_dtype` [tokens,
+ * experts], rows logits_stride apart; w13 [device] [experts, 2 ffn, 128 ceil(hidden / 128)] and w2
+ * [experts, hidden, 128 ceil(ffn / 128)] with their scales, both as fp8_pack writes them, 16-byte
+ * aligned; out [device] `dtype` [tokens, hidden].  workspace [device, 16-byte aligned] of
+ * moe_ffn_workspace bytes needs no clearing and may be reused by the next call on the stream.
+ * hidden and ffn <= 65536, experts and top as for moe_route (BQM_ENOTSUP). */
+int moe_ffn_workspace(int tokens, int experts, int top, int hidden, int ffn, int64_t *bytes);
+int moe_ffn(const void *x, int dtype, int tokens, int hidden, int64_t x_stride, const void *logits, int logits_dtype,
+            int64_t logits_stride, int experts, int top, int renorm, const uint8_t *w13, const float *w13_scale,
+            const uint8_t *w2, const float *w2_scale, int ffn, void *out, void *workspace, int64_t workspace_bytes,
+            bqm_stream_t stream);
+
+/* ---- rotary positions, and a paged cache of E4M3 codes with its attention ----
+ * The pages keep the cache in 8 bits beside 4-bit weights, with windows of 1024
+ * positions in most layers ("14MB holds 45M parameters: dissecting Needle's
+ * .cact file and W4A8 quantization", section 4).
+ *
+ * Turn the first `rotary` columns of every head by its token's position:
+ *   y1 = mscale (x1 cos a - x2 sin a),  y2 = mscale (x1 sin a + x2 cos a),  a = positions[t] freqs[i],
+ * for the pairs (x1, x2) = columns (i, i + rotary / 2) or, interleaved, (2 i, 2 i + 1); the other
+ * columns are copied.  Angles are formed in fp64, the rest in fp32, y is rounded once.  backward: the
+ * gradient's product with the transposed matrix (-sin for sin).
+ * x, y [device] `dtype` [tokens, heads, dim], tokens and heads the given strides apart, a row's
+ * columns side by side, rows not overlapping; y may be x with the same strides, and must not share
+ * memory with it otherwise.  positions [device] int32 [tokens]; freqs [device] fp64 [rotary / 2],
+ * radians a position.  rotary even, 2 <= rotary <= dim <= 1024 (BQM_ENOTSUP past 1024). */
+int rope(const void *x, int dtype, int tokens, int heads, int dim, int64_t x_token_stride, int64_t x_head_stride,
+         const int32_t *positions, const double *freqs, int rotary, int interleaved, float mscale, int backward, void *y,
+         int64_t y_token_stride, int64_t y_head_stride, bqm_stream_t stream);
+
+/* The cache.  A page holds 64 neighbouring positions of one sequence.  With dp = dim rounded up to
+ * 32, 64, 96, 128, 192 or 256 (dim <= 256):
+ *   k_codes [count, heads, 64, dp] and v_codes [count, heads, dp, 64]: E4M3, 16-byte aligned;
+ *   k_scale, v_scale [count, heads]: fp32, powers of two.
+ * A batch of sequences.  Sequence s has lens[s] positions with its newest, which are rows
+ * offsets[s] .. offsets[s + 1] - 1 of k, v or q (row s alone when offsets is NULL, and then
+ * tokens = seqs); its newest row is position lens[s] - 1.  pages [seqs, width] int32, rows
+ * pages_stride apart: positions 64 i .. 64 i + 63 lie in page pages[s, i].  offsets [seqs + 1] int32,
+ * ascending, and lens [seqs] int32.  All [device], and none of them leaves it: a launch is sized from
+ * tokens, seqs, width and heads alone.  Offsets outside [0, tokens] are taken as the nearer end.  Positions below 0,
+ * past the table's width or in a page outside [0, count) are not written and not attended to.
+ * width < 2^25. */
+
+/* Write new keys, turned as by rope (rotary 0: as they are; positions [tokens] and freqs then unused),
+ * and values into their pages.  scale = the smallest power of two, 2^-126 at least, with |value| <=
+ * 448 scale over the new tokens of the page and head, but no smaller than the page's scale where the page holds
+ * positions of the sequence before them; codes = E4M3(value / scale), and where the scale has grown the codes
+ * before become E4M3(code * old scale / scale).  An infinite or NaN element becomes code 0x7F and has no part in
+ * the scale.  Codes of later slots stay as they are.  k, v [device] `dtype` [tokens, heads, dim],
+ * tokens and heads the given strides apart.  No page may be written for two sequences, or twice for
+ * one, in a call: which of them it then holds is not defined. */
+int kv_append(const void *k, const void *v, int dtype, int tokens, int heads, int dim, int64_t k_token_stride,
+              int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride, const int32_t *offsets,
+              const int32_t *lens, int seqs, const int32_t *pages, int64_t pages_stride, int width,
+              const int32_t *positions, const double *freqs, int rotary, int interleaved, float mscale, uint8_t *k_codes,
+              uint8_t *v_codes, float *k_scale, float *v_scale, int count, bqm_stream_t stream);
+
+/* out[t, h] = sum_j p_j v_j, p = softmax over j of scale (q[t, h] . k_j), over the positions j of the
+ * cache with position(t) - window < j <= position(t) (window 0: no lower bound), keys and values of head
+ * h / (heads / kv_heads).  A row that sees no position is zeros; rows of no sequence are not
+ * written.  Products are summed in fp32 (q and p as one or, for an fp32 q, two fp16 terms), the
+ * maxima and sums of the softmax are fp32, out is rounded once.  What is masked has no part in the
+ * result, whatever it holds; a NaN code that is attended to makes NaN.
+ * q [device] `dtype` [tokens, heads, dim], tokens and heads the given strides apart; out [device] `dtype`
+ * [tokens, heads, dim] contiguous.  workspace [device, 16-byte aligned, NULL if none is needed] of
+ * kv_attention_workspace bytes needs no clearing and may be reused by the next call on the
+ * stream.  tokens * heads < 2^24 (BQM_ENOTSUP). */
+int kv_attention_workspace(int tokens, int seqs, int heads, int kv_heads, int dim, int width, int64_t *bytes);
+int kv_attention(const void *q, int dtype, int tokens, int heads, int dim, int64_t q_token_stride, int64_t q_head_stride,
+                 const int32_t *offsets, const int32_t *lens, int seqs, const int32_t *pages, int64_t pages_stride,
+                 int width, const uint8_t *k_codes, const uint8_t *v_codes, const float *k_scale, const float *v_scale,
+                 int count, int kv_heads, float scale, int window, void *out, void *workspace, int64_t workspace_bytes,
+                 bqm_stream_t stream);
+
 /* Human-readable name of an error code (static string). */
 const char *bqm_strerror(int code);
 

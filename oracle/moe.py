@@ -58,3 +58,27 @@ def combine(y, slots, weights):
                 out[t] += term
                 mag[t] += np.abs(term)
     return out, mag
+
+
+def ffn(x, w13, s13, w2, s2, logits, top: int, renorm: bool = True):
+    """The expert layer of unquantized rows x [tokens, hidden] on E4M3 codes, in fp64: (out, a bound of the sums behind
+    it: the absolute values of all terms, with |silu'| <= 1.1 and |silu(g)| <= |g|)."""
+    from . import fp8
+    x = np.asarray(x, dtype=np.float64)
+    ids, weights, *_ = route(logits, top, renorm)
+    n, hidden = w13.shape[1] // 2, x.shape[1]
+    out, mag = np.zeros(x.shape), np.zeros(x.shape)
+    for t in range(x.shape[0]):
+        for e, w in zip(ids[t], weights[t]):
+            if e < 0:
+                continue
+            m13 = fp8.weight_values(w13[e], s13[e])[:, :hidden]
+            m2 = fp8.weight_values(w2[e], s2[e])[:, :n]
+            h, hm = m13 @ x[t], np.abs(m13) @ np.abs(x[t])
+            with np.errstate(over="ignore"):
+                a = h[:n] / (1.0 + np.exp(-h[:n])) * h[n:]
+            # what an error of one part of hm in h can do to a
+            am = 1.1 * hm[:n] * np.abs(h[n:]) + np.abs(h[:n]) * hm[n:]
+            out[t] += w * (m2 @ a)
+            mag[t] += w * (np.abs(m2) @ (am + np.abs(a)))
+    return out, mag
