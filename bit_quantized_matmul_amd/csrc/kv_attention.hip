@@ -1,92 +1,357 @@
-// Attention over the paged 8-bit cache.
+// Attention over the paged 8-bit cache: few rows a sequence, the launches, and the join of parts.
 //
 //   o[t, h] = sum_j p_j v_j,   p = softmax_j(scale q[t, h] . k_j),   position - window < j <= position
 //
-// One wave a row and head: a lane takes a token of a page for the scores and columns for the sum, with the
-// running maximum m and sum l of the softmax: a page with a larger maximum scales what was summed before
-// by exp(m - m').
-#include "kv_common.h"
+// One pass over the pages with the running maximum m and sum l of the softmax: a page with a larger
+// maximum scales what was summed before by exp(m - m').  Codes become fp16 in registers, where they are
+// exact; a page's two scales are applied to its scores and to its sum of values in fp32, so pages whose scales
+// are far apart cost no bits.
+#include "kv_attention.h"
 
 namespace bqm {
+namespace attn {
 namespace {
 
-struct AttnArgs {
-  KvBatch B;
-  int heads, kv_heads, dim, dp, window;
-  int64_t qt, qh;                         // strides of q's tokens and heads
-  float scale;                            // times log2(e)
-  const uint8_t *kc, *vc;
-  const float *ks, *vs;
+// ------------------------------------------------------------------ few rows
+//
+// The cache is read once and bounds the time.  A tile is 16 queries of one key head: the rows of a
+// sequence times the heads that share the key head.  A workgroup takes `chunk` pages of a tile, its waves
+// every NW-th of them, straight into registers: a wave's loads of the next page's keys are on their way
+// while it weighs this page's scores, and its loads of the next values while it multiplies the next keys.
+template <typename T, int kDp, int NW>
+__global__ __launch_bounds__(64 * NW) void kv_stream_kernel(AttnArgs A, bool qvec, const T *__restrict__ q,
+                                                            T *__restrict__ out) {
+  constexpr int kTerms = kTermsOf<T>, kWide = kDp / 64, kSteps = kDp / 32, kCols = kDp / 16;
+  constexpr bool kOdd = kDp % 64 != 0;    // a last half chunk of 32 columns
+  KvSeq s;
+  int job;
+  const int rep = A.rep;
+  if (!kv_find(A.B, blockIdx.x, (rep + 15) / 16, [rep](const KvSeq &x) { return (int)(((int64_t)x.n * rep + 15) / 16); }, &s, &job))
+    return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 15, g = lane >> 4, kh = blockIdx.y;
+  const int last_c = min(s.n * rep, job * 16 + 16) - 1;
+  const int c = min(job * 16 + col, last_c), i = c / rep, h = kh * rep + (c - i * rep);
+  const int64_t row = s.lo + i;
+  const int pos = s.first() + i;
+  const int first = s.first() + job * 16 / rep, last = s.first() + last_c / rep;
+  int p0, p1;
+  pages_of(A, s, first, last, &p0, &p1);
+  p0 += (int)blockIdx.z * A.chunk;
+  p1 = min(p1, p0 + A.chunk);
+  const bool live = job * 16 + col <= last_c;
+
+  __shared__ float sm[NW][16], sl[NW][16];
+  __shared__ __align__(16) float so[NW][16][kDp + 4];
+  const int64_t at = (row * A.heads + h) * A.splits + blockIdx.z;
+  if (p0 >= p1) {                                                        // no page: rows without positions, parts past the last
+    if (A.splits > 1) {
+      if (threadIdx.x < 16 && live) A.ml[at] = float2{-INFINITY, 0.0f};
+    } else if (live) {
+      for (int d = threadIdx.x >> 4; d < A.dim; d += 4 * NW) out[(row * A.heads + h) * A.dim + d] = from_f32<T>(0.0f);
+    }
+    return;
+  }
+  const int lo = A.window ? max(0, pos - A.window + 1) : 0, hi = min(pos + 1, kv_limit(A.B, s));
+
+  // codes of one page: keys, token 16 (r >> 2) + 4 t + (r & 3) as row r of tile t, and values
+  i32x4 kw[4][kWide ? kWide : 1], vw[kCols];
+  i32x2 ko[4];
+  float ks = 0.0f, vs = 0.0f;
+  const int64_t row0 = 16 * (col >> 2) + (col & 3);
+  auto load_k = [&](int page) {
+    const uint8_t *p = A.kc + ((int64_t)page * A.kv_heads + kh) * (kPage * kDp) + row0 * kDp;
+    ks = A.ks[(int64_t)page * A.kv_heads + kh];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int w = 0; w < kWide; ++w) kw[t][w] = *reinterpret_cast<const i32x4 *>(p + t * 4 * kDp + w * 64 + g * 16);
+      if constexpr (kOdd) ko[t] = *reinterpret_cast<const i32x2 *>(p + t * 4 * kDp + kWide * 64 + g * 8);
+    }
+  };
+  auto load_v = [&](int page) {
+    const uint8_t *p = A.vc + ((int64_t)page * A.kv_heads + kh) * (kPage * kDp) + col * kPage + g * 16;
+    vs = A.vs[(int64_t)page * A.kv_heads + kh];
+#pragma unroll
+    for (int d = 0; d < kCols; ++d) vw[d] = *reinterpret_cast<const i32x4 *>(p + d * 16 * kPage);
+  };
+  auto page_at = [&](int pi) { return pi < p1 ? __builtin_amdgcn_readfirstlane(kv_page(A.B, s, pi)) : -1; };
+  int pi = p0 + wave;
+  int page = page_at(pi), next = page_at(pi + NW);
+  if (page >= 0) {
+    load_k(page);
+    load_v(page);
+  }
+
+  // queries, a power of two apart so that the largest of a row is at most 2^15
+  f16x8 qf[kSteps][kTerms];
+  float mul;                                                             // of q, without the page's
+  int qe;
+  {
+    float v[kSteps][8];
+    const T *qr = q + row * A.qt + h * A.qh;
+    uint32_t top = 0;
+#pragma unroll
+    for (int w = 0; w < kSteps; ++w) {
+      const int cc = w < 2 * kWide ? (w / 2) * 64 + g * 16 + (w & 1) * 8 : kWide * 64 + g * 8;
+      load_q8(qr, cc, A.dim, qvec, v[w]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[w][j]) & 0x7FFFFFFFu);
+    }
+    top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+    const float a = __uint_as_float(top);
+    qe = top && top < 0x7F800000u ? __builtin_amdgcn_frexp_expf(a) - 15 : 0;
+    mul = top < 0x7F800000u ? fabsf(A.scale) : __builtin_nanf("");       // a row that is not finite is NaN
+    const float sign = A.scale < 0.0f ? -1.0f : 1.0f;
+#pragma unroll
+    for (int w = 0; w < kSteps; ++w) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[w][j] = sign * ldexpf(v[w][j], -qe);
+      to_terms<kTerms>(v[w], qf[w]);
+    }
+  }
+
+  f32x4_t o[kCols] = {};
+  float m = -INFINITY, l = 0.0f;
+  for (; pi < p1; pi += NW) {
+    const int after = page_at(pi + 2 * NW);
+    f32x4_t x[4] = {};
+    const float k_scale = ks;
+    if (page >= 0) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int w = 0; w < kSteps; ++w) {
+          f16x8 a;
+          if (w < 2 * kWide) a = widen(kw[t][w / 2][2 * (w & 1)], kw[t][w / 2][2 * (w & 1) + 1]);
+          else a = widen(ko[t][0], ko[t][1]);
+#pragma unroll
+          for (int z = 0; z < kTerms; ++z) x[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qf[w][z], x[t], 0, 0, 0);
+        }
+    }
+    if (next >= 0) load_k(next);
+    if (page >= 0) {
+      // scores are x times f >= 0
+      const float f = ldexpf(mul * __builtin_amdgcn_frexp_mantf(k_scale), __builtin_amdgcn_frexp_expf(k_scale) + qe);
+      const int j0 = pi * kPage + g * 16;
+      const bool whole = pi * kPage + kPage <= min(first + 1, kv_limit(A.B, s)) && (!A.window || pi * kPage > last - A.window);
+      uint32_t see = 0xFFFFu;
+      if (!whole) {                                                      // bit 4 t + r: token j0 + 4 t + r
+        const int a = min(max(lo - j0, 0), 16), b = min(max(hi - j0, 0), 16);
+        see = ((1u << b) - 1u) & ~((1u << a) - 1u);
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) top = fmaxf(top, whole || (see >> (4 * t + r) & 1) ? x[t][r] : -INFINITY);
+      top = fmaxf(top, __shfl_xor(top, 16, 64));
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      const float m1 = fmaxf(m, top > -INFINITY ? top * f : -INFINITY);
+      const float base = (m1 > -INFINITY ? m1 : 0.0f) - kUp;
+      if (__ballot(m1 > m)) {
+        const float alpha = __builtin_amdgcn_exp2f(m - (base + kUp));
+        l *= alpha;
+#pragma unroll
+        for (int d = 0; d < kCols; ++d) o[d] *= alpha;
+        m = m1;
+      }
+      f16x8 p[2][kTerms];
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        float e[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const float v = __builtin_amdgcn_exp2f(fmaf(x[2 * a + r / 4][r % 4], f, -base));
+          e[r] = whole || (see >> (8 * a + r) & 1) ? v : 0.0f;
+          l += e[r];
+        }
+        to_terms<kTerms>(e, p[a]);
+      }
+      const float v_scale = vs * 0x1p-15f;
+      if (!whole) {
+        // what some row does not see may be NaN, and 0 times it would be too: such codes are taken out, and
+        // the sums of the rows that do see them made NaN
+        bool bad = false;
+#pragma unroll
+        for (int d = 0; d < kCols; ++d)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) bad |= has_nan(vw[d][w]);
+        if (__builtin_expect(__ballot(bad) != 0, 0)) {
+          f16x8 sees[2];
+#pragma unroll
+          for (int r = 0; r < 16; ++r) sees[r / 8][r % 8] = (_Float16)(see >> r & 1 ? 1.0f : 0.0f);
+#pragma unroll
+          for (int d = 0; d < kCols; ++d) {
+            f32x4_t n = {};
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+              n = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen(nan_ones(vw[d][2 * a]), nan_ones(vw[d][2 * a + 1])), sees[a], n, 0, 0, 0);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              if (n[w] != 0.0f) o[d][w] = __builtin_nanf("");
+              vw[d][w] = without_nan(vw[d][w]);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < kCols; ++d) {
+        f32x4_t part = {};
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          const f16x8 v = widen(vw[d][2 * a], vw[d][2 * a + 1]);
+#pragma unroll
+          for (int z = 0; z < kTerms; ++z) part = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[a][z], part, 0, 0, 0);
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) o[d][w] = fmaf(part[w], v_scale, o[d][w]);
+      }
+    }
+    if (next >= 0) load_v(next);
+    page = next;
+    next = after;
+  }
+  l += __shfl_xor(l, 16, 64);
+  l += __shfl_xor(l, 32, 64);
+
+  // the waves' sums join in LDS
+  if (g == 0) {
+    sm[wave][col] = m;
+    sl[wave][col] = l * 0x1p-15f;
+  }
+#pragma unroll
+  for (int d = 0; d < kCols; ++d) *reinterpret_cast<f32x4_t *>(&so[wave][col][d * 16 + g * 4]) = o[d];
+  __syncthreads();
+  // 4 NW threads a query
+  const int qc = threadIdx.x / (4 * NW), part = threadIdx.x % (4 * NW);
+  const int c2 = job * 16 + qc;
+  if (c2 > last_c) return;
+  const int i2 = c2 / rep, h2 = kh * rep + (c2 - i2 * rep);
+  const int64_t head = (int64_t)(s.lo + i2) * A.heads + h2;
+  float top = -INFINITY, sum = 0.0f, w[NW];
+#pragma unroll
+  for (int v = 0; v < NW; ++v) top = fmaxf(top, sm[v][qc]);
+#pragma unroll
+  for (int v = 0; v < NW; ++v) {
+    w[v] = top > -INFINITY ? __builtin_amdgcn_exp2f(sm[v][qc] - top) : sl[v][qc];   // no maximum: 0, or NaN
+    sum = fmaf(sl[v][qc], w[v], sum);
+  }
+  if (A.splits > 1 && part == 0) A.ml[head * A.splits + blockIdx.z] = float2{top, sum};
+  const float by = sum != 0.0f ? 1.0f / sum : 0.0f;
+  for (int d = part; d < kDp; d += 4 * NW) {
+    float v = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) v = fmaf(so[k][qc][d], w[k], v);
+    if (A.splits > 1) A.part[(head * A.splits + blockIdx.z) * kDp + d] = v;
+    else if (d < A.dim) out[head * A.dim + d] = from_sum<T>(v * by);
+  }
+}
+
+// ------------------------------------------------------------------ parts
+//
+// A wave a row and head: the parts' weights, then their sums.
+template <typename T>
+__global__ __launch_bounds__(256) void kv_join_kernel(AttnArgs A, int dp, T *__restrict__ out) {
+  KvSeq s;
+  int job;
+  const int rep = A.rep;
+  if (!kv_find(A.B, blockIdx.x, (rep + 15) / 16, [rep](const KvSeq &x) { return (int)(((int64_t)x.n * rep + 15) / 16); }, &s, &job))
+    return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int k = wave; k < 16; k += 4) {
+    const int c = job * 16 + k;
+    if (c >= s.n * rep) return;
+    const int i = c / rep;
+    const int64_t head = (int64_t)(s.lo + i) * A.heads + blockIdx.y * rep + (c - i * rep);
+    const float2 *ml = A.ml + head * A.splits;
+    float top = -INFINITY, sum = 0.0f;
+    for (int z = lane; z < A.splits; z += 64) top = fmaxf(top, ml[z].x);
+    top = wave_max(top);
+    for (int z = lane; z < A.splits; z += 64) sum += top > -INFINITY ? ml[z].y * __builtin_amdgcn_exp2f(ml[z].x - top) : ml[z].y;
+    sum = group_sum<64>(sum);
+    const float by = sum != 0.0f ? 1.0f / sum : 0.0f;
+    const float *p = A.part + head * A.splits * dp;
+    for (int d = lane; d < A.dim; d += 64) {
+      float v = 0.0f;
+      for (int z = 0; z < A.splits; ++z) {
+        const float2 w = ml[z];
+        if (w.y != 0.0f) v = fmaf(p[(int64_t)z * dp + d], top > -INFINITY ? __builtin_amdgcn_exp2f(w.x - top) : w.y, v);
+      }
+      out[head * A.dim + d] = from_sum<T>(v * by);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ dispatch
+
+// Tiles of `of` queries that cover every sequence's rows whatever the offsets are.
+int64_t tiles(int tokens, int seqs, int rep, int of) {
+  const int64_t runs = seqs < tokens ? seqs : tokens;
+  const int64_t a = (int64_t)tokens * rep / of + runs, b = (int64_t)tokens * ((rep + of - 1) / of);
+  return a < b ? a : b;
+}
+
+struct Plan {
+  int chunk, splits;
 };
 
-template <typename T>
-__global__ __launch_bounds__(64) void kv_attention_kernel(AttnArgs A, const T *__restrict__ q, T *__restrict__ out) {
-  __shared__ float qs[kMaxKvDim], p[kPage];
-  KvSeq s;
-  int i;
-  if (!kv_find(A.B, blockIdx.x, 1, [](const KvSeq &x) { return x.n; }, &s, &i)) return;
-  const int h = blockIdx.y, kh = h / (A.heads / A.kv_heads), lane = threadIdx.x;
-  const int64_t row = s.lo + i;
-  for (int c = lane; c < A.dp; c += 64) qs[c] = c < A.dim ? to_f32(q[row * A.qt + h * A.qh + c]) : 0.0f;
-  const int pos = s.first() + i, end = min(pos + 1, kv_limit(A.B, s));
-  const int begin = A.window ? max(0, pos - A.window + 1) : 0;
-  float m = -INFINITY, l = 0.0f, o[kMaxKvDim / 64] = {};
-  for (int pi = begin / kPage; pi * kPage < end; ++pi) {
-    const int page = kv_page(A.B, s, pi);
-    if (page < 0) continue;
-    const int64_t ph = (int64_t)page * A.kv_heads + kh;
-    const int j = pi * kPage + lane;
-    const bool see = j >= begin && j < end;
-    __syncthreads();
-    float sum = 0.0f;
-    const int *kr = reinterpret_cast<const int *>(A.kc + (ph * kPage + lane) * A.dp);
-    for (int c = 0; c < A.dp; c += 4) {
-      const int w = kr[c / 4];
-      sum = fmaf(qs[c], __builtin_amdgcn_cvt_f32_fp8(w, 0), sum);
-      sum = fmaf(qs[c + 1], __builtin_amdgcn_cvt_f32_fp8(w, 1), sum);
-      sum = fmaf(qs[c + 2], __builtin_amdgcn_cvt_f32_fp8(w, 2), sum);
-      sum = fmaf(qs[c + 3], __builtin_amdgcn_cvt_f32_fp8(w, 3), sum);
-    }
-    const float x = see ? sum * (A.ks[ph] * A.scale) : -INFINITY;
-    const float m1 = fmaxf(m, wave_max(x)), ref = m1 > -INFINITY ? m1 : 0.0f;
-    const float e = exp2f(x - ref), alpha = exp2f(m - ref);
-    p[lane] = e;
-    l = fmaf(l, alpha, group_sum<64>(e));
-    m = m1;
-    __syncthreads();
-    const float vs = A.vs[ph];
-    const int lo = max(0, begin - pi * kPage), hi = min(kPage, end - pi * kPage);
-#pragma unroll
-    for (int d = 0; d < kMaxKvDim / 64; ++d) {
-      const int c = d * 64 + lane;
-      if (c >= A.dim) continue;
-      const uint8_t *vr = A.vc + (ph * A.dp + c) * kPage;
-      float part = 0.0f;
-      for (int t = lo; t < hi; ++t) part = fmaf(p[t], __builtin_amdgcn_cvt_f32_fp8((int)vr[t], 0), part);
-      o[d] = fmaf(part, vs, o[d] * alpha);
-    }
-  }
-#pragma unroll
-  for (int d = 0; d < kMaxKvDim / 64; ++d) {
-    const int c = d * 64 + lane;
-    if (c < A.dim) out[(row * A.heads + h) * A.dim + c] = from_sum<T>(l != 0.0f ? o[d] / l : 0.0f);
-  }
+// Pages a workgroup takes.
+Plan plan(int64_t groups, int width) {
+  constexpr int64_t kGroups = 2048;
+  int64_t chunk = (groups * width + kGroups - 1) / kGroups;
+  chunk = chunk < 4 ? 4 : chunk;
+  return {(int)chunk, (int)((width + chunk - 1) / chunk)};
+}
+
+template <typename T, int kDp>
+hipError_t stream(const AttnArgs &A, bool qvec, const T *q, T *out, hipStream_t s) {
+  const unsigned n = (unsigned)tiles(A.B.tokens, A.B.seqs, A.rep, 16);
+  kv_stream_kernel<T, kDp, 4><<<dim3(n, A.kv_heads, A.splits), 256, 0, s>>>(A, qvec, q, out);
+  if (A.splits > 1) kv_join_kernel<T><<<dim3(n, A.kv_heads), 256, 0, s>>>(A, kDp, out);
+  return hipGetLastError();
 }
 
 template <typename T>
 hipError_t run(const AttnArgs &A, const void *q, void *out, hipStream_t s) {
-  kv_attention_kernel<T><<<dim3((unsigned)A.B.tokens, (unsigned)A.heads), 64, 0, s>>>(A, (const T *)q, (T *)out);
-  return hipGetLastError();
+  const int64_t unit = 16 / (int)sizeof(T);
+  const bool vec = ((uintptr_t)q & 15u) == 0 && A.qt % unit == 0 && A.qh % unit == 0;
+  switch (kv_padded_dim(A.dim)) {
+    case 32: return stream<T, 32>(A, vec, (const T *)q, (T *)out, s);
+    case 64: return stream<T, 64>(A, vec, (const T *)q, (T *)out, s);
+    case 96: return stream<T, 96>(A, vec, (const T *)q, (T *)out, s);
+    case 128: return stream<T, 128>(A, vec, (const T *)q, (T *)out, s);
+    case 192: return stream<T, 192>(A, vec, (const T *)q, (T *)out, s);
+    default: return stream<T, 256>(A, vec, (const T *)q, (T *)out, s);
+  }
 }
 
 }  // namespace
+}  // namespace attn
 
-int64_t kv_attention_scratch(int, int, int, int, int, int) { return 0; }
+using namespace attn;
+
+int64_t kv_attention_scratch(int tokens, int seqs, int heads, int kv_heads, int dim, int width) {
+  const Plan p = plan(tiles(tokens, seqs, heads / kv_heads, 16) * kv_heads, width);
+  return p.splits > 1 ? (int64_t)tokens * heads * p.splits * (kv_padded_dim(dim) * 4 + 8) : 0;
+}
 
 hipError_t launch_kv_attention(const KvBatch &B, const void *q, int dtype, int heads, int dim, int64_t qt, int64_t qh,
                                const uint8_t *kc, const uint8_t *vc, const float *ks, const float *vs, int kv_heads,
-                               float scale, int window, void *out, void *, hipStream_t s) {
-  const AttnArgs A{B, heads, kv_heads, dim, kv_padded_dim(dim), window, qt, qh, scale * 1.44269504f, kc, vc, ks, vs};
+                               float scale, int window, void *out, void *scratch, hipStream_t s) {
+  const int rep = heads / kv_heads;
+  Plan p = plan(tiles(B.tokens, B.seqs, rep, 16) * kv_heads, B.width);
+  if (window) {                           // the pages that a tile of up to 16 rows can see
+    const int most = (int)(((int64_t)window + 14) / kPage + 2);
+    if (most < B.width) {
+      p.chunk = (most + p.splits - 1) / p.splits < 4 ? 4 : (most + p.splits - 1) / p.splits;
+      p.splits = (most + p.chunk - 1) / p.chunk;
+    }
+  }
+  float *part = (float *)scratch;
+  float2 *ml = (float2 *)(part + (p.splits > 1 ? (int64_t)B.tokens * heads * p.splits * kv_padded_dim(dim) : 0));
+  const AttnArgs A{B, heads, kv_heads, rep, dim, window, qt, qh, scale * 1.44269504f, kc, vc, ks, vs, p.chunk, p.splits, part, ml};
   if (dtype == BQM_F32) return run<float>(A, q, out, s);
   if (dtype == BQM_BF16) return run<__bf16>(A, q, out, s);
   return run<_Float16>(A, q, out, s);

@@ -103,13 +103,14 @@ def values(cache: dict, pages, s: int, length: int, h: int, dim: int):
 
 
 def attention(q, cache: dict, pages, lens, offsets=None, scale=None, window: int = 0):
-    """(out [tokens, heads, dim], sum of p |v|, the largest sum of |scale q k| that a row sees); rows of no
-    sequence are NaN."""
+    """(out [tokens, heads, dim], sum of p |v|, the largest sum of |scale q k| that a row sees, 2^-40 sum of |v|); rows of
+    no sequence are NaN."""
     q = np.asarray(q, dtype=np.float64)
     tokens, heads, dim = q.shape
     rep = heads // cache["k"].shape[1]
     scale = 1.0 / math.sqrt(dim) if scale is None else scale
     out, mag, most = np.full(q.shape, np.nan), np.zeros(q.shape), np.zeros((tokens, heads))
+    small = np.zeros(q.shape)
     for s, length in enumerate(lens):
         lo, hi = (s, s + 1) if offsets is None else (min(max(0, offsets[s]), tokens), min(max(0, offsets[s + 1]), tokens))
         length = max(0, int(length))
@@ -127,5 +128,6 @@ def attention(q, cache: dict, pages, lens, offsets=None, scale=None, window: int
                 e /= e.sum()
                 out[i, h] = e @ v[see]
                 mag[i, h] = e @ np.abs(v[see])
+                small[i, h] = 2.0 ** -40 * np.abs(v[see]).sum(0)
                 most[i, h] = np.max(abs(scale) * (np.abs(k[see]) @ np.abs(q[i, h])))
-    return out, mag, most
+    return out, mag, most, small

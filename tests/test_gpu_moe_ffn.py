@@ -3,7 +3,7 @@
 The bound, from the arithmetic.  The 128 products of a block are exact in fp32, or cut at 2^-22 (a row of x in one
 or two fp16 terms: its elements below 2^-22 of its largest are off by 2^-33 of that), and added with a rounding of
 2^-23 each; the scaling, the blocks' sum and the waves' round kb + 6 times by 2^-24.  silu is within 4 x 2^-23.  The
-hidden row is rounded to 2^-12 (two terms, 2^-22, for fp32) and goes through the same sums; the experts' weights (6 x
+hidden row is rounded to fp16, half a step of which is up to 2^-11 of it (two terms, 2^-22, for fp32) and goes through the same sums; the experts' weights (6 x
 2^-23) and their sum add 6 + top.  All are relative to the oracle's bound of the terms.
 """
 from __future__ import annotations
@@ -37,7 +37,7 @@ def weights(rng, experts, rows, cols):
 
 def tol(mag, hidden, ffn, top, dtype):
     sums = lambda k: 128 * 2.0 ** -23 + (of8.blocks(k) + 6) * 2.0 ** -24          # noqa: E731
-    return mag * (sums(hidden) + sums(ffn) + (2.0 ** -21 if dtype == torch.float32 else 2.0 ** -12 + 2.0 ** -21) + (16 + top) * 2.0 ** -23)
+    return mag * (sums(hidden) + sums(ffn) + (2.0 ** -21 if dtype == torch.float32 else 2.0 ** -11 + 2.0 ** -21) + (16 + top) * 2.0 ** -23)
 
 
 def check(got, ref, t, dtype, label):

@@ -48,10 +48,10 @@ def test_attention_of_one_key_is_its_value_and_of_none_is_zero():
     k, v = rng.standard_normal((2, 1, 2, 8))
     pages = np.array([[2]])
     okv.append(c, k, v, pages, [1])
-    out, _, _ = okv.attention(rng.standard_normal((1, 4, 8)), c, pages, [1])
+    out, *_ = okv.attention(rng.standard_normal((1, 4, 8)), c, pages, [1])
     want = of8.decode(c["v"][2, :, :8, 0]) * c["v_scale"][2][:, None]
     assert np.allclose(out[0], np.repeat(want, 2, 0))
-    out, _, _ = okv.attention(rng.standard_normal((1, 4, 8)), c, np.array([[-1]]), [1])
+    out, *_ = okv.attention(rng.standard_normal((1, 4, 8)), c, np.array([[-1]]), [1])
     assert np.array_equal(out, np.zeros((1, 4, 8)))
 
 
