@@ -76,7 +76,10 @@ __device__ __forceinline__ void load_q8(const T *p, int c, int dim, bool vec, fl
     load_vec<8>(p + c, v);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < dim ? to_f32(p[c + i]) : 0.0f;
+    for (int i = 0; i < 8; ++i) {
+      const float x = to_f32(p[min(c + i, dim - 1)]);
+      v[i] = c + i < dim ? x : 0.0f;
+    }
   }
 }
 
@@ -100,6 +103,9 @@ __device__ __forceinline__ void pages_of(const AttnArgs &A, const KvSeq &s, int 
   *p0 = begin / kPage;
   *p1 = end > begin ? (end - 1) / kPage + 1 : *p0;
 }
+
+// Tiles of 128 queries (kv_attention_tile.hip).
+hipError_t launch_tiles(const AttnArgs &A, int64_t tiles, bool vec, const void *q, int dtype, void *out, hipStream_t s);
 
 }  // namespace attn
 }  // namespace bqm

@@ -251,37 +251,67 @@ __global__ __launch_bounds__(64 * NW) void kv_stream_kernel(AttnArgs A, bool qve
 
 // ------------------------------------------------------------------ parts
 //
-// A wave a row and head: the parts' weights, then their sums.
-template <typename T>
-__global__ __launch_bounds__(256) void kv_join_kernel(AttnArgs A, int dp, T *__restrict__ out) {
-  KvSeq s;
-  int job;
-  const int rep = A.rep;
-  if (!kv_find(A.B, blockIdx.x, (rep + 15) / 16, [rep](const KvSeq &x) { return (int)(((int64_t)x.n * rep + 15) / 16); }, &s, &job))
-    return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int k = wave; k < 16; k += 4) {
-    const int c = job * 16 + k;
-    if (c >= s.n * rep) return;
-    const int i = c / rep;
-    const int64_t head = (int64_t)(s.lo + i) * A.heads + blockIdx.y * rep + (c - i * rep);
-    const float2 *ml = A.ml + head * A.splits;
-    float top = -INFINITY, sum = 0.0f;
-    for (int z = lane; z < A.splits; z += 64) top = fmaxf(top, ml[z].x);
-    top = wave_max(top);
-    for (int z = lane; z < A.splits; z += 64) sum += top > -INFINITY ? ml[z].y * __builtin_amdgcn_exp2f(ml[z].x - top) : ml[z].y;
-    sum = group_sum<64>(sum);
-    const float by = sum != 0.0f ? 1.0f / sum : 0.0f;
-    const float *p = A.part + head * A.splits * dp;
-    for (int d = lane; d < A.dim; d += 64) {
-      float v = 0.0f;
-      for (int z = 0; z < A.splits; ++z) {
-        const float2 w = ml[z];
-        if (w.y != 0.0f) v = fmaf(p[(int64_t)z * dp + d], top > -INFINITY ? __builtin_amdgcn_exp2f(w.x - top) : w.y, v);
-      }
-      out[head * A.dim + d] = from_sum<T>(v * by);
-    }
+// kThreads a row and head: they first weigh the parts, then sum them, four columns a thread and kRows
+// parts at a time.
+constexpr int kMaxParts = 2048, kFewParts = 16;
+
+template <typename T, int kDp, int kThreads>
+__global__ __launch_bounds__(256) void kv_join_kernel(AttnArgs A, T *__restrict__ out) {
+  constexpr int kLanes = kDp / 4, kRows = kThreads / kLanes, kEach = 256 / kThreads, kWavesEach = kThreads / 64;
+  constexpr int kParts = kThreads == 64 ? kFewParts : kMaxParts;
+  __shared__ float w[kEach][kParts], red[2][4];
+  __shared__ f32x4_t sums[kEach][kRows][kLanes];
+  const int row = blockIdx.x, e = threadIdx.x / kThreads, x = threadIdx.x % kThreads;
+  if (A.B.offsets && (row < A.B.offsets[0] || row >= A.B.offsets[A.B.seqs])) return;     // a row of no sequence
+  const int h = blockIdx.y * kEach + e, wave = threadIdx.x >> 6, first = e * kWavesEach;
+  const int64_t head = (int64_t)row * A.heads + min(h, A.heads - 1);
+  const float2 *ml = A.ml + head * A.splits;
+  float top = -INFINITY, sum = 0.0f;
+  for (int z = x; z < A.splits; z += kThreads) top = fmaxf(top, ml[z].x);
+  top = wave_max(top);
+  if constexpr (kWavesEach > 1) {
+    if ((threadIdx.x & 63) == 0) red[0][wave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < kWavesEach; ++v) top = fmaxf(top, red[0][first + v]);
   }
+  for (int z = x; z < A.splits; z += kThreads) {
+    const float2 v = ml[z];
+    // no maximum anywhere: nothing was seen (0), or NaN
+    const float f = v.y == 0.0f ? 0.0f : top > -INFINITY ? __builtin_amdgcn_exp2f(v.x - top) : v.y;
+    w[e][z] = f;
+    sum = fmaf(v.y, f, sum);
+  }
+  sum = group_sum<64>(sum);
+  if ((threadIdx.x & 63) == 0) red[1][wave] = sum;
+  __syncthreads();
+  sum = 0.0f;
+#pragma unroll
+  for (int v = 0; v < kWavesEach; ++v) sum += red[1][first + v];
+  const int d = x % kLanes, r = x / kLanes;
+  const f32x4_t *p = reinterpret_cast<const f32x4_t *>(A.part + head * A.splits * kDp) + d;
+  if (r < kRows) {
+    f32x4_t acc = {};
+#pragma unroll 4
+    for (int z = r; z < A.splits; z += kRows) {
+      const float f = w[e][z];
+      if (f != 0.0f) {                                                   // others may not have been written
+        const f32x4_t v = p[(int64_t)z * kLanes];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(v[i], f, acc[i]);
+      }
+    }
+    sums[e][r][d] = acc;
+  }
+  __syncthreads();
+  if (x >= kLanes || h >= A.heads) return;
+  const float by = sum != 0.0f ? 1.0f / sum : 0.0f;
+  f32x4_t acc = sums[e][0][d];
+#pragma unroll
+  for (int k = 1; k < kRows; ++k) acc += sums[e][k][d];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (d * 4 + i < A.dim) out[head * A.dim + d * 4 + i] = from_sum<T>(acc[i] * by);
 }
 
 // ------------------------------------------------------------------ dispatch
@@ -294,36 +324,71 @@ int64_t tiles(int tokens, int seqs, int rep, int of) {
 }
 
 struct Plan {
+  bool many;                              // tiles of 128 queries
+  int64_t tiles;
   int chunk, splits;
 };
 
-// Pages a workgroup takes.
-Plan plan(int64_t groups, int width) {
-  constexpr int64_t kGroups = 2048;
-  int64_t chunk = (groups * width + kGroups - 1) / kGroups;
-  chunk = chunk < 4 ? 4 : chunk;
-  return {(int)chunk, (int)((width + chunk - 1) / chunk)};
+int64_t above(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Few rows: the pages a workgroup takes are such that there are two workgroups a CU where all sequences are as
+// long as the table is wide, but 4 at least (one a wave) and 32 at most, so that sequences of unlike length
+// share the CUs (us, 8 key heads: one sequence of 131072 in chunks of 32 / 16 / 8 / 4 pages: 58 / 64 / 75 / 96; 64
+// of up to 8192 in chunks of 128 / 32 / 16: 121 / 110 / 118).  The parts of all workgroups are bounded too.
+Plan plan(int tokens, int seqs, int heads, int kv_heads, int width, int window) {
+  constexpr int64_t kGroups = 512, kMostGroups = 4096;
+  const int rep = heads / kv_heads;
+  const int64_t runs = seqs < tokens ? seqs : tokens;
+  Plan p;
+  p.many = (int64_t)tokens * rep >= 64 * runs;
+  p.tiles = tiles(tokens, seqs, rep, p.many ? 128 : 16);
+  const int64_t work = p.tiles * kv_heads * width;
+  int64_t chunk = above(work, kGroups);
+  if (p.many) {
+    chunk = p.tiles * kv_heads >= kGroups ? width : chunk < 16 ? 16 : chunk;
+  } else {
+    chunk = chunk < 4 ? 4 : chunk > 32 ? 32 : chunk;
+    if (chunk < above(work, kMostGroups)) chunk = above(work, kMostGroups);
+  }
+  if (chunk < above(width, kMaxParts)) chunk = above(width, kMaxParts);
+  p.splits = (int)above(width, chunk);
+  // a window: the pages that a tile's rows can see, in no more parts
+  const int64_t most = ((int64_t)window + (p.many ? 128 : 16)) / kPage + 2;
+  if (window && most < width) {
+    if (chunk > above(most, p.splits)) chunk = above(most, p.splits);
+    if (chunk < 4) chunk = 4;
+    p.splits = (int)above(most, chunk);
+  }
+  p.chunk = (int)chunk;
+  return p;
 }
 
 template <typename T, int kDp>
-hipError_t stream(const AttnArgs &A, bool qvec, const T *q, T *out, hipStream_t s) {
-  const unsigned n = (unsigned)tiles(A.B.tokens, A.B.seqs, A.rep, 16);
-  kv_stream_kernel<T, kDp, 4><<<dim3(n, A.kv_heads, A.splits), 256, 0, s>>>(A, qvec, q, out);
-  if (A.splits > 1) kv_join_kernel<T><<<dim3(n, A.kv_heads), 256, 0, s>>>(A, kDp, out);
+hipError_t start(const AttnArgs &A, const Plan &p, bool vec, const T *q, T *out, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  if (p.many) {
+    e = launch_tiles(A, p.tiles, vec, q, std::is_same_v<T, float> ? BQM_F32 : std::is_same_v<T, __bf16> ? BQM_BF16 : BQM_F16, out, s);
+  } else {
+    kv_stream_kernel<T, kDp, 4><<<dim3((unsigned)p.tiles, A.kv_heads, A.splits), 256, 0, s>>>(A, vec, q, out);
+    e = hipGetLastError();
+  }
+  if (e != hipSuccess || A.splits == 1) return e;
+  if (A.splits <= kFewParts) kv_join_kernel<T, kDp, 64><<<dim3(A.B.tokens, (A.heads + 3) / 4), 256, 0, s>>>(A, out);
+  else kv_join_kernel<T, kDp, 256><<<dim3(A.B.tokens, A.heads), 256, 0, s>>>(A, out);
   return hipGetLastError();
 }
 
 template <typename T>
-hipError_t run(const AttnArgs &A, const void *q, void *out, hipStream_t s) {
+hipError_t run(const AttnArgs &A, const Plan &p, const void *q, void *out, hipStream_t s) {
   const int64_t unit = 16 / (int)sizeof(T);
   const bool vec = ((uintptr_t)q & 15u) == 0 && A.qt % unit == 0 && A.qh % unit == 0;
   switch (kv_padded_dim(A.dim)) {
-    case 32: return stream<T, 32>(A, vec, (const T *)q, (T *)out, s);
-    case 64: return stream<T, 64>(A, vec, (const T *)q, (T *)out, s);
-    case 96: return stream<T, 96>(A, vec, (const T *)q, (T *)out, s);
-    case 128: return stream<T, 128>(A, vec, (const T *)q, (T *)out, s);
-    case 192: return stream<T, 192>(A, vec, (const T *)q, (T *)out, s);
-    default: return stream<T, 256>(A, vec, (const T *)q, (T *)out, s);
+    case 32: return start<T, 32>(A, p, vec, (const T *)q, (T *)out, s);
+    case 64: return start<T, 64>(A, p, vec, (const T *)q, (T *)out, s);
+    case 96: return start<T, 96>(A, p, vec, (const T *)q, (T *)out, s);
+    case 128: return start<T, 128>(A, p, vec, (const T *)q, (T *)out, s);
+    case 192: return start<T, 192>(A, p, vec, (const T *)q, (T *)out, s);
+    default: return start<T, 256>(A, p, vec, (const T *)q, (T *)out, s);
   }
 }
 
@@ -333,28 +398,20 @@ hipError_t run(const AttnArgs &A, const void *q, void *out, hipStream_t s) {
 using namespace attn;
 
 int64_t kv_attention_scratch(int tokens, int seqs, int heads, int kv_heads, int dim, int width) {
-  const Plan p = plan(tiles(tokens, seqs, heads / kv_heads, 16) * kv_heads, width);
+  const Plan p = plan(tokens, seqs, heads, kv_heads, width, 0);
   return p.splits > 1 ? (int64_t)tokens * heads * p.splits * (kv_padded_dim(dim) * 4 + 8) : 0;
 }
 
 hipError_t launch_kv_attention(const KvBatch &B, const void *q, int dtype, int heads, int dim, int64_t qt, int64_t qh,
                                const uint8_t *kc, const uint8_t *vc, const float *ks, const float *vs, int kv_heads,
                                float scale, int window, void *out, void *scratch, hipStream_t s) {
-  const int rep = heads / kv_heads;
-  Plan p = plan(tiles(B.tokens, B.seqs, rep, 16) * kv_heads, B.width);
-  if (window) {                           // the pages that a tile of up to 16 rows can see
-    const int most = (int)(((int64_t)window + 14) / kPage + 2);
-    if (most < B.width) {
-      p.chunk = (most + p.splits - 1) / p.splits < 4 ? 4 : (most + p.splits - 1) / p.splits;
-      p.splits = (most + p.chunk - 1) / p.chunk;
-    }
-  }
+  const Plan p = plan(B.tokens, B.seqs, heads, kv_heads, B.width, window);
   float *part = (float *)scratch;
   float2 *ml = (float2 *)(part + (p.splits > 1 ? (int64_t)B.tokens * heads * p.splits * kv_padded_dim(dim) : 0));
-  const AttnArgs A{B, heads, kv_heads, rep, dim, window, qt, qh, scale * 1.44269504f, kc, vc, ks, vs, p.chunk, p.splits, part, ml};
-  if (dtype == BQM_F32) return run<float>(A, q, out, s);
-  if (dtype == BQM_BF16) return run<__bf16>(A, q, out, s);
-  return run<_Float16>(A, q, out, s);
+  const AttnArgs A{B, heads, kv_heads, heads / kv_heads, dim, window, qt, qh, scale * 1.44269504f, kc, vc, ks, vs, p.chunk, p.splits, part, ml};
+  if (dtype == BQM_F32) return run<float>(A, p, q, out, s);
+  if (dtype == BQM_BF16) return run<__bf16>(A, p, q, out, s);
+  return run<_Float16>(A, p, q, out, s);
 }
 
 }  // namespace bqm
