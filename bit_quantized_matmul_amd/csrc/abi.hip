@@ -738,8 +738,7 @@ int moe_ffn(const void *x, int dtype, int tokens, int hidden, int64_t x_stride, 
   rc = current_device(&cus);
   if (rc) return rc;
   return status_of(launch_moe_ffn(x, dtype, tokens, hidden, x_stride, logits, logits_dtype, logits_stride, experts, top,
-                                  renorm != 0, w13, w13_scale, w2, w2_scale, ffn, out, workspace, cus,
-                                  (hipStream_t)stream));
+                                  renorm != 0, w13, w13_scale, w2, w2_scale, ffn, out, workspace, (hipStream_t)stream));
 }
 
 const char *bqm_strerror(int code) {

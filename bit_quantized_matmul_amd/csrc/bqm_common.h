@@ -192,8 +192,7 @@ constexpr int kMoeFewTokens = 32;
 int64_t moe_ffn_scratch(int tokens, int experts, int top, int hidden, int ffn);
 hipError_t launch_moe_ffn(const void *x, int dtype, int tokens, int hidden, int64_t xs, const void *logits, int ltype,
                           int64_t ls, int experts, int top, bool renorm, const uint8_t *w13, const float *s13,
-                          const uint8_t *w2, const float *s2, int ffn, void *out, void *scratch, int num_cus,
-                          hipStream_t s);
+                          const uint8_t *w2, const float *s2, int ffn, void *out, void *scratch, hipStream_t s);
 hipError_t launch_codebook_fit(const double *samples, int64_t n, int levels, int iters,
                                double *raw, float *table, hipStream_t s);
 

@@ -49,6 +49,9 @@ struct MoeArgs {
   const float *s13, *s2;
   MoeList *list;                          // workspace
   __bf16 *act;                            // [terms, tokens * top, 128 ceil(ffn / 128)]
+  float *part;                            // [row tiles, splits, 32 tokens, 16 rows], with splits > 1
+  int *arrived;                           // [row tiles]
+  int splits;
 };
 
 template <typename T> constexpr int kXTerms = sizeof(T) == 4 ? 3 : 1;
@@ -111,9 +114,9 @@ __device__ __forceinline__ void load_x8(const T *p, int c, int cols, bool vec, H
 
 struct Choices {
   uint32_t tokens[kMaxExperts];           // by expert
+  int16_t first[kMaxExperts];             // of its pairs
   int16_t ids[kMaxPairs];                 // [tokens, top]
   float weights[kMaxPairs];
-  float by_place[kMaxPairs];              // in the pairs' order
   uint32_t sums[kUpWaves];
 };
 
@@ -143,8 +146,8 @@ __device__ __forceinline__ void choose_all(const MoeArgs &A, Choices &C) {
 }
 static_assert(kUpWaves * 64 / 16 >= kMoeFewTokens, "16 lanes a token");
 
-// The experts that have tokens into `L` (LDS), the weights in the pairs' order.
-__device__ void list_experts(const MoeArgs &A, Choices &C, MoeList &L) {
+// The experts that have tokens into `L` and the weights in the pairs' order into `by_place` (LDS).
+__device__ void list_experts(const MoeArgs &A, Choices &C, MoeList &L, float *by_place) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   constexpr int kThreads = kUpWaves * 64, kPer = kMaxExperts / kThreads;
   for (int e = tid; e < A.experts; e += kThreads) C.tokens[e] = 0;
@@ -177,20 +180,15 @@ __device__ void list_experts(const MoeArgs &A, Choices &C, MoeList &L) {
     L.expert[at >> 16] = tid * kPer + i;
     L.tokens[at >> 16] = mask[i];
     L.first[at >> 16] = (int)(at & 0xFFFFu);
+    C.first[tid * kPer + i] = (int16_t)(at & 0xFFFFu);
     at += (1u << 16) + (uint32_t)__popc(mask[i]);
   }
   if (tid == 0) L.count = (int)(all >> 16);
   __syncthreads();
   // a pair's place: its expert's first, and the expert's tokens before it
-  for (int a = wave; a < L.count; a += kUpWaves) {
-    const int e = L.expert[a], t = lane & 31;
-    const uint32_t m = L.tokens[a];
-    if (lane < 32 && (m >> t & 1)) {
-      float w = 0.0f;
-      for (int j = 0; j < A.top; ++j)
-        if (C.ids[t * A.top + j] == e) w = C.weights[t * A.top + j];
-      C.by_place[L.first[a] + __popc(m & ((1u << t) - 1u))] = w;
-    }
+  for (int i = tid; i < A.tokens * A.top; i += kThreads) {
+    const int e = C.ids[i], tok = i / A.top;
+    if (e >= 0) by_place[C.first[e] + __popc(C.tokens[e] & ((1u << tok) - 1u))] = C.weights[i];
   }
   __syncthreads();
 }
@@ -218,29 +216,34 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
 }
 
 // ------------------------------------------------------------------ gate and up
-
-template <typename T>
-__global__ __launch_bounds__(64 * kUpWaves, 2) void moe_up_kernel(MoeArgs A, bool xvec, const T *__restrict__ x) {
+//
+// kGroups groups of waves take an item each, so that short rows keep all waves busy.  The sums of an item meet in one
+// of two buffers; its group's waves add them up and form the hidden rows in turn, while the others go on.
+template <typename T, int kGroups>
+__global__ __launch_bounds__(64 * kUpWaves, sizeof(T) == 2 ? 4 : 2) void moe_up_kernel(MoeArgs A, bool xvec, const T *__restrict__ x) {
   using H = Half8<T>;
-  constexpr int NW = kUpWaves, kTerms = kXTerms<T>, kDepth = 2;
-  __shared__ Choices C;
+  constexpr int NW = kUpWaves / kGroups, kTerms = kXTerms<T>, kDepth = 2;
+  __shared__ union {
+    Choices C;
+    f32x4_t red[2][kGroups][NW][2][64];
+  } lds;
   __shared__ MoeList L;
-  __shared__ f32x4_t red[NW][2][64];
-  list_experts(A, C, L);
+  __shared__ float by_place[kMaxPairs];
+  list_experts(A, lds.C, L, by_place);
   if (blockIdx.x == 0) {
     const int *from = reinterpret_cast<const int *>(&L);
-    for (int i = threadIdx.x; i < (int)(sizeof(MoeList) / 4); i += NW * 64) reinterpret_cast<int *>(A.list)[i] = from[i];
+    for (int i = threadIdx.x; i < (int)(sizeof(MoeList) / 4); i += kUpWaves * 64) reinterpret_cast<int *>(A.list)[i] = from[i];
+    for (int i = threadIdx.x; i < (A.hidden + kTile - 1) / kTile; i += kUpWaves * 64) A.arrived[i] = 0;
   }
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int row = lane & 15, grp = lane >> 4;
+  const int lane = threadIdx.x & 63, wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = wave_all / NW, wave = wave_all % NW, row = lane & 15, grp = lane >> 4;
   const int kb = (A.hidden + kBlk - 1) / kBlk, nb = (2 * A.ffn + kBlk - 1) / kBlk;
   const int fp = (A.ffn + kBlk - 1) / kBlk * kBlk, tiles = fp / kTile;
-  const int64_t kp = (int64_t)kb * kBlk;
-  const int items = L.count * tiles;
+  const int64_t kp = (int64_t)kb * kBlk, plane = (int64_t)A.tokens * A.top * fp;
+  const int items = L.count * tiles, stride = gridDim.x * kGroups;
   i32x4 wl[kDepth][2][2] = {};
   auto load_w = [&](int item, int b0) {
     const int a = item / tiles, n0 = (item - a * tiles) * kTile;
-    if (n0 >= A.ffn) return;
     const uint8_t *g = A.w13 + ((int64_t)L.expert[a] * 2 * A.ffn + min(n0 + row, A.ffn - 1)) * kp + grp * 16;
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
@@ -255,213 +258,278 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void moe_up_kernel(MoeArgs A, boo
       }
     }
   };
-  int item = blockIdx.x;
+  int item = blockIdx.x * kGroups + group, turn = 0, c0 = 0;             // c0: the first of an item's tokens, 16 at a time
   if (item < items) load_w(item, wave);
-  for (; item < items; item += gridDim.x) {
-    const int a = item / tiles, n0 = (item - a * tiles) * kTile, e = L.expert[a];
+  // every group of the workgroup makes as many turns as the longest: they meet once a turn
+  int turns = 0;
+  for (int g = 0; g < kGroups; ++g) {
+    int n = 0;
+    for (int i = blockIdx.x * kGroups + g; i < items; i += stride) n += (__popc(L.tokens[i / tiles]) + 15) / 16;
+    turns = max(turns, n);
+  }
+  for (; turn < turns; ++turn) {
+    const bool live = item < items;
+    const int a = live ? item / tiles : 0, n0 = (item - a * tiles) * kTile;
     const uint32_t mask = L.tokens[a];
-    const int count = __popc(mask), p0 = L.first[a], next = item + gridDim.x;
-    const int64_t plane = (int64_t)A.tokens * A.top * fp;
-    if (n0 >= A.ffn) {                                                   // columns that pad the hidden rows: zeros
-      for (int i = threadIdx.x; i < count * kTile * kActTerms<T>; i += NW * 64) {
-        const int z = i / (count * kTile), j = i - z * count * kTile;
-        A.act[z * plane + (int64_t)(p0 + j / kTile) * fp + n0 + j % kTile] = (__bf16)0.0f;
-      }
-      if (next < items) load_w(next, wave);
-      continue;
-    }
-    // scales: the gate rows lie in one block; the up rows may cross into the next from row `cross` on
-    const float *sg = A.s13 + ((int64_t)e * nb + n0 / kBlk) * kb;
-    const int u0 = A.ffn + n0, ub = u0 / kBlk, cross = (ub + 1) * kBlk - u0;
-    const float *su = A.s13 + ((int64_t)e * nb + ub) * kb, *su1 = ub + 1 < nb ? su + kb : su;
-    for (int c0 = 0; c0 < count; c0 += 16) {                             // 16 tokens at a time
-      const bool last = c0 + 16 >= count;
-      const int tok = nth_bit(mask, min(c0 + row, count - 1));
-      const T *xr = x + tok * A.xs;
+    const int count = __popc(mask), p0 = L.first[a] + c0;
+    const bool last = c0 + 16 >= count;
+    const int next = last ? item + stride : item;
+    if (live) {
+      const int e = L.expert[a];
+      // scales: the gate rows lie in one block; the up rows may cross into the next from row `cross` on
+      const float *sg = A.s13 + ((int64_t)e * nb + min(n0, A.ffn - 1) / kBlk) * kb;
+      const int u0 = A.ffn + min(n0, A.ffn - 1), ub = u0 / kBlk, cross = (ub + 1) * kBlk - u0;
+      const float *su = A.s13 + ((int64_t)e * nb + ub) * kb, *su1 = ub + 1 < nb ? su + kb : su;
+      const T *xr = x + nth_bit(mask, min(c0 + row, count - 1)) * A.xs;
       f32x4_t acc[2] = {};
       for (int b0 = wave; b0 < kb; b0 += NW * kDepth) {
-        H wh[kDepth][2][4];
+        H xh[kDepth][4][kTerms];
+        float s[kDepth][3];
 #pragma unroll
-        for (int d = 0; d < kDepth; ++d)
+        for (int d = 0; d < kDepth; ++d) {
+          const int b = b0 + d * NW;
+          if (b < kb) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) wh[d][h][k] = widen_as<H>(wl[d][h][k / 2][2 * (k & 1)], wl[d][h][k / 2][2 * (k & 1) + 1]);
-        // the codes after these: of this item, of its next tokens, of the next item
-        if (b0 + NW * kDepth < kb) load_w(item, b0 + NW * kDepth);
-        else if (!last) load_w(item, wave);
-        else if (next < items) load_w(next, wave);
+            for (int k = 0; k < 4; ++k) load_x8(xr, b * kBlk + (k / 2) * 64 + grp * 16 + (k & 1) * 8, A.hidden, xvec, xh[d][k]);
+            s[d][0] = sg[b], s[d][1] = su[b], s[d][2] = su1[b];
+          }
+        }
 #pragma unroll
         for (int d = 0; d < kDepth; ++d) {
           const int b = b0 + d * NW;
           if (b < kb) {
             f32x4_t part[2] = {};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              H xh[kTerms];
-              load_x8(xr, b * kBlk + (k / 2) * 64 + grp * 16 + (k & 1) * 8, A.hidden, xvec, xh);
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
+              for (int h = 0; h < 2; ++h) {
+                const H w = widen_as<H>(wl[d][h][k / 2][2 * (k & 1)], wl[d][h][k / 2][2 * (k & 1) + 1]);
 #pragma unroll
-                for (int z = 0; z < kTerms; ++z) part[h] = product(wh[d][h][k], xh[z], part[h]);
-            }
-            const float g = sg[b], u = su[b], u1 = su1[b];
+                for (int z = 0; z < kTerms; ++z) part[h] = product(w, xh[d][k][z], part[h]);
+              }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              acc[0][i] = fmaf(part[0][i], g, acc[0][i]);
-              acc[1][i] = fmaf(part[1][i], grp * 4 + i < cross ? u : u1, acc[1][i]);
+              acc[0][i] = fmaf(part[0][i], s[d][0], acc[0][i]);
+              acc[1][i] = fmaf(part[1][i], grp * 4 + i < cross ? s[d][1] : s[d][2], acc[1][i]);
             }
           }
         }
+        // the codes after these: of this item, or of the next turn
+        if (b0 + NW * kDepth < kb) load_w(item, b0 + NW * kDepth);
+        else if (next < items) load_w(next, wave);
       }
+      if (wave >= kb && next < items) load_w(next, wave);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) red[wave][h][lane] = acc[h];
-      __syncthreads();
-      if (wave == 0 && c0 + row < count) {
-        f32x4_t s[2] = {red[0][0][lane], red[0][1][lane]};
-#pragma unroll
-        for (int v = 1; v < NW; ++v)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) s[h] += red[v][h][lane];
-        const float w = C.by_place[p0 + c0 + row];
-        bf16x4 t[kActTerms<T>];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float r = n0 + grp * 4 + i < A.ffn ? silu_mul(s[0][i], s[1][i]) * w : 0.0f;
-#pragma unroll
-          for (int z = 0; z < kActTerms<T>; ++z) {
-            t[z][i] = (__bf16)r;
-            r -= (float)t[z][i];
-          }
-        }
-#pragma unroll
-        for (int z = 0; z < kActTerms<T>; ++z)
-          *reinterpret_cast<bf16x4 *>(A.act + z * plane + (int64_t)(p0 + c0 + row) * fp + n0 + grp * 4) = t[z];
-      }
-      __syncthreads();
+      for (int h = 0; h < 2; ++h) lds.red[turn & 1][group][wave][h][lane] = acc[h];
     }
+    __syncthreads();
+    if (live && wave == turn % NW && c0 + row < count) {
+      f32x4_t s[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        s[h] = lds.red[turn & 1][group][0][h][lane];
+#pragma unroll
+        for (int v = 1; v < NW; ++v) s[h] += lds.red[turn & 1][group][v][h][lane];
+      }
+      const float w = by_place[p0 + row];
+      bf16x4 t[kActTerms<T>];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float r = n0 + grp * 4 + i < A.ffn ? silu_mul(s[0][i], s[1][i]) * w : 0.0f;      // zeros in the columns that pad
+#pragma unroll
+        for (int z = 0; z < kActTerms<T>; ++z) {
+          t[z][i] = (__bf16)r;
+          r -= (float)t[z][i];
+        }
+      }
+#pragma unroll
+      for (int z = 0; z < kActTerms<T>; ++z)
+        *reinterpret_cast<bf16x4 *>(A.act + z * plane + (int64_t)(p0 + row) * fp + n0 + grp * 4) = t[z];
+    }
+    c0 = last ? 0 : c0 + 16;
+    item = next;
   }
 }
 
 // ------------------------------------------------------------------ down and combination
+//
+// An item is kDepth blocks of an expert's 16 rows for 16 of its tokens; its products go to the tokens' sums in the
+// wave's own part of LDS.  The hidden rows come through LDS as well, without passing through registers: an
+// expert has few tokens, and a load of an operand, of which most lanes would hold no token, takes as long as a load
+// of codes (32 tokens of 64 experts of 2048 x 1024: 43 us with operands loaded, 24 without them).
+// Where there are fewer row tiles than CUs the items of one are shared out to several workgroups; the last to
+// arrive adds up their sums, in their order.
+typedef __attribute__((address_space(3))) void lds_void;
 
-template <typename T, int MF>
+template <typename T>
 __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down_kernel(MoeArgs A, T *__restrict__ out) {
-  constexpr int NW = kDownWaves, kTerms = kActTerms<T>, kDepth = MF * kTerms <= 2 ? 4 : MF * kTerms <= 4 ? 2 : 1;
-  __shared__ f32x4_t red[NW][MF][64];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  constexpr int NW = kDownWaves, kTerms = kActTerms<T>, kDepth = kTerms == 2 ? 2 : 1;
+  constexpr int kChunks = 16 * kTerms, kActBytes = 16 * kChunks * 16;    // 16-byte chunks of a token's block; of 16 tokens
+  __shared__ __align__(1024) uint8_t rows_lds[NW][kDepth][kActBytes];
+  __shared__ f32x4_t sums[NW][kMoeFewTokens][4];                         // [wave][token][rows / 4]
+  __shared__ uint32_t tokens[kMaxExperts];
+  __shared__ uint32_t expert_first[kMaxExperts];                         // expert, and its first pair in the upper half
+  __shared__ int before;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row = lane & 15, grp = lane >> 4, n0 = blockIdx.x * kTile;
-  const int fb = (A.ffn + kBlk - 1) / kBlk, nb = (A.hidden + kBlk - 1) / kBlk;
-  const int64_t fp = (int64_t)fb * kBlk, plane = A.tokens * A.top * fp;
-  const MoeList &L = *A.list;
-  const int items = L.count * fb;
-  f32x4_t acc[MF] = {};
+  const int most = min(A.experts, A.tokens * A.top), listed = A.list->count;
+  for (int i = tid; i < most; i += NW * 64) {
+    expert_first[i] = (uint32_t)A.list->expert[i] | (uint32_t)A.list->first[i] << 16;
+    tokens[i] = A.list->tokens[i];
+  }
+#pragma unroll
+  for (int i = 0; i < kMoeFewTokens * 4 / 64; ++i) (&sums[wave][0][0])[i * 64 + lane] = f32x4_t{};
+  __syncthreads();
+  const int fb = (A.ffn + kBlk - 1) / kBlk, nb = (A.hidden + kBlk - 1) / kBlk, each = (fb + kDepth - 1) / kDepth;
+  const int64_t fp = (int64_t)fb * kBlk, plane = (int64_t)A.tokens * A.top * fp;
+  const int items = listed * each, stride = NW * A.splits;
   const int64_t r0 = min(n0 + row, A.hidden - 1);
-  i32x4 wl[kDepth][2];
-  float sl[kDepth];
-  auto load_w = [&](int i0) {
+
+  i32x4 wl[kDepth][2] = {};
+  float sl[kDepth] = {};
+  auto load = [&](int item, int c0) {
+    const int a = item / each, b0 = (item - a * each) * kDepth;
+    const uint32_t ef = __builtin_amdgcn_readfirstlane((int)expert_first[a]), e = ef & 0xFFFFu;
+    const int count = min((int)__popc(__builtin_amdgcn_readfirstlane((int)tokens[a])) - c0, 16);
+    const uint8_t *p = A.w2 + ((int64_t)e * A.hidden + r0) * fp + grp * 16;
+    const __bf16 *q = A.act + (int64_t)((ef >> 16) + c0) * fp;
+    const float *s = A.s2 + ((int64_t)e * nb + n0 / kBlk) * fb;
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
-      const int i = i0 + d * NW;
-      if (i < items) {
-        const int a = i / fb, b = i - a * fb, e = L.expert[a];
-        const uint8_t *p = A.w2 + ((int64_t)e * A.hidden + r0) * fp + b * kBlk + grp * 16;
-        wl[d][0] = *reinterpret_cast<const i32x4 *>(p);
-        wl[d][1] = *reinterpret_cast<const i32x4 *>(p + 64);
-        sl[d] = A.s2[((int64_t)e * nb + n0 / kBlk) * fb + b];
+      const int b = min(b0 + d, fb - 1);
+      wl[d][0] = *reinterpret_cast<const i32x4 *>(p + b * kBlk);
+      wl[d][1] = *reinterpret_cast<const i32x4 *>(p + b * kBlk + 64);
+      sl[d] = s[b];
+      // chunk c of token t lies at c ^ t: 16 tokens' chunks c in 16 groups of four banks
+#pragma unroll
+      for (int i = 0; i < kActBytes / 1024; ++i) {
+        if (i * 64 < count * kChunks) {
+          const int slot = i * 64 + lane, t = slot / kChunks, c = (slot - t * kChunks) ^ t;
+          const __bf16 *from = q + min(t, count - 1) * fp + (c / 16) * plane + b * kBlk + (c % 16) * 8;
+          __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                           (lds_void *)(&rows_lds[wave][d][0] + i * 1024), 16, 0, 0);
+        }
       }
     }
   };
-  load_w(wave);
-  for (int i0 = wave; i0 < items; i0 += NW * kDepth) {
-    bf16x8 al[kDepth][MF][4][kTerms], wh[kDepth][4];
+  int item = blockIdx.y * NW + wave, c0 = 0;
+  if (item < items) load(item, 0);
+  while (item < items) {
+    const uint32_t mask = tokens[item / each];
+    const int count = __popc(mask), at = min(c0 + row, count - 1), tok = nth_bit(mask, at), b0 = item % each * kDepth;
+    const bool mine = c0 + row < count, last = c0 + 16 >= count;
+    const int next = last ? item + stride : item, next_c = last ? 0 : c0 + 16;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");                     // this item's rows and codes have landed
+    bf16x8 al[kDepth][4][kTerms], wh[kDepth][4];
     float s[kDepth];
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
-      const int i = i0 + d * NW;
-      if (i >= items) break;
-      const int a = i / fb, b = i - a * fb;
-      const uint32_t mask = L.tokens[a];
-#pragma unroll
-      for (int f = 0; f < MF; ++f) {
-        const int t = f * 16 + row;
-        const bool has = mask >> t & 1;
-        const __bf16 *q = A.act + (L.first[a] + __popc(mask & ((1u << t) - 1u))) * fp + b * kBlk + grp * 16;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int z = 0; z < kTerms; ++z) {
-            al[d][f][k][z] = bf16x8{};
-            if (has) al[d][f][k][z] = *reinterpret_cast<const bf16x8 *>(q + z * plane + (k / 2) * 64 + (k & 1) * 8);
-          }
-      }
-    }
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
       s[d] = sl[d];
+      const uint8_t *from = &rows_lds[wave][d][0] + (at - c0) * (kChunks * 16);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) wh[d][k] = widen_as<bf16x8>(wl[d][k / 2][2 * (k & 1)], wl[d][k / 2][2 * (k & 1) + 1]);
-    }
-    load_w(i0 + NW * kDepth);
+      for (int k = 0; k < 4; ++k) {
+        const int c = ((k / 2) * 8 + grp * 2 + (k & 1)) ^ (at - c0);
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
-      if (i0 + d * NW >= items) break;
-#pragma unroll
-      for (int f = 0; f < MF; ++f) {
-        f32x4_t part = {};
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int z = 0; z < kTerms; ++z) part = product(wh[d][k], al[d][f][k][z], part);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[f][i] = fmaf(part[i], s[d], acc[f][i]);
+        for (int z = 0; z < kTerms; ++z) al[d][k][z] = *reinterpret_cast<const bf16x8 *>(from + z * 256 + c * 16);
+        wh[d][k] = widen_as<bf16x8>(wl[d][k / 2][2 * (k & 1)], wl[d][k / 2][2 * (k & 1) + 1]);
       }
     }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");                   // and are read: their place is free
+    if (next < items) load(next, next_c);
+    f32x4_t part[kDepth] = {};
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int z = 0; z < kTerms; ++z) part[d] = product(wh[d][k], al[d][k][z], part[d]);
+    if (mine) {
+      f32x4_t sum = sums[wave][tok][grp];
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] = b0 + d < fb ? fmaf(part[d][i], s[d], sum[i]) : sum[i];   // no block past the last
+      sums[wave][tok][grp] = sum;
+    }
+    item = next;
+    c0 = next_c;
   }
-#pragma unroll
-  for (int f = 0; f < MF; ++f) red[wave][f][lane] = acc[f];
   __syncthreads();
-  if (wave >= MF) return;
-  f32x4_t sum = red[0][wave][lane];
+  // a thread a token and row
+  static_assert(NW * 64 == kMoeFewTokens * kTile, "a thread a result");
+  const int t = tid / kTile, r = tid % kTile;
+  float sum = 0.0f;
 #pragma unroll
-  for (int v = 1; v < NW; ++v) sum += red[v][wave][lane];
-  const int t = wave * 16 + row;
-  if (t >= A.tokens) return;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (n0 + grp * 4 + i < A.hidden) out[(int64_t)t * A.hidden + n0 + grp * 4 + i] = from_sum<T>(sum[i]);
+  for (int v = 0; v < NW; ++v) sum += reinterpret_cast<const float *>(&sums[v][t][0])[r];
+  if (A.splits > 1) {
+    float *mine = A.part + (int64_t)blockIdx.x * A.splits * (NW * 64) + tid;
+    // Each sum is stored and loaded as an atomic of the device's scope, which passes the XCDs' own L2; a store that has
+    // been acknowledged can be read.  (Fences, which write back and empty the whole L2, took 40 us.)
+    __hip_atomic_store(mine + blockIdx.y * NW * 64, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (tid == 0) before = __hip_atomic_fetch_add(A.arrived + blockIdx.x, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (before != A.splits - 1) return;
+    sum = 0.0f;
+    for (int z = 0; z < A.splits; ++z) sum += __hip_atomic_load(mine + z * NW * 64, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if (t < A.tokens && n0 + r < A.hidden) out[(int64_t)t * A.hidden + n0 + r] = from_sum<T>(sum);
+}
+
+int row_tiles(int hidden) { return (hidden + kTile - 1) / kTile; }
+
+// Workgroups of a row tile: as many as it takes for one a CU, while each wave has an item (us, one token to 8 of 64
+// experts of 2048 x 1024: 1 / 2 workgroups; the same of 32 tokens).
+int down_splits(int tokens, int experts, int top, int hidden, int ffn) {
+  const int64_t most = tokens * top < experts ? tokens * top : experts;
+  const int64_t items = most * (((ffn + kBlk - 1) / kBlk + 1) / 2);
+  const int64_t want = (256 + row_tiles(hidden) - 1) / row_tiles(hidden), can = (items + kDownWaves - 1) / kDownWaves;
+  return (int)(want < can ? want : can);
 }
 
 template <typename T>
-hipError_t run(const MoeArgs &A, const void *x, void *out, int num_cus, hipStream_t s) {
+hipError_t run(const MoeArgs &A, const void *x, void *out, hipStream_t s) {
   const bool vec = ((uintptr_t)x & 15u) == 0 && A.xs % (16 / (int)sizeof(T)) == 0;
-  const int pairs = A.tokens * A.top, tiles = (A.ffn + kBlk - 1) / kBlk * (kBlk / kTile);
+  const int pairs = A.tokens * A.top, tiles = (A.ffn + kBlk - 1) / kBlk * (kBlk / kTile), kb = (A.hidden + kBlk - 1) / kBlk;
   const int64_t items = (int64_t)(pairs < A.experts ? pairs : A.experts) * tiles;
-  const unsigned grid = (unsigned)(items < 2 * num_cus ? items : 2 * num_cus);
-  moe_up_kernel<T><<<grid, 64 * kUpWaves, 0, s>>>(A, vec, (const T *)x);
+  const int groups = kb >= 8 ? 1 : kb >= 4 ? 2 : 4;
+  const int64_t need = (items + groups - 1) / groups;
+  const unsigned grid = (unsigned)(need < 512 ? need : 512);
+  if (groups == 1) moe_up_kernel<T, 1><<<grid, 64 * kUpWaves, 0, s>>>(A, vec, (const T *)x);
+  else if (groups == 2) moe_up_kernel<T, 2><<<grid, 64 * kUpWaves, 0, s>>>(A, vec, (const T *)x);
+  else moe_up_kernel<T, 4><<<grid, 64 * kUpWaves, 0, s>>>(A, vec, (const T *)x);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const unsigned rows = (unsigned)((A.hidden + kTile - 1) / kTile);
-  if (A.tokens <= 16) moe_down_kernel<T, 1><<<rows, 64 * kDownWaves, 0, s>>>(A, (T *)out);
-  else moe_down_kernel<T, 2><<<rows, 64 * kDownWaves, 0, s>>>(A, (T *)out);
+  moe_down_kernel<T><<<dim3(row_tiles(A.hidden), A.splits), 64 * kDownWaves, 0, s>>>(A, (T *)out);
   return hipGetLastError();
 }
 
+int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
+
 }  // namespace
 
-int64_t moe_ffn_scratch(int tokens, int, int top, int, int ffn) {
-  // three terms: the workspace is asked for without the type
-  return (sizeof(MoeList) + 15) / 16 * 16 + (int64_t)tokens * top * ((ffn + kBlk - 1) / kBlk * kBlk) * 6;
+// The list, the row tiles' counts, the workgroups' sums, the hidden rows (three terms: the workspace is asked
+// for without the type).
+int64_t moe_ffn_scratch(int tokens, int experts, int top, int hidden, int ffn) {
+  const int64_t parts = (int64_t)row_tiles(hidden) * down_splits(tokens, experts, top, hidden, ffn) * kMoeFewTokens * kTile * 4;
+  return align16(sizeof(MoeList)) + align16(row_tiles(hidden) * 4) + parts +
+         (int64_t)tokens * top * ((ffn + kBlk - 1) / kBlk * kBlk) * 6;
 }
 
 hipError_t launch_moe_ffn(const void *x, int dtype, int tokens, int hidden, int64_t xs, const void *logits, int ltype,
                           int64_t ls, int experts, int top, bool renorm, const uint8_t *w13, const float *s13,
-                          const uint8_t *w2, const float *s2, int ffn, void *out, void *scratch, int num_cus, hipStream_t s) {
-  __bf16 *act = (__bf16 *)((char *)scratch + (sizeof(MoeList) + 15) / 16 * 16);
-  const MoeArgs A{logits, ltype, xs, ls, tokens, experts, top, renorm, hidden, ffn, w13, w2, s13, s2, (MoeList *)scratch, act};
-  if (dtype == BQM_F32) return run<float>(A, x, out, num_cus, s);
-  if (dtype == BQM_BF16) return run<__bf16>(A, x, out, num_cus, s);
-  return run<_Float16>(A, x, out, num_cus, s);
+                          const uint8_t *w2, const float *s2, int ffn, void *out, void *scratch, hipStream_t s) {
+  const int splits = down_splits(tokens, experts, top, hidden, ffn);
+  char *at = (char *)scratch;
+  MoeList *list = (MoeList *)at;
+  int *arrived = (int *)(at += align16(sizeof(MoeList)));
+  float *part = (float *)(at += align16(row_tiles(hidden) * 4));
+  __bf16 *act = (__bf16 *)(at + (int64_t)row_tiles(hidden) * splits * kMoeFewTokens * kTile * 4);
+  const MoeArgs A{logits, ltype, xs, ls, tokens, experts, top, renorm, hidden, ffn, w13, w2, s13, s2, list, act, part, arrived, splits};
+  if (dtype == BQM_F32) return run<float>(A, x, out, s);
+  if (dtype == BQM_BF16) return run<__bf16>(A, x, out, s);
+  return run<_Float16>(A, x, out, s);
 }
 
 }  // namespace bqm
