@@ -29,7 +29,10 @@ struct AppendArgs {
   float *ks, *vs;                         // [count, heads]
 };
 
-__device__ __forceinline__ bool finite(float v) { return (__float_as_uint(v) & 0x7FFFFFFFu) < 0x7F800000u; }
+constexpr uint32_t kInf = 0x7F800000u;
+
+// |v| as an integer: ordered as the values are, infinities and NaN above all others
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
 // The smallest power of two >= 2^-126 that amax (finite, >= 0) is at most 448 times of: 448 = 1.75 x 2^8.
 __device__ __forceinline__ float scale_for(float amax) {
@@ -38,21 +41,15 @@ __device__ __forceinline__ float scale_for(float amax) {
   return __uint_as_float((uint32_t)max(e, 1) << 23);
 }
 
-// Four codes of v times inv, NaN for what is not finite.
-__device__ __forceinline__ uint32_t quad(float a, float b, float c, float d, float inv) {
-  const float v[4] = {a, b, c, d};
-  float q[4];
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    q[i] = __builtin_amdgcn_fmed3f(v[i] * inv, -448.0f, 448.0f);
-    bad |= !finite(v[i]);
-  }
-  uint32_t w = e4m3_quad(q[0], q[1], q[2], q[3]);
-  if (__builtin_expect(bad, 0)) {
+// Four codes of v times inv (at most 448 by the choice of the scale), and, where `odd` says that there may be
+// some, NaN for what is not finite.
+__device__ __forceinline__ uint32_t quad(float a, float b, float c, float d, float inv, bool odd) {
+  uint32_t w = e4m3_quad(a * inv, b * inv, c * inv, d * inv);
+  if (__builtin_expect(odd, 0)) {
+    const float v[4] = {a, b, c, d};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (!finite(v[i])) w = (w & ~(0xFFu << (8 * i))) | (0x7Fu << (8 * i));
+      if (magnitude(v[i]) >= kInf) w = (w & ~(0xFFu << (8 * i))) | (0x7Fu << (8 * i));
   }
   return w;
 }
@@ -65,6 +62,29 @@ __device__ __forceinline__ uint32_t rescaled(uint32_t w, float f, uint32_t keep)
   return (n & ~keep) | (w & keep);
 }
 
+// N elements as they are in memory.
+template <typename T, int N>
+struct Raw {
+  typedef T Vec __attribute__((ext_vector_type(N), aligned(16)));
+  Vec v;
+};
+template <typename T>
+struct Raw<T, 1> {
+  T v;
+};
+
+// A 4 x 4 transposition of bytes between four neighbouring lanes: lane r gets byte r of each.  Even lanes take
+// bytes 0 and 2 of their own and of lane ^ 1, odd ones 1 and 3; then lanes 0 and 1 the lower halves of their own
+// and of lane ^ 2, lanes 2 and 3 the upper.
+__device__ __forceinline__ uint32_t turn_bytes(uint32_t w, int r) {
+  const uint32_t near = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w, 0xB1, 0xF, 0xF, false);
+  w = __builtin_amdgcn_perm(near, w, r & 1 ? 0x03070105u : 0x06020400u);
+  const uint32_t far = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w, 0x4E, 0xF, 0xF, false);
+  return __builtin_amdgcn_perm(far, w, r & 2 ? 0x03020706u : 0x05040100u);
+}
+
+// A thread's item is a unit of a token's row, the tokens of a group of four in four neighbouring lanes: their
+// values' codes are turned around between these lanes, so that LDS takes four tokens at a time.
 template <typename T, int N, int kDp>
 __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs A, const T *__restrict__ k,
                                                                    const T *__restrict__ v) {
@@ -84,57 +104,99 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs A,
   if (!kv_find(B, blockIdx.x, 1, pages_of, &q, &job)) return;
   const int first = max(0, q.first()), end = kv_limit(B, q);
   const int pi = first / kPage + job, page = kv_page(B, q, pi);
-  if (page < 0) return;
   // the page's new tokens: slots [a, b), rows from `row` on
   const int a = max(first - pi * kPage, 0), b = min(end - pi * kPage, kPage);
   const int row = q.lo + pi * kPage + a - q.first();
-  const int h = blockIdx.y, n = b - a;
-  const int64_t ph = (int64_t)page * A.heads + h;
-
-  float x[kEach][2][N], y[kEach][2][N];
-  uint32_t top[2] = {0, 0};
-  const auto largest = [](const float (&p)[N], uint32_t m) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const uint32_t u = __float_as_uint(p[i]) & 0x7FFFFFFFu;
-      m = u < 0x7F800000u && u > m ? u : m;
-    }
-    return m;
+  const int h = blockIdx.y, n = b - a, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const auto token_unit = [&](int e, int *t, int *u) {
+    const int i = e * kAppendThreads + threadIdx.x, four = i / 4;
+    *u = four % kUnits;
+    *t = four / kUnits * 4 + i % 4;
   };
-  const auto load = [&](const T *p, int c, float (&o)[N]) {
-    if constexpr (N == 1) o[0] = c < A.dim ? to_f32(p[c]) : 0.0f;
-    else if (c < A.dim) load_vec<N>(p + c, o);
+
+  float x[kEach][2][N];
+  Raw<T, N> y[kEach][2];
+  const auto load = [&](const T *p, int c) {
+    Raw<T, N> o{};
+    if (c < A.dim) o = *reinterpret_cast<const Raw<T, N> *>(p + c);
+    return o;
+  };
+  const auto values = [](const Raw<T, N> &r, float (&o)[N]) {
+    if constexpr (N == 1) {
+      o[0] = to_f32(r.v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) o[j] = to_f32(r.v[j]);
+    }
   };
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
-    const int i = e * kAppendThreads + threadIdx.x, t = i / kUnits, u = i % kUnits;
+    int t, u, c1, c2;
+    token_unit(e, &t, &u);
 #pragma unroll
-    for (int j = 0; j < N; ++j) x[e][0][j] = x[e][1][j] = y[e][0][j] = y[e][1][j] = 0.0f;
+    for (int s = 0; s < 2; ++s) {
+      y[e][s] = Raw<T, N>{};
+#pragma unroll
+      for (int j = 0; j < N; ++j) x[e][s][j] = 0.0f;
+    }
     if (t >= n) continue;
-    int c1, c2;
-    const bool turned = unit_columns<N>(A.R, u, &c1, &c2);
+    unit_columns<N>(A.R, u, &c1, &c2);
     const T *kr = k + (row + t) * A.kt + h * A.kh, *vr = v + (row + t) * A.vt + h * A.vh;
-    load(kr, c1, x[e][0]);
-    load(kr, c2, x[e][1]);
-    load(vr, c1, y[e][0]);
-    load(vr, c2, y[e][1]);
-    if (turned) {
+    values(load(kr, c1), x[e][0]);
+    values(load(kr, c2), x[e][1]);
+    y[e][0] = load(vr, c1);
+    y[e][1] = load(vr, c2);
+  }
+  if (page < 0) return;                                                  // looked up while they are on their way
+  const int64_t ph = (int64_t)page * A.heads + h;
+  const float old_k = A.ks[ph], old_v = A.vs[ph];
+  uint32_t top[2] = {0, 0};
+  const auto largest = [](const float (&p)[N], uint32_t m) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) m = max(m, magnitude(p[i]));
+    return m;
+  };
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    int t, u, c1, c2;
+    token_unit(e, &t, &u);
+    if (unit_columns<N>(A.R, u, &c1, &c2) && t < n) {
       const int p = A.R.positions[row + t];
       float2 cs[N];
 #pragma unroll
-      for (int j = 0; j < N; ++j) turn(p, A.R.freqs[u * N + j], A.R.mscale, A.R.sign, &cs[j].x, &cs[j].y);
+      for (int j = 0; j < N; ++j) turn(p, turns_of(A.R.freqs[u * N + j]), A.R.mscale, A.R.sign, &cs[j].x, &cs[j].y);
       unit_turn<N>(A.R, cs, x[e][0], x[e][1]);
     }
     top[0] = largest(x[e][1], largest(x[e][0], top[0]));
-    top[1] = largest(y[e][1], largest(y[e][0], top[1]));
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      float f[N];
+      values(y[e][s], f);
+      top[1] = largest(f, top[1]);
+    }
   }
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const bool odd_k = top[0] >= kInf, odd_v = top[1] >= kInf;
+  if (__builtin_expect(odd_k || odd_v, 0)) {                             // once more, of the finite ones
+    top[0] = top[1] = 0;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        float f[N];
+        values(y[e][s], f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const uint32_t mk = magnitude(x[e][s][i]), mv = magnitude(f[i]);
+          top[0] = mk < kInf ? max(top[0], mk) : top[0];
+          top[1] = mv < kInf ? max(top[1], mv) : top[1];
+        }
+      }
+  }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const float m = wave_max(__uint_as_float(top[i]));
     if (lane == 0) red[i][wave] = __float_as_uint(m);
   }
-  const float old_k = A.ks[ph], old_v = A.vs[ph];
   __syncthreads();
   float need[2];
 #pragma unroll
@@ -165,32 +227,40 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs A,
   const float ik = 1.0f / sk, iv = 1.0f / sv;
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
-    const int i = e * kAppendThreads + threadIdx.x, t = i / kUnits, u = i % kUnits;
-    if (t >= n) continue;
-    int c[2];
-    unit_columns<N>(A.R, u, &c[0], &c[1]);
+    int t, u, c1, c2;
+    token_unit(e, &t, &u);
+    unit_columns<N>(A.R, u, &c1, &c2);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      uint8_t *to = kp + (a + t) * kDp + c[s];
+      const int c = s ? c2 : c1, r = threadIdx.x & 3;
+      uint8_t *to = kp + (a + t) * kDp + c;
+      float f[N];
+      values(y[e][s], f);
       if constexpr (N == 1) {
-        *to = (uint8_t)quad(x[e][s][0], 0.0f, 0.0f, 0.0f, ik);
-        turned_v[c[s] * kRow + t] = (uint8_t)quad(y[e][s][0], 0.0f, 0.0f, 0.0f, iv);
+        if (t >= n) continue;
+        *to = (uint8_t)quad(x[e][s][0], 0.0f, 0.0f, 0.0f, ik, odd_k);
+        turned_v[c * kRow + t] = (uint8_t)quad(f[0], 0.0f, 0.0f, 0.0f, iv, odd_v);
       } else {
         uint32_t w[2], z[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          w[j] = quad(x[e][s][4 * j], x[e][s][4 * j + 1], x[e][s][4 * j + 2], x[e][s][4 * j + 3], ik);
-          z[j] = quad(y[e][s][4 * j], y[e][s][4 * j + 1], y[e][s][4 * j + 2], y[e][s][4 * j + 3], iv);
+          w[j] = quad(x[e][s][4 * j], x[e][s][4 * j + 1], x[e][s][4 * j + 2], x[e][s][4 * j + 3], ik, odd_k);
+          z[j] = turn_bytes(quad(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3], iv, odd_v), r);
+          if (kItems % kAppendThreads == 0 || t < kPage)
+            *reinterpret_cast<uint32_t *>(turned_v + (c + 4 * j + r) * kRow + t - r) = z[j];
         }
-        *reinterpret_cast<u32x2_t *>(to) = u32x2_t{w[0], w[1]};
-#pragma unroll
-        for (int j = 0; j < N; ++j) turned_v[(c[s] + j) * kRow + t] = (uint8_t)(z[j / 4] >> (8 * (j % 4)));
+        if (t < n) *reinterpret_cast<u32x2_t *>(to) = u32x2_t{w[0], w[1]};
       }
     }
   }
   __syncthreads();
-  // a column's tokens, four a thread where the page's slots are aligned to that
-  if (((a | n) & 3) == 0) {
+  // a column's tokens: the page's, or four a thread where the slots are aligned to that, or one
+  if (n == kPage) {
+    for (int i = threadIdx.x; i < A.dim * 4; i += kAppendThreads) {
+      const uint32_t *from = reinterpret_cast<const uint32_t *>(turned_v + i / 4 * kRow + i % 4 * 16);
+      *reinterpret_cast<u32x4_t *>(vp + i * 16) = u32x4_t{from[0], from[1], from[2], from[3]};
+    }
+  } else if (((a | n) & 3) == 0) {
     const int words = n / 4;
     for (int i = threadIdx.x; i < A.dim * words; i += kAppendThreads) {
       const int c = i / words, t = (i - c * words) * 4;

@@ -57,7 +57,8 @@ __device__ __forceinline__ bool kv_find(const KvBatch &B, int bid, int each, F j
   const int lane = threadIdx.x & 63;
   int before = 0;
   for (int s0 = 0; s0 < B.seqs; s0 += 64) {
-    const int mine = s0 + lane < B.seqs ? jobs(kv_seq(B, s0 + lane)) : 0;
+    const KvSeq own = s0 + lane < B.seqs ? kv_seq(B, s0 + lane) : KvSeq{0, 0, 0, 0};
+    const int mine = s0 + lane < B.seqs ? jobs(own) : 0;
     const int inc = wave_prefix(mine);
     const int sum = __builtin_amdgcn_readlane(inc, 63);
     if (bid < before + sum) {
@@ -65,7 +66,8 @@ __device__ __forceinline__ bool kv_find(const KvBatch &B, int bid, int each, F j
       const int j = bid - before - (at ? __builtin_amdgcn_readlane(inc, at - 1) : 0);
       // ascending offsets always pass; others, whose sums may overflow, stay in their buffers
       if (at >= 64 || s0 + at >= B.seqs || j < 0 || j >= __builtin_amdgcn_readlane(mine, at)) return false;
-      *q = kv_seq(B, s0 + at);
+      *q = KvSeq{s0 + at, __builtin_amdgcn_readlane(own.lo, at), __builtin_amdgcn_readlane(own.n, at),
+                 __builtin_amdgcn_readlane(own.len, at)};
       *job = j;
       return true;
     }
@@ -76,20 +78,25 @@ __device__ __forceinline__ bool kv_find(const KvBatch &B, int bid, int each, F j
 
 // ------------------------------------------------------------------ rotation
 //
-// cos and sin of position p times f radians.  The angle is formed and reduced to an eighth of
-// a turn in 64 bits: in 32, position 2^20 would leave it 0.06 off.  The series' first terms left out are
-// below 2^-28.
+// Turns a position: f / (2 pi), for f radians.
+__device__ __forceinline__ double turns_of(double f) { return f * 0.15915494309189535; }
+
+// cos and sin of p times f turns.  The angle is formed and whole turns are taken off it in 64 bits: in 32,
+// position 2^20 would leave a radian 0.06 off.  What is left, at most half a turn, is within 2^-26 of one in fp32;
+// the quarter turns come off it exactly, and the series' first terms left out are below 2^-25.
 __device__ __forceinline__ void turn(int p, double f, float scale, float sign, float *c, float *s) {
-  const double t = (double)p * (f * 0.15915494309189535);               // in turns: f / (2 pi)
-  const double q4 = rint(4.0 * t);
-  const float x = (float)((t - 0.25 * q4) * 6.283185307179586);
+  const double t = (double)p * f;
+  const float r = (float)(t - rint(t));
+  const float q4 = rintf(4.0f * r);                                      // -2 .. 2
+  const float x = fmaf(-0.25f, q4, r) * 6.2831853f;
   const float x2 = x * x;
   const float sn = x * fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), 1.0f);
-  const float cs = fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, -1.0f / 3628800, 1.0f / 40320), -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
-  const int q = (int)(q4 - 4.0 * rint(0.25 * q4)) & 3;                   // quarter turns, modulo 4
+  const float cs = fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.0f / 40320, -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
+  const int q = (int)q4 & 3;                                             // quarter turns, modulo 4
   const float a = q & 1 ? sn : cs, b = q & 1 ? cs : sn;
-  *c = scale * (q == 1 || q == 2 ? -a : a);
-  *s = scale * sign * (q >= 2 ? -b : b);
+  const float ss = scale * sign;
+  *c = (q + 1) & 2 ? -scale * a : scale * a;
+  *s = q & 2 ? -ss * b : ss * b;
 }
 
 struct Rope {

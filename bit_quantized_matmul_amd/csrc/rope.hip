@@ -42,7 +42,7 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs A, int per,
   const int t0 = blockIdx.x * per, n = min(per, A.tokens - t0);
   for (int i = threadIdx.x; i < n * half; i += kRopeThreads) {
     const int t = i / half, j = i - t * half;
-    turn(A.R.positions[t0 + t], A.R.freqs[j], A.R.mscale, A.R.sign, &cs[i].x, &cs[i].y);
+    turn(A.R.positions[t0 + t], turns_of(A.R.freqs[j]), A.R.mscale, A.R.sign, &cs[i].x, &cs[i].y);
   }
   __syncthreads();
   const int units = (A.dim + 2 * N - 1) / (2 * N);
