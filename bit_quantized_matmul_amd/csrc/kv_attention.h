@@ -83,6 +83,35 @@ __device__ __forceinline__ void load_q8(const T *p, int c, int dim, bool vec, fl
   }
 }
 
+// The larger of the two halves' v, and their sum: swapped between registers.
+__device__ __forceinline__ float halves_max(float v) {
+  const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+__device__ __forceinline__ float halves_sum(float v) {
+  const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+// The same of the four rows of 16 lanes.
+__device__ __forceinline__ float rows_max(float v) {
+  const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return halves_max(fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1])));
+}
+__device__ __forceinline__ float rows_sum(float v) {
+  const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return halves_sum(__uint_as_float(s[0]) + __uint_as_float(s[1]));
+}
+
+// l + the sum of probabilities as they were rounded: what the second product weighs with.
+template <int kTerms>
+__device__ __forceinline__ float add_terms(const f16x8 (&t)[kTerms], float l) {
+#pragma unroll
+  for (int z = 0; z < kTerms; ++z)
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) l = __builtin_amdgcn_fdot2(f16x2{t[z][i], t[z][i + 1]}, f16x2{(_Float16)1.0f, (_Float16)1.0f}, l, false);
+  return l;
+}
+
 // True where some byte is a NaN code.
 __device__ __forceinline__ bool has_nan(int w) { return (((w & 0x7F7F7F7F) + 0x01010101) & (int)0x80808080) != 0; }
 

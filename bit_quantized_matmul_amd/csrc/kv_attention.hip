@@ -146,8 +146,7 @@ __global__ __launch_bounds__(64 * NW) void kv_stream_kernel(AttnArgs A, bool qve
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) top = fmaxf(top, whole || (see >> (4 * t + r) & 1) ? x[t][r] : -INFINITY);
-      top = fmaxf(top, __shfl_xor(top, 16, 64));
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      top = rows_max(top);
       const float m1 = fmaxf(m, top > -INFINITY ? top * f : -INFINITY);
       const float base = (m1 > -INFINITY ? m1 : 0.0f) - kUp;
       if (__ballot(m1 > m)) {
@@ -165,9 +164,9 @@ __global__ __launch_bounds__(64 * NW) void kv_stream_kernel(AttnArgs A, bool qve
         for (int r = 0; r < 8; ++r) {
           const float v = __builtin_amdgcn_exp2f(fmaf(x[2 * a + r / 4][r % 4], f, -base));
           e[r] = whole || (see >> (8 * a + r) & 1) ? v : 0.0f;
-          l += e[r];
         }
         to_terms<kTerms>(e, p[a]);
+        l = add_terms<kTerms>(p[a], l);
       }
       const float v_scale = vs * 0x1p-15f;
       if (!whole) {
@@ -213,8 +212,7 @@ __global__ __launch_bounds__(64 * NW) void kv_stream_kernel(AttnArgs A, bool qve
     page = next;
     next = after;
   }
-  l += __shfl_xor(l, 16, 64);
-  l += __shfl_xor(l, 32, 64);
+  l = rows_sum(l);
 
   // the waves' sums join in LDS
   if (g == 0) {

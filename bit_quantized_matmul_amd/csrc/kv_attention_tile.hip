@@ -32,6 +32,9 @@ __device__ __forceinline__ int value_swizzle(int d) { return d >> 2 & 3; }
 template <typename T, int kDp>
 __global__ __launch_bounds__(64 * kWaves, (kDp > 128 || kTermsOf<T> > 1) ? 1 : 2) void kv_tile_kernel(
     AttnArgs A, bool qvec, const T *__restrict__ q, T *__restrict__ out) {
+  // The sums follow a row's maximum when it has grown by more than 2^kLag, or, with two terms, at once: some row of the
+  // wave's 32 has a larger one in most pages, and to scale all sums takes a sixth of a page's time.
+  constexpr float kLag = kTermsOf<T> == 1 ? 4.0f : 0.0f, kUpLag = kUp - kLag, kDown = kTermsOf<T> == 1 ? 0x1p-11f : 0x1p-15f;
   constexpr int kTerms = kTermsOf<T>, kSteps = kDp / 16, kCols = kDp / 32, kChunks = kRowChunks<kDp>;
   constexpr int kKeyBytes = kPage * kChunks * 16, kStage = kKeyBytes + kPage * kDp;
   constexpr int kLoads = kStage / 1024;                                  // of a wave's 64 lanes, 16 bytes each
@@ -60,8 +63,10 @@ __global__ __launch_bounds__(64 * kWaves, (kDp > 128 || kTermsOf<T> > 1) ? 1 : 2
   const int pos = s.first() + i, first = s.first() + min(c0, tile_last) / rep, last = s.first() + last_c / rep;
   const int lo = A.window ? max(0, pos - A.window + 1) : 0, hi = min(pos + 1, limit);
 
+  // Sums of values are in units of the scale of the page that came last, v_unit: pages' scales are powers of two and
+  // mostly the same, and then the second product adds to them as they are.
   f32x16 o[kCols] = {};
-  float m = -INFINITY, l = 0.0f;
+  float m = -INFINITY, l = 0.0f, v_unit = 0.0f;
   if (p0 < p1) {
     // loads: load n of a stage brings 1 KiB, lane x the 16 bytes that go to slot 64 n + x
     auto load_page = [&](int to, int page) {
@@ -113,7 +118,7 @@ __global__ __launch_bounds__(64 * kWaves, (kDp > 128 || kTermsOf<T> > 1) ? 1 : 2
     int at = 0;
     for (int pi = p0; pi < p1; ++pi, at ^= kStage) {
       const int64_t ph = (int64_t)max(page, 0) * A.kv_heads + kh;
-      const float ks = A.ks[ph], vs = A.vs[ph] * 0x1p-15f;
+      const float ks = A.ks[ph], vs = A.vs[ph];
       const bool there = page >= 0;
       page = pi + 1 < p1 ? kv_page(A.B, s, pi + 1) : -1;
       // this page has landed, and everyone is done with the one before
@@ -149,7 +154,6 @@ __global__ __launch_bounds__(64 * kWaves, (kDp > 128 || kTermsOf<T> > 1) ? 1 : 2
         }
       }
       __builtin_amdgcn_sched_barrier(0);
-      i32x4 vn[2] = {value(0, 0), value(0, 1)};
       const float f = ldexpf(mul * __builtin_amdgcn_frexp_mantf(ks), __builtin_amdgcn_frexp_expf(ks) + qe);
       const bool whole = start + kPage <= min(first + 1, limit) && (!A.window || start > last - A.window);
       uint32_t see = 0xFFFFFFFFu;                                        // bit 16 t + r: token start + 32 t + 16 hf + r
@@ -170,16 +174,16 @@ __global__ __launch_bounds__(64 * kWaves, (kDp > 128 || kTermsOf<T> > 1) ? 1 : 2
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r) top = fmaxf(top, x[t][r]);
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      top = halves_max(top);
       const float m1 = fmaxf(m, top > -INFINITY ? top * f : -INFINITY);
-      const float base = (m1 > -INFINITY ? m1 : 0.0f) - kUp;
-      if (__ballot(m1 > m)) {
-        const float alpha = __builtin_amdgcn_exp2f(m - (base + kUp));
+      if (__ballot(m1 > m + kLag)) {
+        const float alpha = m1 > -INFINITY ? __builtin_amdgcn_exp2f(m - m1) : 0.0f;
         l *= alpha;
 #pragma unroll
         for (int d = 0; d < kCols; ++d) o[d] *= alpha;
         m = m1;
       }
+      const float base = (m > -INFINITY ? m : 0.0f) - kUpLag;
       f16x8 p[4][kTerms];
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
@@ -190,13 +194,11 @@ __global__ __launch_bounds__(64 * kWaves, (kDp > 128 || kTermsOf<T> > 1) ? 1 : 2
 #pragma unroll
           for (int r = 0; r < 8; ++r) e[r] = see >> (8 * a + r) & 1 ? e[r] : 0.0f;
         }
-#pragma unroll
-        for (int r = 0; r < 8; ++r) l += e[r];
         to_terms<kTerms>(e, p[a]);
+        l = add_terms<kTerms>(p[a], l);
       }
-      // What some row does not see may be NaN, and 0 times it would be too: in a page with such codes that some row sees
-      // in part they are taken out, and the sums of the rows that do see them made NaN.
-      int spoiled = 0;
+      // What some row does not see may be NaN, and 0 times it would be too.
+      int rare = 0;
       if (!whole) {
         bool bad = false;
 #pragma unroll
@@ -207,53 +209,74 @@ __global__ __launch_bounds__(64 * kWaves, (kDp > 128 || kTermsOf<T> > 1) ? 1 : 2
 #pragma unroll
             for (int w = 0; w < 4; ++w) bad |= has_nan(vw[w]);
           }
-        spoiled = __ballot(bad) != 0;
+        rare = __ballot(bad) != 0;
       }
+      // Another scale: the sums change to its units.  A page of far smaller ones (below 2^-40 of the units, or 0) is summed
+      // apart and added with its share of them instead, so that neither leaves fp32.
+      float share = 1.0f;
+      if (vs != v_unit || vs == 0.0f) {
+        if (vs > 0.0f && v_unit == 0.0f) {
+          v_unit = vs;                                                   // the first
+        } else if (vs > 0.0f && v_unit / vs < 0x1p40f) {
+          const float by = v_unit / vs;
 #pragma unroll
-      for (int d = 0; d < kCols; ++d) {
-        f32x16 part = {};
-        i32x4 now[2] = {vn[0], vn[1]};
-        if (d + 1 < kCols) {
-          vn[0] = value(d + 1, 0);
-          vn[1] = value(d + 1, 1);
+          for (int d = 0; d < kCols; ++d) o[d] *= by;
+          v_unit = vs;
+        } else {
+          share = v_unit > 0.0f ? vs / v_unit : vs;
+          rare = 1;
         }
-        spoiled = __builtin_amdgcn_readfirstlane(spoiled);
-        asm("" : "+s"(spoiled));                                // one test here, not two copies of what follows
-        if (__builtin_expect(spoiled, 0)) {
-          f32x16 n = {};
+      }
+      if (__builtin_expect(!__builtin_amdgcn_readfirstlane(rare), 1)) {
+        i32x4 vn[2] = {value(0, 0), value(0, 1)};
+#pragma unroll
+        for (int d = 0; d < kCols; ++d) {
+          const i32x4 now[2] = {vn[0], vn[1]};
+          if (d + 1 < kCols) {
+            vn[0] = value(d + 1, 0);
+            vn[1] = value(d + 1, 1);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+              const f16x8 vf = widen(now[t][2 * a], now[t][2 * a + 1]);
+#pragma unroll
+              for (int z = 0; z < kTerms; ++z) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, p[2 * t + a][z], o[d], 0, 0, 0);
+            }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      } else {
+        // NaN codes are taken out, and the sums of the rows that see one made NaN
+#pragma unroll
+        for (int d = 0; d < kCols; ++d) {
+          f32x16 part = {}, n = {};
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
+            const i32x4 vw = value(d, t);
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
               f16x8 sees;
 #pragma unroll
               for (int r = 0; r < 8; ++r) sees[r] = (_Float16)(see >> (16 * t + 8 * a + r) & 1 ? 1.0f : 0.0f);
-              n = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen(nan_ones(now[t][2 * a]), nan_ones(now[t][2 * a + 1])), sees, n, 0, 0, 0);
+              n = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen(nan_ones(vw[2 * a]), nan_ones(vw[2 * a + 1])), sees, n, 0, 0, 0);
+              const f16x8 vf = widen(without_nan(vw[2 * a]), without_nan(vw[2 * a + 1]));
+#pragma unroll
+              for (int z = 0; z < kTerms; ++z) part = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, p[2 * t + a][z], part, 0, 0, 0);
+              __builtin_amdgcn_sched_barrier(0);
             }
-#pragma unroll
-            for (int w = 0; w < 4; ++w) now[t][w] = without_nan(now[t][w]);
           }
 #pragma unroll
-          for (int r = 0; r < 16; ++r) o[d][r] = n[r] != 0.0f ? __builtin_nanf("") : o[d][r];
+          for (int r = 0; r < 16; ++r) o[d][r] = n[r] != 0.0f ? __builtin_nanf("") : fmaf(part[r], share, o[d][r]);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int a = 0; a < 2; ++a) {
-            const f16x8 vf = widen(now[t][2 * a], now[t][2 * a + 1]);
-#pragma unroll
-            for (int z = 0; z < kTerms; ++z) part = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, p[2 * t + a][z], part, 0, 0, 0);
-          }
-#pragma unroll
-        for (int r = 0; r < 16; ++r) o[d][r] = fmaf(part[r], vs, o[d][r]);
-        __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
   if (!any || c0 + col > tile_last) return;
-  l += __shfl_xor(l, 32, 64);
-  l *= 0x1p-15f;
+  l = halves_sum(l);
+  l *= kDown;
   if (A.splits > 1) {
     const int64_t at = head * A.splits + blockIdx.y;
     if (hf == 0) A.ml[at] = float2{m, l};
@@ -262,11 +285,15 @@ __global__ __launch_bounds__(64 * kWaves, (kDp > 128 || kTermsOf<T> > 1) ? 1 : 2
 #pragma unroll
     for (int d = 0; d < kCols; ++d)
 #pragma unroll
+      for (int r = 0; r < 16; ++r) o[d][r] = o[d][r] * kDown * v_unit;
+#pragma unroll
+    for (int d = 0; d < kCols; ++d)
+#pragma unroll
       for (int b = 0; b < 4; ++b)
         *reinterpret_cast<f32x4_t *>(p + d * 32 + 8 * b + 4 * hf) = f32x4_t{o[d][4 * b], o[d][4 * b + 1], o[d][4 * b + 2], o[d][4 * b + 3]};
     return;
   }
-  const float by = l != 0.0f ? 1.0f / l : 0.0f;
+  const float by = l != 0.0f ? kDown / l : 0.0f;
   T *to = out + head * A.dim;
   typedef T tx4 __attribute__((ext_vector_type(4)));
   const bool four = (A.dim & 3) == 0 && ((uintptr_t)out & (4 * sizeof(T) - 1)) == 0;
@@ -277,7 +304,7 @@ __global__ __launch_bounds__(64 * kWaves, (kDp > 128 || kTermsOf<T> > 1) ? 1 : 2
       const int c1 = d * 32 + 8 * b + 4 * hf;
       T v[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = from_sum<T>(o[d][4 * b + r] * by);
+      for (int r = 0; r < 4; ++r) v[r] = from_sum<T>(o[d][4 * b + r] * by * v_unit);
       if (four && c1 < A.dim) {
         *reinterpret_cast<tx4 *>(to + c1) = tx4{v[0], v[1], v[2], v[3]};
       } else {

@@ -16,8 +16,8 @@ absolute.  exp adds 2^-22.  p is rounded to fp16, of 11 bits, half a step of whi
 summed within a page (66 roundings of 2^-23) and over pages and parts (2^-23 each), the sum of p likewise: with L
 positions in all, out is off by at most
     (2 e + 2^-21 + p's + (66 + L / 16) 2^-22) sum p |v| + 2^-40 sum |v|
-and half a step of the type: 2^15 p in fp16 is in steps of 2^-24 below 2^-14, so a p below 2^-29 of the largest is off
-by up to 2^-40 of it, in two terms too.
+and half a step of the type: p times 2^15 in fp16 is in steps of 2^-24 below 2^-14, so a p below 2^-29 of the largest is
+off by up to 2^-40 of it, in two terms too.  With 16-bit rows p is times 2^11 of a maximum that may lag behind by 2^4: 2^-36.
 """
 from __future__ import annotations
 
@@ -280,7 +280,7 @@ def test_append_leaves_out_what_has_no_place():
 def attention_tol(mag, most, small, dp, length, dtype):
     e = (2 * dp + 16) * 2.0 ** -23 * most[..., None]
     p = 2.0 ** -22 if dtype == torch.float32 else 2.0 ** -11
-    return (2 * e + 2.0 ** -21 + p + (66 + length / 16) * 2.0 ** -22) * mag + small
+    return (2 * e + 2.0 ** -21 + p + (66 + length / 16) * 2.0 ** -22) * mag + small * (1 if dtype == torch.float32 else 16)
 
 
 def check_attention(rng, lens, news, heads, kv, dim, dtype, window=0, scale=None, cache=None, pages=None, count=None, q=None, off=None):
