@@ -329,23 +329,32 @@ struct Plan {
 
 int64_t above(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Few rows: the pages a workgroup takes are such that there are two workgroups a CU where all sequences are as
-// long as the table is wide, but 4 at least (one a wave) and 32 at most, so that sequences of unlike length
-// share the CUs (us, 8 key heads: one sequence of 131072 in chunks of 32 / 16 / 8 / 4 pages: 58 / 64 / 75 / 96; 64
-// of up to 8192 in chunks of 128 / 32 / 16: 121 / 110 / 118).  The parts of all workgroups are bounded too.
+// Tiles of 128 queries where a sequence has more than 16 in the mean and there is work for them: 6000 pages times key
+// heads times 32 queries.  (us in tiles of 16 / 128 queries, 32 heads to 8 key heads, 128 columns: 64 sequences of 2048
+// with 16 queries of a key head each 44 / 61, with 32 83 / 62, with 128 298 / 109; one of 8192 with 64, 128 and 256:
+// 24 / 36, 32 / 38, 54 / 41; 8 of 2048 with 64 and 96: 32 / 37, 42 / 39.)
+//
+// Pages a workgroup takes.  Tiles of 16: one workgroup a CU where all sequences are as long as the table is wide, but 4
+// pages at least (one a wave), all of up to 8, and 32 at most, so that sequences of unlike length share the CUs (us with
+// 4 / 8 / 16 / 32 pages: one sequence of 512 10.4 / 9.1 / 9.0 / 9.0, of 8192 11.8 / 13.0 / 16.2 / 23.4, of 131072 96 / 75 / 64
+// / 58; 4 of 4096 16.4 / 14.8 / 18.0 / 25.2; 16 of 8192 69 / 59 / 50 / 48; 64 of up to 8192 110 with 32, 121 with 128).  The
+// parts of all workgroups are bounded too.  Tiles of 128: two workgroups a CU, 8 pages at least (us with 8 / 16 / 32 / 64
+// pages: 128 rows of 8192 50 / 59 / 65 / 110, 512 145 / 119 / 106 / 160).
 Plan plan(int tokens, int seqs, int heads, int kv_heads, int width, int window) {
-  constexpr int64_t kGroups = 512, kMostGroups = 4096;
+  constexpr int64_t kManyWork = 6000, kMostGroups = 4096;
   const int rep = heads / kv_heads;
-  const int64_t runs = seqs < tokens ? seqs : tokens;
+  const int64_t runs = seqs < tokens ? seqs : tokens, queries = (int64_t)tokens * rep;
   Plan p;
-  p.many = (int64_t)tokens * rep >= 64 * runs;
+  p.many = queries > 16 * runs && above(queries, 32 * runs) * runs * kv_heads * width >= kManyWork;
   p.tiles = tiles(tokens, seqs, rep, p.many ? 128 : 16);
   const int64_t work = p.tiles * kv_heads * width;
-  int64_t chunk = above(work, kGroups);
+  int64_t chunk;
   if (p.many) {
-    chunk = p.tiles * kv_heads >= kGroups ? width : chunk < 16 ? 16 : chunk;
+    chunk = p.tiles * kv_heads >= 512 ? width : above(work, 512);
+    if (chunk < 8) chunk = 8;
   } else {
-    chunk = chunk < 4 ? 4 : chunk > 32 ? 32 : chunk;
+    chunk = above(work, 256);
+    chunk = width <= 8 ? width : chunk < 4 ? 4 : chunk > 32 ? 32 : chunk;
     if (chunk < above(work, kMostGroups)) chunk = above(work, kMostGroups);
   }
   if (chunk < above(width, kMaxParts)) chunk = above(width, kMaxParts);
@@ -403,6 +412,9 @@ int64_t kv_attention_scratch(int tokens, int seqs, int heads, int kv_heads, int 
 hipError_t launch_kv_attention(const KvBatch &B, const void *q, int dtype, int heads, int dim, int64_t qt, int64_t qh,
                                const uint8_t *kc, const uint8_t *vc, const float *ks, const float *vs, int kv_heads,
                                float scale, int window, void *out, void *scratch, hipStream_t s) {
+  // position - window stays in 32 bits: positions are above -2^24, and no cache holds 2^31 - 2^25
+  constexpr int kMostWindow = 0x7FFFFFFF - (1 << 25);
+  window = window < kMostWindow ? window : kMostWindow;
   const Plan p = plan(B.tokens, B.seqs, heads, kv_heads, B.width, window);
   float *part = (float *)scratch;
   float2 *ml = (float2 *)(part + (p.splits > 1 ? (int64_t)B.tokens * heads * p.splits * kv_padded_dim(dim) : 0));

@@ -283,9 +283,18 @@ def attention_tol(mag, most, small, dp, length, dtype):
     return (2 * e + 2.0 ** -21 + p + (66 + length / 16) * 2.0 ** -22) * mag + small * (1 if dtype == torch.float32 else 16)
 
 
-def check_attention(rng, lens, news, heads, kv, dim, dtype, window=0, scale=None, cache=None, pages=None, count=None, q=None, off=None):
+WIDE = 8192      # pages of a table for which a few rows are taken in tiles of 128 queries, in parts
+
+
+def widened(pages, width):
+    """The table with columns of no page behind the others."""
+    return np.pad(pages, ((0, 0), (0, max(0, width - pages.shape[1]))), constant_values=-1)
+
+
+def check_attention(rng, lens, news, heads, kv, dim, dtype, window=0, scale=None, cache=None, pages=None, count=None, q=None, off=None, width=0):
     if pages is None:
         pages, off, count = batch(rng, lens, news)
+    pages = widened(pages, width)
     cache = cache or filled(rng, count, kv, dim)
     tokens = int(off[-1])
     q, d = rounded(rng.standard_normal((tokens, heads, dim)), dtype) if q is None else rounded(q, dtype)
@@ -311,8 +320,9 @@ def test_attention_decode(lens, news, heads, kv, dim, dtype):
 @pytest.mark.parametrize("window", [0, 1, 50, 64])
 @pytest.mark.parametrize("heads,kv,dim", [(6, 2, 26), (4, 1, 128), (2, 2, 64), (20, 1, 32)])
 @pytest.mark.parametrize("lens,news", [([70], [70]), ([200, 64, 9, 130], [5, 64, 0, 67]), ([260], [3])])
-def test_attention_of_several_rows(lens, news, heads, kv, dim, window, dtype):
-    check_attention(np.random.default_rng(sum(lens) + dim + window), lens, news, heads, kv, dim, dtype, window)
+@pytest.mark.parametrize("width", [0, WIDE])
+def test_attention_of_several_rows(lens, news, heads, kv, dim, window, width, dtype):
+    check_attention(np.random.default_rng(sum(lens) + dim + window), lens, news, heads, kv, dim, dtype, window, width=width)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -320,17 +330,30 @@ def test_attention_of_several_rows(lens, news, heads, kv, dim, window, dtype):
     (8, 2, 128, [5000], [1], 0), (4, 1, 64, [3000, 100, 4097], [1, 1, 1], 1000), (8, 8, 128, [1500], [200], 0),
     (4, 1, 128, [700, 900], [600, 300], 0), (16, 2, 128, [2100], [64], 300), (3, 3, 26, [600], [600], 0),
     (4, 2, 96, [1100], [260], 0), (2, 1, 192, [900], [257], 0), (2, 1, 256, [700], [300], 100)])
-def test_attention_of_long_sequences(heads, kv, dim, lens, news, window, dtype):
+@pytest.mark.parametrize("width", [0, WIDE])
+def test_attention_of_long_sequences(heads, kv, dim, lens, news, window, width, dtype):
     rng = np.random.default_rng(sum(lens))
     q = rng.standard_normal((sum(news), heads, dim)) * np.exp(rng.standard_normal((sum(news), heads, 1)))
-    check_attention(rng, lens, news, heads, kv, dim, dtype, window, q=q)
+    check_attention(rng, lens, news, heads, kv, dim, dtype, window, q=q, width=width)
 
 
-def test_attention_rows_without_positions_are_zero():
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim,window", [(32, 0), (26, 70), (128, 0)])
+def test_attention_of_many_sequences(dim, window, dtype):
+    """Tiles of 128 queries without parts: 64 sequences of 0 .. 40 rows, some of one or none."""
+    rng = np.random.default_rng(dim)
+    news = rng.integers(0, 41, 64)
+    news[:3] = 0, 1, 40
+    lens = [int(n + rng.integers(0, 300)) for n in news]
+    check_attention(rng, lens, news.tolist(), 16, 8, dim, dtype, window, width=16)
+
+
+@pytest.mark.parametrize("width", [0, WIDE])
+def test_attention_rows_without_positions_are_zero(width):
     rng = np.random.default_rng(21)
     pages = np.array([[-1, 3], [2, 99], [-1, -1], [4, 5]], dtype=np.int32)
     lens, off = [100, 100, 64, 2], np.array([0, 70, 75, 78, 84], dtype=np.int32)  # the last: 6 rows of 2 positions
-    got, ref = check_attention(rng, lens, None, 4, 2, 64, torch.bfloat16, pages=pages, off=off, count=6)
+    got, ref = check_attention(rng, lens, None, 4, 2, 64, torch.bfloat16, pages=pages, off=off, count=6, width=width)
     assert np.all(got[:34] == 0.0) and np.all(got[75:78] == 0.0) and np.all(got[78:82] == 0.0)
 
 
@@ -339,7 +362,8 @@ def test_attention_leaves_rows_of_no_sequence():
     pages, _, count = batch(rng, [80, 90], [1, 1])
     cache = filled(rng, count, 2, 64)
     q, d = rounded(rng.standard_normal((40, 2, 64)), torch.float16)
-    for off in ([3, 5, 30], [3, 25, 30]):
+    for off, width in (([3, 5, 30], 0), ([3, 25, 30], 0), ([3, 25, 30], WIDE)):
+        pages = widened(pages, width)
         out = torch.full((40, 2, 64), -3.0, dtype=torch.float16, device=DEV)
         B.kv_attention(d, on_device(cache), ints(pages), ints([80, 90]), ints(off), out=out)
         ref, mag, most, small = okv.attention(q, cache, pages, [80, 90], off)
@@ -349,12 +373,14 @@ def test_attention_leaves_rows_of_no_sequence():
         assert np.all(host(out)[~rows] == -3.0)
 
 
+@pytest.mark.parametrize("width", [0, WIDE])
 @pytest.mark.parametrize("news,window", [(1, 0), (1, 30), (40, 0), (150, 40), (200, 0)])
-def test_attention_ignores_what_is_masked(news, window):
+def test_attention_ignores_what_is_masked(news, window, width):
     """NaN codes past the end, before the window and ahead of a row; slots after the end hold whatever they did."""
     rng = np.random.default_rng(news + window)
     length = 200
     pages, off, count = batch(rng, [length], [news])
+    pages = widened(pages, width)
     clean = filled(rng, count, 2, 64)
     q = rng.standard_normal((news, 4, 64))
     base, _ = check_attention(rng, [length], [news], 4, 2, 64, torch.bfloat16, window, cache=clean, pages=pages, off=off, q=q)
@@ -392,11 +418,13 @@ def test_attention_ignores_what_is_masked(news, window):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-def test_attention_of_a_row_that_is_not_finite(dtype):
+@pytest.mark.parametrize("news,width", [(3, 0), (40, WIDE)])
+def test_attention_of_a_row_that_is_not_finite(news, width, dtype):
     rng = np.random.default_rng(5)
-    pages, off, count = batch(rng, [100], [3])
+    pages, off, count = batch(rng, [100], [news])
+    pages = widened(pages, width)
     cache = filled(rng, count, 2, 32)
-    _, d = rounded(rng.standard_normal((3, 4, 32)), dtype)
+    _, d = rounded(rng.standard_normal((news, 4, 32)), dtype)
     base = host(B.kv_attention(d, on_device(cache), ints(pages), ints([100]), ints(off)))
     d[0, 1, 5], d[2, 3, 0] = float("inf"), float("nan")
     got = host(B.kv_attention(d, on_device(cache), ints(pages), ints([100]), ints(off)))
@@ -406,12 +434,13 @@ def test_attention_of_a_row_that_is_not_finite(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("news", [1, 90])
-def test_attention_of_far_scales(news, dtype):
+@pytest.mark.parametrize("news,width", [(1, 0), (90, 0), (90, WIDE)])
+def test_attention_of_far_scales(news, width, dtype):
     """Pages whose scales are 2^40 apart, in keys (a softmax of one key) and in values."""
     rng = np.random.default_rng(31)
     lens = [700]
     pages, off, count = batch(rng, lens, [news])
+    pages = widened(pages, width)
     cache = filled(rng, count, 2, 64)
     cache["v_scale"][:] = 2.0 ** rng.integers(-60, 60, cache["v_scale"].shape) if dtype != torch.float16 else 2.0 ** rng.integers(-30, 3, cache["v_scale"].shape)
     cache["k_scale"][:] = 2.0 ** rng.integers(-40, -6, cache["k_scale"].shape)
@@ -420,10 +449,12 @@ def test_attention_of_far_scales(news, dtype):
     check_attention(rng, lens, [news], 4, 2, 64, dtype, cache=cache, pages=pages, off=off, scale=0.7, q=q)
 
 
-def test_attention_strided_queries():
+@pytest.mark.parametrize("width", [0, WIDE])
+def test_attention_strided_queries(width):
     rng = np.random.default_rng(33)
     lens, news = [150, 77], [20, 77]
     pages, off, count = batch(rng, lens, news)
+    pages = widened(pages, width)
     cache = on_device(filled(rng, count, 2, 80))
     wide = torch.randn(97, 9, 81, device=DEV).half()
     args = (cache, ints(pages), ints(lens), ints(off))
@@ -493,6 +524,42 @@ def test_prompt_then_tokens_as_a_graph():
         again = B.kv_attention(B.rope(x[:, :heads], positions - 1, f), cache, tables, lens - 1)
     side.synchronize()
     assert torch.equal(again, got[-1])
+
+
+def test_windows_as_large_as_integers():
+    rng = np.random.default_rng(60)
+    lens, news = [300, 40], [100, 40]
+    pages, off, count = batch(rng, lens, news)
+    cache, q = on_device(filled(rng, count, 2, 64)), torch.randn(140, 4, 64, device=DEV).bfloat16()
+    for width in (0, WIDE):
+        args = (q, cache, ints(widened(pages, width)), ints(lens), ints(off))
+        want = B.kv_attention(*args)
+        for window in (300, 2 ** 30, 2 ** 31 - 1):
+            got, ref = host(B.kv_attention(*args, window=window)), host(want)
+            # other parts, other orders of the same sums: a step of bf16 at most
+            assert np.all(np.abs(got - ref) <= 2.0 ** -7 * np.abs(ref) + 2.0 ** -12)
+
+
+def test_codes_past_32_bits():
+    """Pages whose codes begin past 2^32 bytes hold and give what the same pages of a small cache do."""
+    rng = np.random.default_rng(61)
+    heads, dim, far = 8, 128, 70000                                       # 64 KiB a page
+    lens, news = [200, 130], [200, 130]
+    pages, off, count = batch(rng, lens, news)
+    small, large = B.kv_cache(count, heads, dim), B.kv_cache(far + count, heads, dim)
+    k, v, q = (torch.randn(330, heads, dim, device=DEV).bfloat16() for _ in range(3))
+    pos, f = ints(np.concatenate([np.arange(n) for n in news])), dev(B.rope_freqs(dim))
+    out = []
+    for cache, shift in ((small, 0), (large, far)):
+        table = ints(np.where(pages >= 0, pages + shift, -1))
+        B.kv_append(cache, k, v, table, ints(lens), ints(off), pos, f)
+        out.append([B.kv_attention(q, cache, ints(widened(table.cpu().numpy(), w)), ints(lens), ints(off)) for w in (0, WIDE)])
+        out[-1].append(B.kv_attention(q[:2], cache, table, ints(lens)))
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+    for a, b in zip(small, large):
+        assert torch.equal(a.view(torch.uint8) if a.dtype == F8 else a, (b.view(torch.uint8) if b.dtype == F8 else b)[far:])
+    assert not large.k[:far].view(torch.uint8).any() and not large.v[:far].view(torch.uint8).any()
 
 
 def test_attention_given_workspace_and_refusals():

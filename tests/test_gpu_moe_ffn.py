@@ -97,6 +97,25 @@ def test_routing_is_moe_routes(tokens, renorm):
         assert np.all(host(y)[1] == 0.0) and np.any(ref[2] != 0.0)
 
 
+@pytest.mark.parametrize("tokens,hidden,ffn", [(1, 64, 64), (32, 200, 130)])
+def test_no_token_has_an_expert(tokens, hidden, ffn):
+    logits = np.full((tokens, 9), -np.inf)
+    *_, y, ref = run(np.random.default_rng(2), tokens, 9, 3, hidden, ffn, torch.bfloat16, logits=logits)
+    assert np.all(host(y) == 0.0) and np.all(ref == 0.0)
+
+
+def test_all_tokens_to_one_expert():
+    logits = np.full((32, 70), -np.inf)
+    logits[:, 66] = np.arange(32)
+    run(np.random.default_rng(4), 32, 70, 4, 260, 140, torch.float16, logits=logits)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_wide_layers(dtype):
+    """More blocks a row than waves, and rows in several turns of every workgroup."""
+    run(np.random.default_rng(6), 20, 24, 2, 2200, 1300, dtype)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_rows_of_unlike_size_and_not_finite(dtype):
     rng = np.random.default_rng(9)
