@@ -81,18 +81,19 @@ __device__ __forceinline__ bool kv_find(const KvBatch &B, int bid, int each, F j
 // Turns a position: f / (2 pi), for f radians.
 __device__ __forceinline__ double turns_of(double f) { return f * 0.15915494309189535; }
 
-// cos and sin of p times f turns.  The angle is formed and whole turns are taken off it in 64 bits: in 32,
-// position 2^20 would leave a radian 0.06 off.  What is left, at most half a turn, is within 2^-26 of one in fp32;
-// the quarter turns come off it exactly, and the series' first terms left out are below 2^-25.
+// cos and sin of p times f turns.  The angle is formed and quarter turns are taken off it in 64 bits (in 32, position
+// 2^20 would leave a radian 0.06 off): the nearest whole number of them is what 1.5 x 2^52 added to it leaves in its
+// lower bits.  What is left, at most an eighth, is rounded once; the series' first terms left out are below 2^-28.
+// So cos and sin are nearly what rounding from 64 bits gives: of 19 million turned keys 13 to 22 become another code than
+// exact ones would, and 22 to 29 with cos and sin rounded from 64 bits.
 __device__ __forceinline__ void turn(int p, double f, float scale, float sign, float *c, float *s) {
-  const double t = (double)p * f;
-  const float r = (float)(t - rint(t));
-  const float q4 = rintf(4.0f * r);                                      // -2 .. 2
-  const float x = fmaf(-0.25f, q4, r) * 6.2831853f;
+  constexpr double kWhole = 0x1.8p52;
+  const double t = (double)p * f, z = fma(4.0, t, kWhole);
+  const float x = (float)(fma(-0.25, z - kWhole, t) * 6.283185307179586);
   const float x2 = x * x;
-  const float sn = x * fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), 1.0f);
-  const float cs = fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.0f / 40320, -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
-  const int q = (int)q4 & 3;                                             // quarter turns, modulo 4
+  const float sn = fmaf(x * x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), x);
+  const float cs = fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, -1.0f / 3628800, 1.0f / 40320), -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
+  const int q = (int)(__double_as_longlong(z) & 3);                      // quarter turns, modulo 4
   const float a = q & 1 ? sn : cs, b = q & 1 ? cs : sn;
   const float ss = scale * sign;
   *c = (q + 1) & 2 ? -scale * a : scale * a;
