@@ -261,10 +261,11 @@ __global__ __launch_bounds__(64 * kUpWaves, sizeof(T) == 2 ? 4 : 2) void moe_up_
   int item = blockIdx.x * kGroups + group, turn = 0, c0 = 0;             // c0: the first of an item's tokens, 16 at a time
   if (item < items) load_w(item, wave);
   // every group of the workgroup makes as many turns as the longest: they meet once a turn
-  int turns = 0;
-  for (int g = 0; g < kGroups; ++g) {
+  const int lead = blockIdx.x * kGroups;
+  int turns = items > lead ? (items - lead + stride - 1) / stride : 0;
+  for (int g = 0; g < kGroups && A.tokens > 16; ++g) {                   // items of several turns
     int n = 0;
-    for (int i = blockIdx.x * kGroups + g; i < items; i += stride) n += (__popc(L.tokens[i / tiles]) + 15) / 16;
+    for (int i = lead + g; i < items; i += stride) n += (__popc(L.tokens[i / tiles]) + 15) / 16;
     turns = max(turns, n);
   }
   for (; turn < turns; ++turn) {
