@@ -22,6 +22,7 @@ constexpr int kAppendThreads = 256;
 
 struct AppendArgs {
   KvBatch B;
+  KvMap M;
   Rope R;
   int heads, dim;
   int64_t kt, kh, vt, vh;                 // strides of tokens and heads
@@ -101,7 +102,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs A,
     const int first = max(0, x.first()), end = kv_limit(B, x);
     return end > first ? (end - 1) / kPage - first / kPage + 1 : 0;
   };
-  if (!kv_find(B, blockIdx.x, 1, pages_of, &q, &job)) return;
+  if (!kv_find(B, A.M, blockIdx.x, pages_of, &q, &job)) return;
   const int first = max(0, q.first()), end = kv_limit(B, q);
   const int pi = first / kPage + job, page = kv_page(B, q, pi);
   // the page's new tokens: slots [a, b), rows from `row` on
@@ -276,7 +277,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs A,
 
 template <typename T, int N, int kDp>
 hipError_t start(const AppendArgs &A, const T *k, const T *v, hipStream_t s) {
-  const dim3 grid((unsigned)kv_append_jobs(A.B.tokens, A.B.seqs), (unsigned)A.heads);
+  const dim3 grid((unsigned)A.M.groups, (unsigned)A.heads);
   kv_append_kernel<T, N, kDp><<<grid, kAppendThreads, 0, s>>>(A, k, v);
   return hipGetLastError();
 }
@@ -304,17 +305,17 @@ hipError_t run(const AppendArgs &A, const void *k, const void *v, hipStream_t s)
 
 }  // namespace
 
-// Pages that `tokens` new tokens of `seqs` sequences can touch at most: a run of n touches
-// (n + 62) / 64 + 1 of them, and no more than n.
-int64_t kv_append_jobs(int tokens, int seqs) {
-  const int64_t runs = seqs < tokens ? seqs : tokens, most = tokens / kPage + 2 * runs;
-  return most < tokens ? most : tokens;
-}
+namespace {
+// n new tokens touch (n + 62) / 64 + 1 pages at most, which is n / 64 + 2 or less, and no more than n.
+KvMap append_map(int tokens, int seqs) { return kv_map(tokens, seqs, 1, 1, kPage, 2); }
+}  // namespace
+
+int64_t kv_append_jobs(int tokens, int seqs) { return append_map(tokens, seqs).groups; }
 
 hipError_t launch_kv_append(const KvBatch &B, const void *k, const void *v, int dtype, int heads, int dim, int64_t kt,
                             int64_t kh, int64_t vt, int64_t vh, const int32_t *positions, const double *freqs, int rotary,
                             bool interleaved, float mscale, uint8_t *kc, uint8_t *vc, float *ks, float *vs, hipStream_t s) {
-  const AppendArgs A{B, {positions, freqs, rotary, interleaved, mscale, 1.0f}, heads, dim, kt, kh, vt, vh, kc, vc, ks, vs};
+  const AppendArgs A{B, append_map(B.tokens, B.seqs), {positions, freqs, rotary, interleaved, mscale, 1.0f}, heads, dim, kt, kh, vt, vh, kc, vc, ks, vs};
   if (dtype == BQM_F32) return run<float>(A, k, v, s);
   if (dtype == BQM_BF16) return run<__bf16>(A, k, v, s);
   return run<_Float16>(A, k, v, s);

@@ -22,6 +22,7 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 struct AttnArgs {
   KvBatch B;
+  KvMap M;                                // tiles to sequences
   int heads, kv_heads, rep, dim, window;  // rep: heads / kv_heads
   int64_t qt, qh;                         // strides of q's tokens and heads
   float scale;                            // times log2(e)
@@ -134,7 +135,7 @@ __device__ __forceinline__ void pages_of(const AttnArgs &A, const KvSeq &s, int 
 }
 
 // Tiles of 128 queries (kv_attention_tile.hip).
-hipError_t launch_tiles(const AttnArgs &A, int64_t tiles, bool vec, const void *q, int dtype, void *out, hipStream_t s);
+hipError_t launch_tiles(const AttnArgs &A, bool vec, const void *q, int dtype, void *out, hipStream_t s);
 
 }  // namespace attn
 }  // namespace bqm

@@ -26,8 +26,7 @@ __global__ __launch_bounds__(64 * NW) void kv_stream_kernel(AttnArgs A, bool qve
   KvSeq s;
   int job;
   const int rep = A.rep;
-  if (!kv_find(A.B, blockIdx.x, (rep + 15) / 16, [rep](const KvSeq &x) { return (int)(((int64_t)x.n * rep + 15) / 16); }, &s, &job))
-    return;
+  if (!kv_find(A.B, A.M, blockIdx.x, [rep](const KvSeq &x) { return (int)(((int64_t)x.n * rep + 15) / 16); }, &s, &job)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4, kh = blockIdx.y;
   const int last_c = min(s.n * rep, job * 16 + 16) - 1;
@@ -314,16 +313,9 @@ __global__ __launch_bounds__(256) void kv_join_kernel(AttnArgs A, T *__restrict_
 
 // ------------------------------------------------------------------ dispatch
 
-// Tiles of `of` queries that cover every sequence's rows whatever the offsets are.
-int64_t tiles(int tokens, int seqs, int rep, int of) {
-  const int64_t runs = seqs < tokens ? seqs : tokens;
-  const int64_t a = (int64_t)tokens * rep / of + runs, b = (int64_t)tokens * ((rep + of - 1) / of);
-  return a < b ? a : b;
-}
-
 struct Plan {
   bool many;                              // tiles of 128 queries
-  int64_t tiles;
+  KvMap map;
   int chunk, splits;
 };
 
@@ -346,11 +338,12 @@ Plan plan(int tokens, int seqs, int heads, int kv_heads, int width, int window) 
   const int64_t runs = seqs < tokens ? seqs : tokens, queries = (int64_t)tokens * rep;
   Plan p;
   p.many = queries > 16 * runs && above(queries, 32 * runs) * runs * kv_heads * width >= kManyWork;
-  p.tiles = tiles(tokens, seqs, rep, p.many ? 128 : 16);
-  const int64_t work = p.tiles * kv_heads * width;
+  const int of = p.many ? 128 : 16;
+  p.map = kv_map(tokens, seqs, (rep + of - 1) / of, rep, of, 1);
+  const int64_t groups = p.map.groups * kv_heads, work = groups * width;
   int64_t chunk;
   if (p.many) {
-    chunk = p.tiles * kv_heads >= 512 ? width : above(work, 512);
+    chunk = groups >= 512 ? width : above(work, 512);
     if (chunk < 8) chunk = 8;
   } else {
     chunk = above(work, 256);
@@ -360,7 +353,7 @@ Plan plan(int tokens, int seqs, int heads, int kv_heads, int width, int window) 
   if (chunk < above(width, kMaxParts)) chunk = above(width, kMaxParts);
   p.splits = (int)above(width, chunk);
   // a window: the pages that a tile's rows can see, in no more parts
-  const int64_t most = ((int64_t)window + (p.many ? 128 : 16)) / kPage + 2;
+  const int64_t most = ((int64_t)window + of) / kPage + 2;
   if (window && most < width) {
     if (chunk > above(most, p.splits)) chunk = above(most, p.splits);
     if (chunk < 4) chunk = 4;
@@ -374,9 +367,9 @@ template <typename T, int kDp>
 hipError_t start(const AttnArgs &A, const Plan &p, bool vec, const T *q, T *out, hipStream_t s) {
   hipError_t e = hipSuccess;
   if (p.many) {
-    e = launch_tiles(A, p.tiles, vec, q, std::is_same_v<T, float> ? BQM_F32 : std::is_same_v<T, __bf16> ? BQM_BF16 : BQM_F16, out, s);
+    e = launch_tiles(A, vec, q, std::is_same_v<T, float> ? BQM_F32 : std::is_same_v<T, __bf16> ? BQM_BF16 : BQM_F16, out, s);
   } else {
-    kv_stream_kernel<T, kDp, 4><<<dim3((unsigned)p.tiles, A.kv_heads, A.splits), 256, 0, s>>>(A, vec, q, out);
+    kv_stream_kernel<T, kDp, 4><<<dim3((unsigned)A.M.groups, A.kv_heads, A.splits), 256, 0, s>>>(A, vec, q, out);
     e = hipGetLastError();
   }
   if (e != hipSuccess || A.splits == 1) return e;
@@ -418,7 +411,7 @@ hipError_t launch_kv_attention(const KvBatch &B, const void *q, int dtype, int h
   const Plan p = plan(B.tokens, B.seqs, heads, kv_heads, B.width, window);
   float *part = (float *)scratch;
   float2 *ml = (float2 *)(part + (p.splits > 1 ? (int64_t)B.tokens * heads * p.splits * kv_padded_dim(dim) : 0));
-  const AttnArgs A{B, heads, kv_heads, heads / kv_heads, dim, window, qt, qh, scale * 1.44269504f, kc, vc, ks, vs, p.chunk, p.splits, part, ml};
+  const AttnArgs A{B, p.map, heads, kv_heads, heads / kv_heads, dim, window, qt, qh, scale * 1.44269504f, kc, vc, ks, vs, p.chunk, p.splits, part, ml};
   if (dtype == BQM_F32) return run<float>(A, p, q, out, s);
   if (dtype == BQM_BF16) return run<__bf16>(A, p, q, out, s);
   return run<_Float16>(A, p, q, out, s);

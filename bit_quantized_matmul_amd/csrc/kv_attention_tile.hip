@@ -44,7 +44,7 @@ __global__ __launch_bounds__(64 * kWaves, (kDp > 128 || kTermsOf<T> > 1) ? 1 : 2
   KvSeq s;
   int job;
   const auto jobs = [rep](const KvSeq &x) { return (int)(((int64_t)x.n * rep + 127) / 128); };
-  if (!kv_find(A.B, bid / A.kv_heads, (rep + 127) / 128, jobs, &s, &job)) return;
+  if (!kv_find(A.B, A.M, bid / A.kv_heads, jobs, &s, &job)) return;
   job = jobs(s) - 1 - job;                                               // the last rows see the most: they begin
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, hf = lane >> 5;
@@ -320,29 +320,29 @@ __global__ __launch_bounds__(64 * kWaves, (kDp > 128 || kTermsOf<T> > 1) ? 1 : 2
 }
 
 template <typename T, int kDp>
-hipError_t start(const AttnArgs &A, int64_t tiles, bool qvec, const T *q, T *out, hipStream_t s) {
-  kv_tile_kernel<T, kDp><<<dim3((unsigned)(tiles * A.kv_heads), A.splits), 64 * kWaves, 0, s>>>(A, qvec, q, out);
+hipError_t start(const AttnArgs &A, bool qvec, const T *q, T *out, hipStream_t s) {
+  kv_tile_kernel<T, kDp><<<dim3((unsigned)(A.M.groups * A.kv_heads), A.splits), 64 * kWaves, 0, s>>>(A, qvec, q, out);
   return hipGetLastError();
 }
 
 template <typename T>
-hipError_t by_dim(const AttnArgs &A, int64_t tiles, bool vec, const void *q, void *out, hipStream_t s) {
+hipError_t by_dim(const AttnArgs &A, bool vec, const void *q, void *out, hipStream_t s) {
   switch (kv_padded_dim(A.dim)) {
-    case 32: return start<T, 32>(A, tiles, vec, (const T *)q, (T *)out, s);
-    case 64: return start<T, 64>(A, tiles, vec, (const T *)q, (T *)out, s);
-    case 96: return start<T, 96>(A, tiles, vec, (const T *)q, (T *)out, s);
-    case 128: return start<T, 128>(A, tiles, vec, (const T *)q, (T *)out, s);
-    case 192: return start<T, 192>(A, tiles, vec, (const T *)q, (T *)out, s);
-    default: return start<T, 256>(A, tiles, vec, (const T *)q, (T *)out, s);
+    case 32: return start<T, 32>(A, vec, (const T *)q, (T *)out, s);
+    case 64: return start<T, 64>(A, vec, (const T *)q, (T *)out, s);
+    case 96: return start<T, 96>(A, vec, (const T *)q, (T *)out, s);
+    case 128: return start<T, 128>(A, vec, (const T *)q, (T *)out, s);
+    case 192: return start<T, 192>(A, vec, (const T *)q, (T *)out, s);
+    default: return start<T, 256>(A, vec, (const T *)q, (T *)out, s);
   }
 }
 
 }  // namespace
 
-hipError_t launch_tiles(const AttnArgs &A, int64_t tiles, bool vec, const void *q, int dtype, void *out, hipStream_t s) {
-  if (dtype == BQM_F32) return by_dim<float>(A, tiles, vec, q, out, s);
-  if (dtype == BQM_BF16) return by_dim<__bf16>(A, tiles, vec, q, out, s);
-  return by_dim<_Float16>(A, tiles, vec, q, out, s);
+hipError_t launch_tiles(const AttnArgs &A, bool vec, const void *q, int dtype, void *out, hipStream_t s) {
+  if (dtype == BQM_F32) return by_dim<float>(A, vec, q, out, s);
+  if (dtype == BQM_BF16) return by_dim<__bf16>(A, vec, q, out, s);
+  return by_dim<_Float16>(A, vec, q, out, s);
 }
 
 }  // namespace attn

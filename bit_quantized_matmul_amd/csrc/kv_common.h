@@ -42,38 +42,53 @@ __device__ __forceinline__ int kv_page(const KvBatch &B, const KvSeq &q, int i) 
   return (unsigned)p < (unsigned)B.count ? p : -1;
 }
 
-// Job `bid` of the sequences' jobs(seq) each, in order: its sequence and its place there.  Every
-// wave searches for itself, 64 sequences at a time.  Without offsets every sequence has
-// `each` places.  False past the last.
+// Which workgroups a sequence has: those from offset * mul / div + add * (its number) on.  The map is such that
+// the next sequence's begin behind all that this one can need, so a workgroup finds its own in a few steps and not by
+// adding up what the sequences before it have; the ones that nobody needs end.
+struct KvMap {
+  int mul, div, add;
+  int64_t groups;
+};
+
+// Places of sequences that need at most `most` a row, and at most n mul / div rounded up and `add` - 1 more of n rows:
+// whichever of the two maps takes fewer.
+inline KvMap kv_map(int tokens, int seqs, int most, int mul, int div, int add) {
+  const int64_t rows = (int64_t)tokens * most, runs = (int64_t)tokens * mul / div + (int64_t)seqs * add;
+  return rows <= runs ? KvMap{most, 1, 0, rows} : KvMap{mul, div, add, runs};
+}
+
+// The sequence of workgroup `bid` and its place there, below jobs(seq); false where there is none.  Every wave
+// searches for itself, 64 sequences at a time.
 template <typename F>
-__device__ __forceinline__ bool kv_find(const KvBatch &B, int bid, int each, F jobs, KvSeq *q, int *job) {
-  if (!B.offsets) {
-    const int s = bid / each;
+__device__ __forceinline__ bool kv_find(const KvBatch &B, const KvMap &M, int bid, F jobs, KvSeq *q, int *job) {
+  if (!B.offsets) {                                                      // offset s is s, and most of the first map
+    const int s = bid / M.mul;
     if (s >= B.seqs) return false;
     *q = kv_seq(B, s);
-    *job = bid - s * each;
+    *job = bid - s * M.mul;
     return *job < jobs(*q);
   }
   const int lane = threadIdx.x & 63;
-  int before = 0;
-  for (int s0 = 0; s0 < B.seqs; s0 += 64) {
-    const KvSeq own = s0 + lane < B.seqs ? kv_seq(B, s0 + lane) : KvSeq{0, 0, 0, 0};
-    const int mine = s0 + lane < B.seqs ? jobs(own) : 0;
-    const int inc = wave_prefix(mine);
-    const int sum = __builtin_amdgcn_readlane(inc, 63);
-    if (bid < before + sum) {
-      const int at = __popcll(__ballot(before + inc <= bid));
-      const int j = bid - before - (at ? __builtin_amdgcn_readlane(inc, at - 1) : 0);
-      // ascending offsets always pass; others, whose sums may overflow, stay in their buffers
-      if (at >= 64 || s0 + at >= B.seqs || j < 0 || j >= __builtin_amdgcn_readlane(mine, at)) return false;
-      *q = KvSeq{s0 + at, __builtin_amdgcn_readlane(own.lo, at), __builtin_amdgcn_readlane(own.n, at),
-                 __builtin_amdgcn_readlane(own.len, at)};
-      *job = j;
-      return true;
-    }
-    before += sum;
+  const auto begin = [&](int s, int offset) { return (int)((int64_t)offset * M.mul / M.div) + M.add * s; };
+  int s0 = 0, n = B.seqs;
+  while (n > 64) {
+    const int step = (n + 63) / 64, s = s0 + lane * step;
+    const bool before = s < s0 + n && begin(s, min(max(0, B.offsets[min(s, B.seqs - 1)]), B.tokens)) <= bid;
+    const int at = __popcll(__ballot(before)) - 1;
+    if (at < 0) return false;
+    n = min(step, n - at * step);
+    s0 += at * step;
+    if (n <= 0) return false;                                            // offsets out of order
   }
-  return false;
+  const bool in = lane < n;
+  const KvSeq own = in ? kv_seq(B, s0 + lane) : KvSeq{0, 0, 0, 0};
+  const int first = begin(s0 + lane, own.lo);
+  const int at = __popcll(__ballot(in && first <= bid)) - 1;
+  if (at < 0) return false;
+  *q = KvSeq{s0 + at, __builtin_amdgcn_readlane(own.lo, at), __builtin_amdgcn_readlane(own.n, at),
+             __builtin_amdgcn_readlane(own.len, at)};
+  *job = bid - __builtin_amdgcn_readlane(first, at);
+  return *job >= 0 && *job < jobs(*q);
 }
 
 // ------------------------------------------------------------------ rotation

@@ -319,7 +319,6 @@ __global__ __launch_bounds__(64 * kUpWaves, sizeof(T) == 2 ? 4 : 2) void moe_up_
         if (b0 + NW * kDepth < kb) load_w(item, b0 + NW * kDepth);
         else if (next < items) load_w(next, wave);
       }
-      if (wave >= kb && next < items) load_w(next, wave);
 #pragma unroll
       for (int h = 0; h < 2; ++h) lds.red[turn & 1][group][wave][h][lane] = acc[h];
     }

@@ -526,6 +526,30 @@ def test_prompt_then_tokens_as_a_graph():
     assert torch.equal(again, got[-1])
 
 
+@pytest.mark.parametrize("seqs,most", [(65, 3), (128, 40), (1000, 2), (4097, 1), (4200, 3)])
+def test_many_sequences(seqs, most):
+    """Workgroups find their sequence among many, with ones without rows between, at the start and at the end."""
+    rng = np.random.default_rng(seqs)
+    news = rng.integers(0, most + 1, seqs)
+    news[[0, 1, -1, seqs // 2]] = 0
+    news[2] = most
+    lens = (news + rng.integers(0, 70, seqs)).tolist()
+    pages, off, count = batch(rng, lens, news)
+    want = filled(rng, count, 1, 32)
+    cache = on_device(want)
+    x, d = rounded(rng.standard_normal((int(off[-1]), 1, 32)), torch.bfloat16)
+    okv.append(want, x, -x, pages, lens, off)
+    B.kv_append(cache, d, -d, ints(pages), ints(lens), ints(off))
+    same_cache(cache, want, 32)
+    some = rng.permutation(np.flatnonzero(news))[:40].tolist() + [2]
+    got = host(B.kv_attention(d, cache, ints(pages), ints(lens), ints(off)))
+    for s in some:
+        rows = slice(off[s], off[s + 1])
+        ref, mag, most_, small = okv.attention(x[rows], want, pages[s:s + 1], [lens[s]], [0, int(news[s])])
+        check(got[rows], ref, attention_tol(mag, most_, small, 32, lens[s], torch.bfloat16), torch.bfloat16, f"sequence {s}")
+    assert np.all(np.isfinite(got))
+
+
 def test_windows_as_large_as_integers():
     rng = np.random.default_rng(60)
     lens, news = [300, 40], [100, 40]
