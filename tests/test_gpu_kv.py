@@ -450,6 +450,24 @@ def test_attention_of_far_scales(news, width, dtype):
 
 
 @pytest.mark.parametrize("width", [0, WIDE])
+def test_attention_of_shared_pages(width):
+    """Two sequences whose first pages are the same, and a page that a table names twice."""
+    rng = np.random.default_rng(34)
+    lens, news = [150, 200, 192], [20, 77, 30]
+    pages, off, count = batch(rng, lens, news)
+    pages[1, :2] = pages[0, :2]
+    pages[2, 2] = pages[2, 0]
+    check_attention(rng, lens, news, 4, 2, 64, torch.bfloat16, pages=pages, off=off, count=count, width=width)
+
+
+@pytest.mark.parametrize("width", [0, WIDE])
+def test_attention_of_many_heads_to_one(width):
+    rng = np.random.default_rng(35)
+    check_attention(rng, [70, 9, 130], [3, 0, 2], 200, 1, 32, torch.float16, width=width)
+    check_attention(rng, [70, 9, 130], [1, 1, 1], 260, 2, 26, torch.bfloat16, width=width)
+
+
+@pytest.mark.parametrize("width", [0, WIDE])
 def test_attention_strided_queries(width):
     rng = np.random.default_rng(33)
     lens, news = [150, 77], [20, 77]
@@ -584,6 +602,29 @@ def test_codes_past_32_bits():
     for a, b in zip(small, large):
         assert torch.equal(a.view(torch.uint8) if a.dtype == F8 else a, (b.view(torch.uint8) if b.dtype == F8 else b)[far:])
     assert not large.k[:far].view(torch.uint8).any() and not large.v[:far].view(torch.uint8).any()
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured calls of unlike sizes with one workspace, replayed in turn with eager work between."""
+    rng = np.random.default_rng(51)
+    calls = []
+    for lens, news in (([5000, 300], [1, 1]), ([900, 2000, 70], [60, 1, 70])):
+        pages, off, count = batch(rng, lens, news)
+        calls.append((torch.randn(sum(news), 8, 128, device=DEV).bfloat16(), on_device(filled(rng, count, 2, 128)),
+                      ints(widened(pages, 3000)), ints(lens), ints(off)))
+    want = [B.kv_attention(*c) for c in calls]
+    need = max(B.kv_attention_workspace(c[0].shape[0], c[2].shape[0], 8, 2, 128, 3000) for c in calls)
+    assert need > 0
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in calls], []
+    for g, c in zip(graphs, calls):
+        with torch.cuda.graph(g):
+            outs.append(B.kv_attention(*c, workspace=ws))
+    for i in range(6):
+        outs[i % 2].zero_()
+        graphs[i % 2].replay()
+        assert torch.equal(outs[i % 2], want[i % 2])
+        assert torch.equal(B.kv_attention(*calls[i % 2], workspace=ws), want[i % 2])
 
 
 def test_attention_given_workspace_and_refusals():

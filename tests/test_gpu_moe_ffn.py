@@ -173,6 +173,24 @@ def test_beside_the_calls_it_joins():
     assert ((got - want).norm() / want.norm()).item() < 0.1
 
 
+def test_graphs_that_share_a_workspace():
+    rng = np.random.default_rng(13)
+    layers = [run(rng, 3, 10, 3, 200, 150, torch.bfloat16), run(rng, 20, 5, 2, 1100, 70, torch.float32)]
+    calls = [(d.to(DEV), *args, dl.to(DEV), top) for (d, dl, args, *_), top in zip(layers, (3, 2))]
+    want = [B.moe_ffn(*c) for c in calls]
+    need = max(B.moe_ffn_workspace(3, 10, 3, 200, 150), B.moe_ffn_workspace(20, 5, 2, 1100, 70))
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in calls], []
+    for g, c in zip(graphs, calls):
+        with torch.cuda.graph(g):
+            outs.append(B.moe_ffn(*c, workspace=ws))
+    for i in range(6):
+        outs[i % 2].zero_()
+        graphs[i % 2].replay()
+        assert torch.equal(outs[i % 2], want[i % 2])
+        assert torch.equal(B.moe_ffn(*calls[i % 2], workspace=ws), want[i % 2])
+
+
 def test_graph_replays_and_other_streams():
     rng = np.random.default_rng(12)
     d, dl, args, y, _ = run(rng, 6, 10, 3, 200, 150, torch.bfloat16)
