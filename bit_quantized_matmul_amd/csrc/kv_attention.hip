@@ -250,56 +250,64 @@ __global__ __launch_bounds__(64 * NW) void kv_stream_kernel(AttnArgs A, bool qve
 // ------------------------------------------------------------------ parts
 //
 // kThreads a row and head: they first weigh the parts, then sum them, four columns a thread and kRows
-// parts at a time.  A wave takes up to 16 parts, a workgroup more (us, 32 heads of 64 parts: 12.7 and 6.0; 64 rows of 32
-// heads, 4 parts: 4.9 with a wave).
+// parts at a time.  A wave takes up to 16 parts, a workgroup more (us, a wave and a workgroup: 32 heads of 64 parts
+// 6.2 and 4.8; 64 rows of 32 heads, 4 parts 4.8 and 5.6).  What bounds it is one trip to memory after the other, so
+// the parts are asked for before their weights are known (5.9 -> 4.8 and 4.9 -> 4.8; 9 sequences of 12 heads 4.2 -> 3.6).
 constexpr int kMaxParts = 2048, kFewParts = 16;
 
 template <typename T, int kDp, int kThreads>
 __global__ __launch_bounds__(256) void kv_join_kernel(AttnArgs A, T *__restrict__ out) {
   constexpr int kLanes = kDp / 4, kRows = kThreads / kLanes, kEach = 256 / kThreads, kWavesEach = kThreads / 64;
   constexpr int kParts = kThreads == 64 ? kFewParts : kMaxParts;
+  constexpr int kFirst = kThreads == 64 ? (kFewParts + kRows - 1) / kRows : 8;
   __shared__ float w[kEach][kParts], red[2][4];
   __shared__ f32x4_t sums[kEach][kRows][kLanes];
   const int row = blockIdx.x, e = threadIdx.x / kThreads, x = threadIdx.x % kThreads;
-  if (A.B.offsets && (row < A.B.offsets[0] || row >= A.B.offsets[A.B.seqs])) return;     // a row of no sequence
   const int h = blockIdx.y * kEach + e, wave = threadIdx.x >> 6, first = e * kWavesEach;
   const int64_t head = (int64_t)row * A.heads + min(h, A.heads - 1);
   const float2 *ml = A.ml + head * A.splits;
-  float top = -INFINITY, sum = 0.0f;
-  for (int z = x; z < A.splits; z += kThreads) top = fmaxf(top, ml[z].x);
+  const int d = x % kLanes, r = x / kLanes;
+  const f32x4_t *p = reinterpret_cast<const f32x4_t *>(A.part + head * A.splits * kDp) + d;
+  // everything goes out at once, before it is known which parts there are: what was not written is not used
+  f32x4_t v[kFirst];
+#pragma unroll
+  for (int i = 0; i < kFirst; ++i) v[i] = p[(int64_t)min(r + i * kRows, A.splits - 1) * kLanes];
+  const float2 mine = ml[min(x, A.splits - 1)];
+  if (A.B.offsets && (row < A.B.offsets[0] || row >= A.B.offsets[A.B.seqs])) return;     // a row of no sequence
+  float top = mine.x, sum = 0.0f;
+  for (int z = x + kThreads; z < A.splits; z += kThreads) top = fmaxf(top, ml[z].x);
   top = wave_max(top);
   if constexpr (kWavesEach > 1) {
     if ((threadIdx.x & 63) == 0) red[0][wave] = top;
     __syncthreads();
 #pragma unroll
-    for (int v = 0; v < kWavesEach; ++v) top = fmaxf(top, red[0][first + v]);
+    for (int i = 0; i < kWavesEach; ++i) top = fmaxf(top, red[0][first + i]);
   }
   for (int z = x; z < A.splits; z += kThreads) {
-    const float2 v = ml[z];
+    const float2 m = z == x ? mine : ml[z];
     // no maximum anywhere: nothing was seen (0), or NaN
-    const float f = v.y == 0.0f ? 0.0f : top > -INFINITY ? __builtin_amdgcn_exp2f(v.x - top) : v.y;
+    const float f = m.y == 0.0f ? 0.0f : top > -INFINITY ? __builtin_amdgcn_exp2f(m.x - top) : m.y;
     w[e][z] = f;
-    sum = fmaf(v.y, f, sum);
+    sum = fmaf(m.y, f, sum);
   }
   sum = group_sum<64>(sum);
   if ((threadIdx.x & 63) == 0) red[1][wave] = sum;
   __syncthreads();
   sum = 0.0f;
 #pragma unroll
-  for (int v = 0; v < kWavesEach; ++v) sum += red[1][first + v];
-  const int d = x % kLanes, r = x / kLanes;
-  const f32x4_t *p = reinterpret_cast<const f32x4_t *>(A.part + head * A.splits * kDp) + d;
+  for (int i = 0; i < kWavesEach; ++i) sum += red[1][first + i];
   if (r < kRows) {
     f32x4_t acc = {};
-#pragma unroll 4
-    for (int z = r; z < A.splits; z += kRows) {
+    const auto add = [&](int z, f32x4_t part) {
       const float f = w[e][z];
-      if (f != 0.0f) {                                                   // others may not have been written
-        const f32x4_t v = p[(int64_t)z * kLanes];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = fmaf(v[i], f, acc[i]);
-      }
-    }
+      for (int i = 0; i < 4; ++i) acc[i] = f != 0.0f ? fmaf(part[i], f, acc[i]) : acc[i];
+    };
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i)
+      if (r + i * kRows < A.splits) add(r + i * kRows, v[i]);
+#pragma unroll 4
+    for (int z = r + kFirst * kRows; z < A.splits; z += kRows) add(z, p[(int64_t)z * kLanes]);
     sums[e][r][d] = acc;
   }
   __syncthreads();
