@@ -68,8 +68,8 @@ __global__ __launch_bounds__(64 * kWaves, (kDp > 128 || kTermsOf<T> > 1) ? 1 : 2
   const int pos = s.first() + i, first = s.first() + min(c0, tile_last) / rep, last = s.first() + last_c / rep;
   const int lo = A.window ? max(0, pos - A.window + 1) : 0, hi = min(pos + 1, limit);
 
-  // Sums of values are in units of the scale of the page that came last, v_unit: pages' scales are powers of two and
-  // mostly the same, and then the second product adds to them as they are.
+  // A row's sums of values are in units of the scale of the last page that it sees, v_unit: pages' scales are powers of two
+  // and mostly the same, and then the second product adds to them as they are.
   f32x16 o[kCols] = {};
   float m = -INFINITY, l = 0.0f, v_unit = 0.0f;
   if (p0 < p1) {
@@ -219,22 +219,20 @@ __global__ __launch_bounds__(64 * kWaves, (kDp > 128 || kTermsOf<T> > 1) ? 1 : 2
           }
         rare = __ballot(bad) != 0;
       }
-      // Another scale: the sums change to its units.  A page of far smaller ones (below 2^-40 of the units, or 0) is summed
-      // apart and added with its share of them instead, so that neither leaves fp32.
+      // Another scale: the row's sums change to its units, exactly.  A page whose scale is outside [2^-40, 2^16] is summed apart
+      // and added with its share of the nearer end.  From a scale of 2^16 on the units stay there: sums of numbers up to fp32's
+      // largest then stay below 2^123 and shares above 2^-142, and else sums are below 2^76 times the positions.
+      constexpr float kLeast = 0x1p-40f, kMost = 0x1p16f;
       float share = 1.0f;
-      if (vs != v_unit || vs == 0.0f) {
-        if (vs > 0.0f && v_unit == 0.0f) {
-          v_unit = vs;                                                   // the first
-        } else if (vs > 0.0f && v_unit / vs < 0x1p40f) {
-          const float by = v_unit / vs;
+      if (top > -INFINITY && vs != v_unit) {
+        const float unit = v_unit == kMost ? kMost : fminf(fmaxf(vs, kLeast), kMost);
+        const float by = v_unit / unit;                                  // the first page's sums are of zeros
 #pragma unroll
-          for (int d = 0; d < kCols; ++d) o[d] *= by;
-          v_unit = vs;
-        } else {
-          share = v_unit > 0.0f ? vs / v_unit : vs;
-          rare = 1;
-        }
+        for (int d = 0; d < kCols; ++d) o[d] *= by;
+        v_unit = unit;
+        share = vs / unit;
       }
+      rare |= __ballot(share != 1.0f) != 0;
       if (__builtin_expect(!__builtin_amdgcn_readfirstlane(rare), 1)) {
         __builtin_amdgcn_s_setprio(1);
         i32x4 vn[2] = {value(0, 0), value(0, 1)};

@@ -449,6 +449,21 @@ def test_attention_of_far_scales(news, width, dtype):
     check_attention(rng, lens, [news], 4, 2, 64, dtype, cache=cache, pages=pages, off=off, scale=0.7, q=q)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("window", [0, 30])
+@pytest.mark.parametrize("large", [0, 1, 2])
+@pytest.mark.parametrize("width", [0, WIDE])
+def test_attention_of_a_page_near_the_largest_number(width, large, window, dtype):
+    """Rows that do not see the page keep their sums, 2^157 smaller, as they are."""
+    rng = np.random.default_rng(36)
+    lens, news = [200], [150]
+    pages, off, count = batch(rng, lens, news)
+    cache = filled(rng, count, 2, 64)
+    cache["v_scale"][:] = 2.0 ** -50
+    cache["v_scale"][pages[0, large]] = 2.0 ** 107
+    check_attention(rng, lens, news, 4, 2, 64, dtype, window, cache=cache, pages=pages, off=off, width=width)
+
+
 @pytest.mark.parametrize("width", [0, WIDE])
 def test_attention_of_shared_pages(width):
     """Two sequences whose first pages are the same, and a page that a table names twice."""
