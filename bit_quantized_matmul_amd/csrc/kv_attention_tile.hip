@@ -1,7 +1,7 @@
 // Attention over the paged 8-bit cache: many rows a sequence.
 //
 // Bound by arithmetic: 4 x 2048 rows of 8192 positions, 32 heads of 128 columns to 8: 1070 us, 900 TFLOP/s.  The vector
-// instructions (410 a wave and page, 128 of them conversions and 32 exponentials) are busy 73% of the time, the matrix
+// instructions (410 a wave and page, 128 of them conversions and 32 exponentials) are busy 69% of the time, the matrix
 // instructions (32) 40%; two waves a SIMD hide no more.  Codes widened once a workgroup, to fp16 in LDS, took a fourth of the vector
 // instructions away and 13% more time: twice the reads of LDS, whose latency two waves do not hide.
 //
