@@ -168,7 +168,8 @@ __global__ __launch_bounds__(64 * NW) void kv_stream_kernel(AttnArgs A, bool qve
         to_terms<kTerms>(e, p[a]);
         l = add_terms<kTerms>(p[a], l);
       }
-      const float v_scale = vs * 0x1p-15f;
+      // of a row that sees none of the page's positions 0, and not what may be no number
+      const float v_scale = top > -INFINITY ? vs * 0x1p-15f : 0.0f;
       if (!whole) {
         // what some row does not see may be NaN, and 0 times it would be too: such codes are taken out, and
         // the sums of the rows that do see them made NaN

@@ -1,0 +1,50 @@
+"""The attention over the 8-bit cache at the ends of its range, and how many bits its probabilities hold; what
+rope returns; the calls in a row against attention over the whole in one call.
+
+``sharp`` is the attention's bound with probabilities of 22 bits (two fp16 terms): with e as in test_gpu_kv.py, out is off by at most
+    (2 e + 2^-21 + 2^-22 + (66 + L / 16) 2^-22) sum p |v| + 2^-40 sum |v|.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from bit_quantized_matmul_amd import binding as B
+from oracle import fp8 as of8
+from oracle import kv as okv
+from tests.test_gpu_kv import DEV, F8, TYPES, WIDE, attention_tol, batch, check, check_attention, dev, filled, host, ints, on_device, rounded, widened
+
+pytestmark = pytest.mark.gpu
+
+
+def sharp(mag, most, small, dp, length, dtype):
+    return attention_tol(mag, most, small / (1 if dtype == torch.float32 else 16), dp, length, dtype) - (0 if dtype == torch.float32 else (2.0 ** -11 - 2.0 ** -22) * mag)
+
+
+# ------------------------------------------------------------------ masked scales, far parts
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("which", ["k_scale", "v_scale"])
+@pytest.mark.parametrize("news,window", [(10, 0), (10, 40), (150, 0), (150, 30)])
+@pytest.mark.parametrize("width", [0, WIDE])
+def test_scales_of_pages_that_only_some_rows_see(width, news, window, which, bad, dtype):
+    """A page with a scale that is not finite beside rows of the same tile that end before it or begin after it."""
+    rng = np.random.default_rng(news + window)
+    length, heads, kv, dim = 198, 4, 2, 64
+    pages, off, count = batch(rng, [length], [news])
+    pages = widened(pages, width)
+    clean = filled(rng, count, kv, dim)
+    q = rng.standard_normal((news, heads, dim))
+    base, _ = check_attention(rng, [length], [news], heads, kv, dim, dtype, window, cache=clean, pages=pages, off=off, q=q)
+    _, d = rounded(q, dtype)
+    pos = length - news + np.arange(news)
+    for page in range(4):
+        spoiled = {n: a.copy() for n, a in clean.items()}
+        spoiled[which][pages[0, page], 1] = bad                          # read by heads 2 and 3
+        got = host(B.kv_attention(d, on_device(spoiled), ints(pages), ints([length]), ints(off), window=window))
+        sees = (pos >= 64 * page) & ((pos - window < 64 * page + 63) if window else True)
+        assert np.array_equal(got[:, :2], base[:, :2]) and np.array_equal(got[~sees], base[~sees])
+        gone = ~np.isfinite(got[sees][:, 2:])
+        assert gone.all() or which == "k_scale" and bad == float("inf")   # scores of -inf beside +inf may leave one key
