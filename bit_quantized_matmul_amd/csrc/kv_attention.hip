@@ -286,10 +286,11 @@ __global__ __launch_bounds__(256) void kv_join_kernel(AttnArgs A, T *__restrict_
   }
   for (int z = x; z < A.splits; z += kThreads) {
     const float2 m = z == x ? mine : ml[z];
-    // no maximum anywhere: nothing was seen (0), or NaN
-    const float f = m.y == 0.0f ? 0.0f : top > -INFINITY ? __builtin_amdgcn_exp2f(m.x - top) : m.y;
+    // nothing was seen (the part may not be written: marked by -1), or no maximum anywhere: NaN.  A weight that is too small
+    // for fp32 stays 0: what is NaN in such a part was attended to as well.
+    const float f = m.y == 0.0f ? -1.0f : top > -INFINITY ? __builtin_amdgcn_exp2f(m.x - top) : m.y;
     w[e][z] = f;
-    sum = fmaf(m.y, f, sum);
+    sum = f < 0.0f ? sum : fmaf(m.y, f, sum);
   }
   sum = group_sum<64>(sum);
   if ((threadIdx.x & 63) == 0) red[1][wave] = sum;
@@ -302,7 +303,7 @@ __global__ __launch_bounds__(256) void kv_join_kernel(AttnArgs A, T *__restrict_
     const auto add = [&](int z, f32x4_t part) {
       const float f = w[e][z];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = f != 0.0f ? fmaf(part[i], f, acc[i]) : acc[i];
+      for (int i = 0; i < 4; ++i) acc[i] = f < 0.0f ? acc[i] : fmaf(part[i], f, acc[i]);
     };
 #pragma unroll
     for (int i = 0; i < kFirst; ++i)

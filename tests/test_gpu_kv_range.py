@@ -48,3 +48,31 @@ def test_scales_of_pages_that_only_some_rows_see(width, news, window, which, bad
         assert np.array_equal(got[:, :2], base[:, :2]) and np.array_equal(got[~sees], base[~sees])
         gone = ~np.isfinite(got[sees][:, 2:])
         assert gone.all() or which == "k_scale" and bad == float("inf")   # scores of -inf beside +inf may leave one key
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("news,heads,kv,width", [(1, 4, 2, 64), (1, 1, 1, 2000), (40, 4, 2, 2000), (200, 4, 1, 64)])
+def test_nan_values_of_far_scores(news, heads, kv, width, dtype):
+    """A NaN value whose probability is below fp32's numbers is attended to all the same: its column is NaN, also where its
+    page is in another part than the row's largest score."""
+    rng = np.random.default_rng(width + news)
+    dim, length = 64, 64 * 40 + news
+    pages, off, count = batch(rng, [length], [news])
+    pages = widened(pages, width)
+    cache = okv.empty(count, kv, dim)
+    cache["v"][:] = of8.encode(rng.standard_normal(cache["v"].shape))
+    cache["k_scale"][:], cache["v_scale"][:] = 1.0, 1.0
+    near, far = pages[0, 3], pages[0, 30]
+    cache["k"][..., 0] = of8.encode(-448.0)                              # scores of -448 and, on page 3, of 0
+    cache["k"][near, ..., 0] = 0
+    q = np.zeros((news, heads, dim))
+    q[..., 0] = 1.0
+    args = (rounded(q, dtype)[1], ints(pages), ints([length]), ints(off))
+    run = lambda c: host(B.kv_attention(args[0], on_device(c), *args[1:], scale=1.0))   # noqa: E731
+    base = run(cache)
+    assert np.all(np.isfinite(base))
+    cache["v"][far, :, 5, 17] = 0x7F
+    got = run(cache)
+    assert np.all(np.isnan(got[..., 5]))
+    keep = np.arange(dim) != 5
+    assert np.array_equal(got[..., keep], base[..., keep])
