@@ -22,7 +22,9 @@ namespace {
 template <typename T, int kDp, int NW>
 __global__ __launch_bounds__(64 * NW) void kv_stream_kernel(AttnArgs A, bool qvec, const T *__restrict__ q,
                                                             T *__restrict__ out) {
-  constexpr int kTerms = kTermsOf<T>, kWide = kDp / 64, kSteps = kDp / 32, kCols = kDp / 16;
+  // Probabilities are two fp16 terms for every type: one, of 11 bits, leaves errors like half a step of an fp16 result, and the kernel
+  // waits for memory (one token of 131072: the same; 64 of up to 8192: 116 us with one term, 117 with two).
+  constexpr int kTerms = kTermsOf<T>, kPTerms = 2, kWide = kDp / 64, kSteps = kDp / 32, kCols = kDp / 16;
   constexpr bool kOdd = kDp % 64 != 0;    // a last half chunk of 32 columns
   KvSeq s;
   int job;
@@ -156,7 +158,7 @@ __global__ __launch_bounds__(64 * NW) void kv_stream_kernel(AttnArgs A, bool qve
         for (int d = 0; d < kCols; ++d) o[d] *= alpha;
         m = m1;
       }
-      f16x8 p[2][kTerms];
+      f16x8 p[2][kPTerms];
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
         float e[8];
@@ -165,8 +167,8 @@ __global__ __launch_bounds__(64 * NW) void kv_stream_kernel(AttnArgs A, bool qve
           const float v = __builtin_amdgcn_exp2f(fmaf(x[2 * a + r / 4][r % 4], f, -base));
           e[r] = whole || (see >> (8 * a + r) & 1) ? v : 0.0f;
         }
-        to_terms<kTerms>(e, p[a]);
-        l = add_terms<kTerms>(p[a], l);
+        to_terms<kPTerms>(e, p[a]);
+        l = add_terms<kPTerms>(p[a], l);
       }
       // of a row that sees none of the page's positions 0, and not what may be no number
       const float v_scale = top > -INFINITY ? vs * 0x1p-15f : 0.0f;
@@ -203,7 +205,7 @@ __global__ __launch_bounds__(64 * NW) void kv_stream_kernel(AttnArgs A, bool qve
         for (int a = 0; a < 2; ++a) {
           const f16x8 v = widen(vw[d][2 * a], vw[d][2 * a + 1]);
 #pragma unroll
-          for (int z = 0; z < kTerms; ++z) part = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[a][z], part, 0, 0, 0);
+          for (int z = 0; z < kPTerms; ++z) part = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[a][z], part, 0, 0, 0);
         }
 #pragma unroll
         for (int w = 0; w < 4; ++w) o[d][w] = fmaf(part[w], v_scale, o[d][w]);

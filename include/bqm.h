@@ -532,8 +532,8 @@ int kv_append(const void *k, const void *v, int dtype, int tokens, int heads, in
 /* out[t, h] = sum_j p_j v_j, p = softmax over j of scale (q[t, h] . k_j), over the positions j of the
  * cache with position(t) - window < j <= position(t) (window 0: no lower bound), keys and values of head
  * h / (heads / kv_heads).  A row that sees no position is zeros; rows of no sequence are not
- * written.  Products are summed in fp32 (q and p as one or, for an fp32 q, two fp16 terms; p to 2^-36
- * or 2^-40 of the row's largest), the maxima and sums of the softmax are fp32, out is rounded once.  Sums of
+ * written.  Products are summed in fp32 (q as one fp16 term, an fp32 q as two; p as two, or one where
+ * q is of 16 bits and sequences have many rows; p to 2^-36 or 2^-40 of the row's largest), the maxima and sums of the softmax are fp32, out is rounded once.  Sums of
  * values weigh the row's largest p as 1: values times positions have to stay below fp32's largest
  * number.  What is masked has no part in the result, whatever it holds; a NaN code that is attended to makes NaN.
  * q [device] `dtype` [tokens, heads, dim], tokens and heads the given strides apart; out [device] `dtype`

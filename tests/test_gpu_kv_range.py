@@ -76,3 +76,27 @@ def test_nan_values_of_far_scores(news, heads, kv, width, dtype):
     assert np.all(np.isnan(got[..., 5]))
     keep = np.arange(dim) != 5
     assert np.array_equal(got[..., keep], base[..., keep])
+
+
+# ------------------------------------------------------------------ bits of the probabilities
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim,heads,kv", [(32, 6, 2), (128, 4, 1), (80, 8, 8), (256, 2, 1)])
+@pytest.mark.parametrize("length,news", [(20, 1), (64, 1), (40, 3), (2000, 1)])
+def test_probabilities_of_few_rows_hold_22_bits(length, news, dim, heads, kv, dtype):
+    """Values of both signs that nearly cancel, so that a result is as small as the errors of its probabilities: half a step of the
+    result's type hides none of them."""
+    rng = np.random.default_rng(length + dim)
+    pages, off, count = batch(rng, [length], [news])
+    cache = filled(rng, count, kv, dim)
+    cache["v"][..., 1::2] = cache["v"][..., 0::2] ^ 0x80                 # neighbouring tokens' values cancel
+    cache["k"][..., 1::2, :] = cache["k"][..., 0::2, :]
+    cache["k"][..., 1::2, 0] = of8.encode(0.0)                           # but for one column of their keys
+    cache["k"][..., 0::2, 0] = of8.encode(448.0)
+    cache["k_scale"][:], cache["v_scale"][:] = 2.0 ** -9, 1.0
+    q = 0.05 * rng.standard_normal((news, heads, dim))
+    q[..., 0] = 0.02
+    q, d = rounded(q, dtype)
+    got = B.kv_attention(d, on_device(cache), ints(pages), ints([length]), ints(off))
+    ref, mag, most, small = okv.attention(q, cache, pages, [length], off)
+    check(host(got), ref, sharp(mag, most, small, okv.padded_dim(dim), length, dtype), dtype)
