@@ -60,18 +60,22 @@ template <typename T> constexpr int kXTerms = sizeof(T) == 4 ? 3 : 1;
 template <typename T> constexpr int kActTerms = sizeof(T) == 4 ? 3 : 2;
 template <typename T> using Half8 = std::conditional_t<std::is_same_v<T, _Float16>, f16x8, bf16x8>;
 
+// Codes go into bf16 products as 2^-17 of themselves, exactly: sums of 128 products of up to 448 times fp32's largest number stay in
+// fp32 so, and a block's scale can bring them back.  What was summed is 2^17 times that (fp16 rows reach no such sums).
+template <typename H> constexpr float kCode = std::is_same_v<H, f16x8> ? 1.0f : 0x1p-17f;
+
 template <typename H>
 __device__ __forceinline__ H widen_as(int lo, int hi) {
   H h;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     if constexpr (std::is_same_v<H, f16x8>) {
-      const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(i ? hi : lo, 1.0f, false);
-      const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(i ? hi : lo, 1.0f, true);
+      const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(i ? hi : lo, kCode<H>, false);
+      const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(i ? hi : lo, kCode<H>, true);
       h[4 * i] = a[0], h[4 * i + 1] = a[1], h[4 * i + 2] = b[0], h[4 * i + 3] = b[1];
     } else {
-      const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(i ? hi : lo, 1.0f, false);
-      const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(i ? hi : lo, 1.0f, true);
+      const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(i ? hi : lo, kCode<H>, false);
+      const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(i ? hi : lo, kCode<H>, true);
       h[4 * i] = a[0], h[4 * i + 1] = a[1], h[4 * i + 2] = b[0], h[4 * i + 3] = b[1];
     }
   }
@@ -332,6 +336,7 @@ __global__ __launch_bounds__(64 * kUpWaves, sizeof(T) == 2 ? 4 : 2) void moe_up_
         s[h] = lds.red[turn & 1][group][0][h][lane];
 #pragma unroll
         for (int v = 1; v < NW; ++v) s[h] += lds.red[turn & 1][group][v][h][lane];
+        s[h] *= 1.0f / kCode<H>;
       }
       const float w = by_place[p0 + row];
       bf16x4 t[kActTerms<T>];
@@ -476,7 +481,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down_kernel(MoeArgs A,
     sum = 0.0f;
     for (int z = 0; z < A.splits; ++z) sum += __hip_atomic_load(mine + z * NW * 64, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  if (t < A.tokens && n0 + r < A.hidden) out[(int64_t)t * A.hidden + n0 + r] = from_sum<T>(sum);
+  if (t < A.tokens && n0 + r < A.hidden) out[(int64_t)t * A.hidden + n0 + r] = from_sum<T>(sum * (1.0f / kCode<bf16x8>));
 }
 
 int row_tiles(int hidden) { return (hidden + kTile - 1) / kTile; }

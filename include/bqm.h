@@ -470,7 +470,8 @@ int moe_combine(const void *y, int dtype, int64_t y_rows, int d, const int32_t *
  *   out[t] = sum_j w[t, j] W2[e_j] (silu(G[e_j] x_t) * (U[e_j] x_t)),  W13 = [G | U],
  * e_j and w[t, j] as moe_route gives them (the same ties, masks and renorm; a token without an
  * expert has a row of zeros).  x is not quantized: the products of its elements and the codes are summed
- * in fp32 (an fp32 x as three bf16 terms, the hidden rows as two or, for an fp32 x, three), and out is
+ * in fp32 (an fp32 x as three bf16 terms, the hidden rows as two or, for an fp32 x, three; sums of a block may pass
+ * fp32's largest number before its scale, and products below 2^-109 lose bits), and out is
  * rounded once.  A row of x with a NaN or an infinity, and an expert, has a row of NaN.
  * x [device] `dtype` [tokens, hidden], rows x_stride apart; logits [device] `logits_dtype` [tokens,
  * experts], rows logits_stride apart; w13 [device] [experts, 2 ffn, 128 ceil(hidden / 128)] and w2
