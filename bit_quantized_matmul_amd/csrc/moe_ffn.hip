@@ -15,7 +15,8 @@
 // the same registers, so the combination is part of the sum.
 //
 // Operands.  Codes are exact in fp16 and bf16, so 16-bit rows of x enter as they are; an fp32 x is three bf16 terms,
-// which hold its 24 bits.  Hidden rows are two bf16 terms (2^-17), for an fp32 x three.
+// which hold its 24 bits.  Hidden rows are two bf16 terms (2^-17 against half a step of 2^-8 or, in fp16, 2^-11 of the result; a third
+// would be half as much to read again), for an fp32 x three.
 #include "moe_choose.h"
 
 #include <type_traits>
@@ -106,9 +107,11 @@ __device__ __forceinline__ void load_x8(const T *p, int c, int cols, bool vec, H
     if constexpr (sizeof(T) == 2) {
       t[0][i] = v[i];
     } else {
-      float r = v[i];
+      // the first term is cut, so that it is finite where x is; what it leaves, 16 bits, are two more, exactly
+      t[0][i] = __builtin_bit_cast(__bf16, (uint16_t)(__float_as_uint(v[i]) >> 16));
+      float r = v[i] - __uint_as_float(__float_as_uint(v[i]) & 0xFFFF0000u);
 #pragma unroll
-      for (int z = 0; z < 3; ++z) {
+      for (int z = 1; z < 3; ++z) {
         t[z][i] = (__bf16)r;
         r -= (float)t[z][i];
       }
@@ -152,7 +155,10 @@ __device__ __forceinline__ void choose_all(const MoeArgs &A, Choices &C) {
 }
 static_assert(kUpWaves * 64 / 16 >= kMoeFewTokens, "16 lanes a token");
 
-// The experts that have tokens into `L` and the weights in the pairs' order into `by_place` (LDS).
+// Hidden rows go out as half of themselves, so that the nearest bf16 of each is finite.
+constexpr float kHidden = 0.5f;
+
+// The experts that have tokens into `L` and the weights, times kHidden, in the pairs' order into `by_place` (LDS).
 __device__ void list_experts(const MoeArgs &A, Choices &C, MoeList &L, float *by_place) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   constexpr int kThreads = kUpWaves * 64, kPer = kMaxExperts / kThreads;
@@ -194,7 +200,7 @@ __device__ void list_experts(const MoeArgs &A, Choices &C, MoeList &L, float *by
   // a pair's place: its expert's first, and the expert's tokens before it
   for (int i = tid; i < A.tokens * A.top; i += kThreads) {
     const int e = C.ids[i], tok = i / A.top;
-    if (e >= 0) by_place[C.first[e] + __popc(C.tokens[e] & ((1u << tok) - 1u))] = C.weights[i];
+    if (e >= 0) by_place[C.first[e] + __popc(C.tokens[e] & ((1u << tok) - 1u))] = kHidden * C.weights[i];
   }
   __syncthreads();
 }
@@ -481,7 +487,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down_kernel(MoeArgs A,
     sum = 0.0f;
     for (int z = 0; z < A.splits; ++z) sum += __hip_atomic_load(mine + z * NW * 64, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  if (t < A.tokens && n0 + r < A.hidden) out[(int64_t)t * A.hidden + n0 + r] = from_sum<T>(sum * (1.0f / kCode<bf16x8>));
+  if (t < A.tokens && n0 + r < A.hidden) out[(int64_t)t * A.hidden + n0 + r] = from_sum<T>(sum * (1.0f / (kCode<bf16x8> * kHidden)));
 }
 
 int row_tiles(int hidden) { return (hidden + kTile - 1) / kTile; }

@@ -471,8 +471,9 @@ int moe_combine(const void *y, int dtype, int64_t y_rows, int d, const int32_t *
  * e_j and w[t, j] as moe_route gives them (the same ties, masks and renorm; a token without an
  * expert has a row of zeros).  x is not quantized: the products of its elements and the codes are summed
  * in fp32 (an fp32 x as three bf16 terms, the hidden rows as two or, for an fp32 x, three; sums of a block may pass
- * fp32's largest number before its scale, and products below 2^-109 lose bits), and out is
- * rounded once.  A row of x with a NaN or an infinity, and an expert, has a row of NaN.
+ * fp32's largest number before its scale, and products below 2^-108 lose bits), and out is
+ * rounded once.  A row of x with a NaN or an infinity, and an expert, has a row of NaN; so has one with a
+ * gate, an up value or their silu(gate) * up past fp32's largest number.
  * x [device] `dtype` [tokens, hidden], rows x_stride apart; logits [device] `logits_dtype` [tokens,
  * experts], rows logits_stride apart; w13 [device] [experts, 2 ffn, 128 ceil(hidden / 128)] and w2
  * [experts, hidden, 128 ceil(ffn / 128)] with their scales, both as fp8_pack writes them, 16-byte

@@ -52,6 +52,22 @@ def ones(rows, cols, s=1.0):
 # ------------------------------------------------------------------ range
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("hidden", [1, 40, 300])
+def test_largest_numbers_in_a_row(hidden, dtype):
+    """A row that holds the type's largest numbers, with scales that bring its products back: codes up to 1, so that a
+    block's sum of one column stays in fp32 unscaled too."""
+    rng = np.random.default_rng(hidden)
+    big = torch.finfo(dtype).max
+    x = np.zeros((3, hidden))
+    x[0, 0], x[1, hidden // 2], x[2, -1] = big, -big, big * (1 - 2.0 ** -7)
+    ffn = 20
+    w13 = codes(2 * ffn, hidden, rng.choice([-1.0, -0.625, 0.25, 0.5, 1.0], (2 * ffn, hidden)), np.s_[:, :hidden])
+    w2 = codes(hidden, ffn, rng.standard_normal((hidden, ffn)), np.s_[:, :ffn])
+    got, ref, mag = layer(x, w13, ones(2 * ffn, hidden, 2.0 ** -126), w2, ones(hidden, ffn), np.zeros((3, 1)), 1, dtype)
+    check(got, ref, tol(mag, hidden, ffn, 1, dtype), dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_small_numbers(dtype):
     """Rows and hidden rows of 2^-85, whose last terms lie far below: nothing of them is lost."""
     rng = np.random.default_rng(4)
@@ -82,6 +98,20 @@ def test_sums_of_large_numbers(tokens, experts, top, hidden, ffn, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("ffn", [1, 33, 129])
+def test_hidden_rows_near_the_largest_number(ffn, dtype):
+    """silu(gate) * up = 0.999 x 2^128, past the nearest bf16 that is finite."""
+    x = np.ones((1, 1))
+    s13 = ones(2 * ffn, 1, np.float32(np.sqrt(0.999) * 2.0 ** 64))
+    w13 = codes(2 * ffn, 1, 1.0, np.s_[:, :1])
+    signs = np.where(np.arange(ffn) % 2, -1.0, 1.0) * np.where(np.arange(ffn) % 3, 0.5, 1.0)
+    w2 = codes(1, ffn, signs, np.s_[0, :ffn])
+    got, ref, mag = layer(x, w13, s13, w2, ones(1, ffn, 2.0 ** -120), np.zeros((1, 1)), 1, dtype)
+    assert np.all(np.abs(ref) > 1.0)
+    check(got, ref, tol(mag, 1, ffn, 1, dtype), dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_sums_of_large_hidden_rows(dtype):
     rng = np.random.default_rng(5)
     hidden, ffn = 60, 200
@@ -92,6 +122,27 @@ def test_sums_of_large_hidden_rows(dtype):
                           rng.standard_normal((4, 2)), 2, dtype)
     assert np.all(np.isfinite(ref)) and np.abs(ref).max() > 1.0
     check(got, ref, tol(mag, hidden, ffn, 2, dtype), dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_what_leaves_fp32_is_nan(dtype):
+    """Gates, up rows and hidden rows past fp32: rows of NaN, and the other tokens' as they were."""
+    rng = np.random.default_rng(6)
+    hidden, ffn = 64, 48
+    q13, s13 = weights(rng, 1, 2 * ffn, hidden)
+    q2, s2 = weights(rng, 1, hidden, ffn)
+    s13 = (s13 * np.float32(2.0 ** 60)).astype(np.float32)
+    s2 = (s2 * np.float32(2.0 ** -115)).astype(np.float32)
+    x = np.abs(rng.standard_normal((4, hidden))) * 2.0 ** -3
+    clean, ref, mag = layer(x, q13, s13, q2, s2, np.zeros((4, 1)), 1, dtype)
+    check(clean, ref, tol(mag, hidden, ffn, 1, dtype), dtype)
+    x[1] *= 2.0 ** 12                                                    # gate times up is past 2^128
+    if dtype != torch.float16:
+        x[3] *= 2.0 ** 90                                                # gates and up rows are
+    got, _, _ = layer(x, q13, s13, q2, s2, np.zeros((4, 1)), 1, dtype)
+    gone = [1] if dtype == torch.float16 else [1, 3]
+    rest = [t for t in range(4) if t not in gone]
+    assert np.all(np.isnan(got[gone])) and np.array_equal(got[rest], clean[rest])
 
 
 # ------------------------------------------------------------------ bits
