@@ -134,7 +134,8 @@ __device__ __forceinline__ void pages_of(const AttnArgs &A, const KvSeq &s, int 
   *p1 = end > begin ? (end - 1) / kPage + 1 : *p0;
 }
 
-// Tiles of 128 queries (kv_attention_tile.hip).
+// Tiles of 128 queries (kv_attention_tile.hip): fp32 heads up to kMostTileF32 columns, padded.
+constexpr int kMostTileF32 = 192;
 hipError_t launch_tiles(const AttnArgs &A, bool vec, const void *q, int dtype, void *out, hipStream_t s);
 
 }  // namespace attn

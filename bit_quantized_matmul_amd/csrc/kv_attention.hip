@@ -8,6 +8,8 @@
 // are far apart cost no bits.
 #include "kv_attention.h"
 
+#include <algorithm>
+
 namespace bqm {
 namespace attn {
 namespace {
@@ -335,23 +337,45 @@ struct Plan {
 
 int64_t above(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tiles of 128 queries where a sequence has more than 16 in the mean and there is work for them: 6000 pages times key
-// heads times 32 queries.  (us in tiles of 16 / 128 queries, 32 heads to 8 key heads, 128 columns: 64 sequences of 2048
-// with 16 queries of a key head each 44 / 61, with 32 83 / 62, with 128 298 / 109; one of 8192 with 64, 128 and 256:
-// 24 / 36, 32 / 38, 54 / 41; 8 of 2048 with 64 and 96: 32 / 37, 42 / 39.)
-//
+// Tiles of 128 queries where a sequence has many in the mean and there is work for them, in pages times key heads
+// times 32 queries.  How many depends on how many waves the tile's registers leave (16 bits up to 128 columns two or more a SIMD,
+// fp32 one from 96 columns on, all one past 128) and on fp32's two terms, which cost the tiles more: they are bound by arithmetic,
+// the others by memory.  us in tiles of 16 / 128 queries, 8 key heads; sequences x rows of positions, 32 heads:
+//                16 bits, 128 columns   192            256            fp32, 64       128            192            256
+//   1 x 64 of 8192         56 / 41      66 / 76        110 / 114      34 / 35        58 / 74        90 / 95        113 / 207
+//   64 x 8 of 2048        100 / 65      136 / 192      209 / 326      58 / 68        102 / 191      164 / 262      209 / 561
+//   64 x 16 of 2048       170 / 126     239 / 290      375 / 485      88 / 135       171 / 291      288 / 398      372 / 799
+//   128 x 20 of 300       126 / 52      157 / 119      357 / 184      67 / 50        131 / 109      279 / 151      393 / 335
+//   16 x 32 of 4096       177 / 99      253 / 209      384 / 365      96 / 97        182 / 211      295 / 291      386 / 658
+//   64 x 64 of 512        177 / 74      219 / 163      479 / 267      102 / 76       182 / 158      384 / 226      520 / 546
+//   1 x 512 of 8192       241 / 104     289 / 223      561 / 350      141 / 109      252 / 222      454 / 302      584 / 789
+//   4 x 2048 of 4096     1274 / 498    1471 / 1111    2881 / 1877     737 / 528     1306 / 1166    2416 / 1601    2943 / 4530
+//   8 heads: 16 x 256 of 1024
+//                          75 / 55      92 / 110       190 / 165      44 / 52        79 / 104       150 / 145      196 / 314
+// fp32 of 256 columns, whose queries alone are 256 registers, stays in tiles of 16 (there is no other kernel of it).
+struct ManyRule {
+  int queries;                            // more than these a sequence
+  int64_t work;                           // and no less than this
+};
+bool takes_many(int dtype, int dim, int64_t queries, int64_t runs, int kv_heads, int width) {
+  const int dp = kv_padded_dim(dim);
+  if (dtype == BQM_F32 && dp > kMostTileF32) return false;
+  const ManyRule r = dp > 128 ? ManyRule{64, 12000} : dtype == BQM_F32 ? ManyRule{128, 24000} : ManyRule{16, 6000};
+  return queries > r.queries * runs && above(queries, 32 * runs) * runs * kv_heads * width >= r.work;
+}
+
 // Pages a workgroup takes.  Tiles of 16: one workgroup a CU where all sequences are as long as the table is wide, but 4
 // pages at least (one a wave), all of up to 8, and 32 at most, so that sequences of unlike length share the CUs (us with
 // 4 / 8 / 16 / 32 pages: one sequence of 512 10.4 / 9.1 / 9.0 / 9.0, of 8192 11.8 / 13.0 / 16.2 / 23.4, of 131072 96 / 75 / 64
 // / 58; 4 of 4096 16.4 / 14.8 / 18.0 / 25.2; 16 of 8192 69 / 59 / 50 / 48; 64 of up to 8192 110 with 32, 121 with 128).  The
 // parts of all workgroups are bounded too.  Tiles of 128: two workgroups a CU, 8 pages at least (us with 8 / 16 / 32 / 64
 // pages: 128 rows of 8192 50 / 59 / 65 / 110, 512 145 / 119 / 106 / 160).
-Plan plan(int tokens, int seqs, int heads, int kv_heads, int width, int window) {
-  constexpr int64_t kManyWork = 6000, kMostGroups = 4096;
+Plan plan(int dtype, int tokens, int seqs, int heads, int kv_heads, int dim, int width, int window) {
+  constexpr int64_t kMostGroups = 4096;
   const int rep = heads / kv_heads;
   const int64_t runs = seqs < tokens ? seqs : tokens, queries = (int64_t)tokens * rep;
   Plan p;
-  p.many = queries > 16 * runs && above(queries, 32 * runs) * runs * kv_heads * width >= kManyWork;
+  p.many = takes_many(dtype, dim, queries, runs, kv_heads, width);
   const int of = p.many ? 128 : 16;
   p.map = kv_map(tokens, seqs, (rep + of - 1) / of, rep, of, 1);
   const int64_t groups = p.map.groups * kv_heads, work = groups * width;
@@ -412,8 +436,9 @@ hipError_t run(const AttnArgs &A, const Plan &p, const void *q, void *out, hipSt
 using namespace attn;
 
 int64_t kv_attention_scratch(int tokens, int seqs, int heads, int kv_heads, int dim, int width) {
-  const Plan p = plan(tokens, seqs, heads, kv_heads, width, 0);
-  return p.splits > 1 ? (int64_t)tokens * heads * p.splits * (kv_padded_dim(dim) * 4 + 8) : 0;
+  int splits = 1;                         // the workspace is asked for without the type
+  for (int dtype : {BQM_F32, BQM_BF16}) splits = std::max(splits, plan(dtype, tokens, seqs, heads, kv_heads, dim, width, 0).splits);
+  return splits > 1 ? (int64_t)tokens * heads * splits * (kv_padded_dim(dim) * 4 + 8) : 0;
 }
 
 hipError_t launch_kv_attention(const KvBatch &B, const void *q, int dtype, int heads, int dim, int64_t qt, int64_t qh,
@@ -422,7 +447,7 @@ hipError_t launch_kv_attention(const KvBatch &B, const void *q, int dtype, int h
   // position - window stays in 32 bits: positions are above -2^24, and no cache holds 2^31 - 2^25
   constexpr int kMostWindow = 0x7FFFFFFF - (1 << 25);
   window = window < kMostWindow ? window : kMostWindow;
-  const Plan p = plan(B.tokens, B.seqs, heads, kv_heads, B.width, window);
+  const Plan p = plan(dtype, B.tokens, B.seqs, heads, kv_heads, dim, B.width, window);
   float *part = (float *)scratch;
   float2 *ml = (float2 *)(part + (p.splits > 1 ? (int64_t)B.tokens * heads * p.splits * kv_padded_dim(dim) : 0));
   const AttnArgs A{B, p.map, heads, kv_heads, heads / kv_heads, dim, window, qt, qh, scale * 1.44269504f, kc, vc, ks, vs, p.chunk, p.splits, part, ml};

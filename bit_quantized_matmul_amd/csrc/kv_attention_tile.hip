@@ -336,7 +336,9 @@ hipError_t by_dim(const AttnArgs &A, bool vec, const void *q, void *out, hipStre
     case 96: return start<T, 96>(A, vec, (const T *)q, (T *)out, s);
     case 128: return start<T, 128>(A, vec, (const T *)q, (T *)out, s);
     case 192: return start<T, 192>(A, vec, (const T *)q, (T *)out, s);
-    default: return start<T, 256>(A, vec, (const T *)q, (T *)out, s);
+    default:
+      if constexpr (sizeof(T) == 2) return start<T, 256>(A, vec, (const T *)q, (T *)out, s);
+      else return hipErrorInvalidValue;                                  // past kMostTileF32
   }
 }
 

@@ -80,6 +80,17 @@ def test_nan_values_of_far_scores(news, heads, kv, width, dtype):
 
 # ------------------------------------------------------------------ bits of the probabilities
 
+def cancelling(rng, count, kv, dim):
+    """Neighbouring tokens' values are each other's negatives, and their keys alike but for one column."""
+    cache = filled(rng, count, kv, dim)
+    cache["v"][..., 1::2] = cache["v"][..., 0::2] ^ 0x80
+    cache["k"][..., 1::2, :] = cache["k"][..., 0::2, :]
+    cache["k"][..., 1::2, 0] = of8.encode(0.0)
+    cache["k"][..., 0::2, 0] = of8.encode(448.0)
+    cache["k_scale"][:], cache["v_scale"][:] = 2.0 ** -9, 1.0
+    return cache
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("dim,heads,kv", [(32, 6, 2), (128, 4, 1), (80, 8, 8), (256, 2, 1)])
 @pytest.mark.parametrize("length,news", [(20, 1), (64, 1), (40, 3), (2000, 1)])
@@ -88,15 +99,44 @@ def test_probabilities_of_few_rows_hold_22_bits(length, news, dim, heads, kv, dt
     result's type hides none of them."""
     rng = np.random.default_rng(length + dim)
     pages, off, count = batch(rng, [length], [news])
-    cache = filled(rng, count, kv, dim)
-    cache["v"][..., 1::2] = cache["v"][..., 0::2] ^ 0x80                 # neighbouring tokens' values cancel
-    cache["k"][..., 1::2, :] = cache["k"][..., 0::2, :]
-    cache["k"][..., 1::2, 0] = of8.encode(0.0)                           # but for one column of their keys
-    cache["k"][..., 0::2, 0] = of8.encode(448.0)
-    cache["k_scale"][:], cache["v_scale"][:] = 2.0 ** -9, 1.0
+    cache = cancelling(rng, count, kv, dim)
     q = 0.05 * rng.standard_normal((news, heads, dim))
     q[..., 0] = 0.02
     q, d = rounded(q, dtype)
     got = B.kv_attention(d, on_device(cache), ints(pages), ints([length]), ints(off))
     ref, mag, most, small = okv.attention(q, cache, pages, [length], off)
     check(host(got), ref, sharp(mag, most, small, okv.padded_dim(dim), length, dtype), dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim,news,width", [(192, 8, 100), (256, 16, 100), (160, 5, 100)])
+def test_wide_heads_of_few_rows_hold_22_bits(dim, news, width, dtype):
+    """Past 128 columns a few rows of many sequences are no work for tiles of 128 queries: probabilities hold 22 bits there too."""
+    rng = np.random.default_rng(dim)
+    seqs, heads, kv = 64, 8, 2
+    lens = rng.integers(news, 41, seqs).tolist()
+    pages, off, count = batch(rng, lens, [news] * seqs)
+    pages = widened(pages, width)
+    cache = cancelling(rng, count, kv, dim)
+    q = 0.05 * rng.standard_normal((news * seqs, heads, dim))
+    q[..., 0] = 0.02
+    q, d = rounded(q, dtype)
+    got = host(B.kv_attention(d, on_device(cache), ints(pages), ints(lens), ints(off)))
+    for s in (0, 13, 63):
+        rows = slice(off[s], off[s + 1])
+        ref, mag, most, small = okv.attention(q[rows], cache, pages[s:s + 1], [lens[s]], [0, news])
+        check(got[rows], ref, sharp(mag, most, small, okv.padded_dim(dim), lens[s], dtype), dtype)
+    assert np.all(np.isfinite(got))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim,window", [(64, 0), (96, 50), (128, 0), (192, 90), (256, 0)])
+def test_ragged_prompts_in_both_routes(dim, window, dtype):
+    """Sequences of 0 to 200 rows, none and single ones among them, in a narrow table and in one that is wide enough for tiles of
+    128 queries whatever the type."""
+    rng = np.random.default_rng(dim + 1)
+    news = rng.integers(60, 201, 9)
+    news[[0, 3, 8]] = 0, 1, 200
+    lens = [int(n + rng.integers(0, 200)) for n in news]
+    for width in (0, 1000):
+        check_attention(rng, lens, news.tolist(), 4, 2, dim, dtype, window, width=width)
