@@ -220,8 +220,10 @@ __global__ __launch_bounds__(64 * kWaves, (kDp > 128 || kTermsOf<T> > 1) ? 1 : 2
         rare = __ballot(bad) != 0;
       }
       // Another scale: the row's sums change to its units, exactly.  A page whose scale is outside [2^-40, 2^16] is summed apart
-      // and added with its share of the nearer end.  From a scale of 2^16 on the units stay there: sums of numbers up to fp32's
-      // largest then stay below 2^123 and shares above 2^-142, and else sums are below 2^76 times the positions.
+      // and added with its share of the nearer end.  From a scale of 2^16 on the units stay there.  Probabilities weigh up to 2^15
+      // (2^11 above a maximum that lags by 2^4): where values times positions are below 2^128, as the caller sees to, sums in
+      // units of 2^16 are below 2^127, and shares above 2^-142; else, after a step from 2^15 to 2^-40, below 448 x 2^15 x
+      // 2^55 < 2^79 times the positions.
       constexpr float kLeast = 0x1p-40f, kMost = 0x1p16f;
       float share = 1.0f;
       if (top > -INFINITY && vs != v_unit) {
@@ -286,13 +288,15 @@ __global__ __launch_bounds__(64 * kWaves, (kDp > 128 || kTermsOf<T> > 1) ? 1 : 2
   l *= kDown;
   if (A.splits > 1) {
     const int64_t at = head * A.splits + blockIdx.y;
-    if (hf == 0) A.ml[at] = float2{m, l};
+    // sums and their weights 2^kLag smaller in every part, so that no probability weighs more than 1: sums near fp32's largest fit
+    constexpr float kPart = kTermsOf<T> == 1 ? 0x1p-4f : 1.0f;
+    if (hf == 0) A.ml[at] = float2{m, l * kPart};
     if (p0 >= p1) return;
     float *p = A.part + at * kDp;
 #pragma unroll
     for (int d = 0; d < kCols; ++d)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) o[d][r] = o[d][r] * kDown * v_unit;
+      for (int r = 0; r < 16; ++r) o[d][r] = o[d][r] * (kDown * kPart) * v_unit;
 #pragma unroll
     for (int d = 0; d < kCols; ++d)
 #pragma unroll

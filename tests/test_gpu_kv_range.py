@@ -78,6 +78,32 @@ def test_nan_values_of_far_scores(news, heads, kv, width, dtype):
     assert np.array_equal(got[..., keep], base[..., keep])
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rise", [[0, 0, 0, 3.97, 3.97, 3.97, 3.97, 3.97], [0, 3.97, 7.9, 8, 11.5, 11.5, 15, 16], [0, 0, 0, 0, 0, 0, 0, 3.97]])
+@pytest.mark.parametrize("news,width", [(1, 0), (1, 2000), (130, 0), (130, WIDE)])
+def test_values_at_the_limit_with_rising_scores(news, width, rise, dtype):
+    """Values times positions just below fp32's largest number, all of one sign, and scores that rise by up to 4 a page in the
+    base of two: as far as the tiles' maxima may lag behind."""
+    rng = np.random.default_rng(70)
+    length, dim = 64 * 8, 32
+    pages, off, count = batch(rng, [length], [news])
+    pages = widened(pages, width)
+    cache = okv.empty(count, 1, dim)
+    order = pages[0, :8]
+    cache["v"][:] = of8.encode(448.0)
+    cache["v_scale"][:] = 2.0 ** 110                                     # 448 x 2^110 x 512 = 1.75 x 2^127
+    cache["k_scale"][:] = 1.0
+    cache["k"][order, 0, :, 0] = of8.encode(np.log(2.0) * np.array(rise, dtype=np.float64))[:, None]
+    q = np.zeros((news, 2, dim))
+    q[..., 0] = rng.uniform(0.9, 1.0, (news, 2))
+    run = lambda: check_attention(rng, [length], [news], 2, 1, dim, dtype, scale=1.0, cache=cache, pages=pages, off=off, q=q)   # noqa: E731
+    run()
+    cache["v_scale"][order[::2]] = 2.0 ** -40                            # and beside the smallest units
+    run()
+    cache["v_scale"][order, 0] = 2.0 ** np.array([15.0, -40, 15, 16, 17, -41, 110, -126])
+    run()
+
+
 # ------------------------------------------------------------------ bits of the probabilities
 
 def cancelling(rng, count, kv, dim):
