@@ -728,12 +728,15 @@ def rope_freqs(rotary: int, theta: float = 10000.0, kind: str = "none", factor: 
     if kind in ("turns", "pairs"):
         if context < 1 or not high > low:
             raise ValueError(f"{kind} needs context and low < high, got {context}, {low} and {high}")
+        if kind == "pairs" and not (low > 0 and theta > 1):
+            raise ValueError(f"pairs needs low above 0 and theta above 1, got {low} and {theta}")
         turns = context * f / (2.0 * np.pi)
         if kind == "turns":
             keep = (turns - low) / (high - low)
         else:
             at = lambda n: rotary * np.log(context / (2.0 * np.pi * n)) / (2.0 * np.log(theta))  # noqa: E731
-            first, last = max(np.floor(at(high)), 0.0), min(np.ceil(at(low)), rotary // 2 - 1.0)
+            first, last = np.floor(at(high)), min(np.ceil(at(low)), rotary // 2 - 1.0)
+            first = max(first, 0.0) if last > 0.0 else first             # else no pair turns often enough
             keep = 1.0 - (i - first) / max(last - first, 1e-3)
         keep = np.clip(keep, 0.0, 1.0)
         return f * keep + f / factor * (1.0 - keep)
