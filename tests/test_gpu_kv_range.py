@@ -1,5 +1,4 @@
-"""The attention over the 8-bit cache at the ends of its range, and how many bits its probabilities hold; what
-rope returns; the calls in a row against attention over the whole in one call.
+"""The attention over the 8-bit cache at the ends of its range, and how many bits its probabilities hold.
 
 ``sharp`` is the attention's bound with probabilities of 22 bits (two fp16 terms): with e as in test_gpu_kv.py, out is off by at most
     (2 e + 2^-21 + 2^-22 + (66 + L / 16) 2^-22) sum p |v| + 2^-40 sum |v|.
