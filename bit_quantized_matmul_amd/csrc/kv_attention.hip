@@ -151,22 +151,24 @@ __global__ __launch_bounds__(64 * NW) void kv_stream_kernel(AttnArgs A, bool qve
 #pragma unroll
         for (int r = 0; r < 4; ++r) top = fmaxf(top, whole || (see >> (4 * t + r) & 1) ? x[t][r] : -INFINITY);
       top = rows_max(top);
-      const float m1 = fmaxf(m, top > -INFINITY ? top * f : -INFINITY);
-      const float base = (m1 > -INFINITY ? m1 : 0.0f) - kUp;
+      const float most = top > -INFINITY ? top * f : -INFINITY, m1 = fmaxf(m, most);
       if (__ballot(m1 > m)) {
-        const float alpha = __builtin_amdgcn_exp2f(m - (base + kUp));
+        const float alpha = m1 > -INFINITY ? __builtin_amdgcn_exp2f(m - m1) : 0.0f;
         l *= alpha;
 #pragma unroll
         for (int d = 0; d < kCols; ++d) o[d] *= alpha;
         m = m1;
       }
+      // exponents are taken from the page's largest score on: past 2^24 a score's own steps in fp32 are larger than 2^15, the
+      // largest probability, has room for in fp16
+      const float lead = (most - m) + kUp;
       f16x8 p[2][kPTerms];
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
         float e[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-          const float v = __builtin_amdgcn_exp2f(fmaf(x[2 * a + r / 4][r % 4], f, -base));
+          const float v = __builtin_amdgcn_exp2f(fmaf(x[2 * a + r / 4][r % 4] - top, f, lead));
           e[r] = whole || (see >> (8 * a + r) & 1) ? v : 0.0f;
         }
         to_terms<kPTerms>(e, p[a]);

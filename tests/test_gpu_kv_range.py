@@ -103,6 +103,43 @@ def test_values_at_the_limit_with_rising_scores(news, width, rise, dtype):
     run()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("exponent", [0, 17, 20, 26, 60, 115])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("news,width,window", [(1, 0, 0), (1, 2000, 0), (150, 0, 0), (150, 0, 30), (150, WIDE, 0), (150, WIDE, 30)])
+def test_scores_far_past_their_differences(news, width, window, sign, exponent, dtype):
+    """Scores of up to 448 x 2^exponent, whose steps in fp32 are larger than a probability's whole range: one column of keys, so that
+    they are exact.  All weight is on a row's largest, or shared among equal ones."""
+    rng = np.random.default_rng(exponent)
+    length, dim, heads, kv = 300, 32, 4, 2
+    pages, off, count = batch(rng, [length], [news])
+    pages = widened(pages, width)
+    cache = okv.empty(count, kv, dim)
+    cache["k"][..., 0] = rng.choice([0x7E, 0x7C, 0x76, 0x30, 0xF0, 0xFE], cache["k"][..., 0].shape, p=[0.02, 0.08, 0.2, 0.3, 0.2, 0.2])
+    cache["v"][:] = of8.encode(rng.integers(-8, 9, cache["v"].shape))
+    cache["k_scale"][:], cache["v_scale"][:] = 1.0, 1.0
+    q = np.zeros((news, heads, dim))
+    q[..., 0] = sign * 2.0 ** rng.integers(0, 2, (news, heads))
+    _, d = rounded(q, dtype)
+    got = host(B.kv_attention(d, on_device(cache), ints(pages), ints([length]), ints(off), scale=16.0 * 2.0 ** (exponent - 8), window=window))
+    for i in range(news):
+        for h in range(heads):
+            k, v, _ = okv.values(cache, pages, 0, length, h // 2, dim)
+            j = np.arange(length)
+            p = length - news + i
+            see = (j <= p) & ((j > p - window) if window else True)
+            s = 16.0 * 2.0 ** (exponent - 8) * k[see, 0] * q[i, h, 0]
+            e = np.exp(s - s.max())
+            e /= e.sum()
+            want, mag = e @ v[see], e @ np.abs(v[see])
+            # scores are exact; times log2(e) their differences, below 100 where they count, are off by 2^-23 of them.  p is off by up to
+            # 2^-11 of it where it is one term: sum p d (v - o), |d| <= 2^-11, is at most 2^-11 (sum p |v| + |o|) <= 2^-10 sum p |v|
+            t = (2.0 ** -10 + 2.0 ** -16) * mag + 2.0 ** -36 * np.abs(v[see]).sum(0)
+            # and half a step of the type, below its normal numbers too
+            half = torch.finfo(dtype).eps / 2 * np.maximum(np.abs(want) + t, torch.finfo(dtype).smallest_normal)
+            assert np.all(np.abs(got[i, h] - want) <= t + half), (i, h)
+
+
 # ------------------------------------------------------------------ bits of the probabilities
 
 def cancelling(rng, count, kv, dim):
