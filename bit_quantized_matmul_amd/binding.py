@@ -744,7 +744,7 @@ def rope_freqs(rotary: int, theta: float = 10000.0, kind: str = "none", factor: 
 
 
 def rope(x, positions, freqs, interleaved: bool = False, mscale: float = 1.0, backward: bool = False, out=None):
-    """Rotary positions: x [tokens, heads, dim] (float32, bfloat16 or float16, tokens and heads may be strided), positions
+    """Rotary positions: x [tokens, heads, dim] (float32, bfloat16 or float16; tokens and heads may be strided, rows not overlap), positions
     int32 [tokens], freqs float64 [rotary / 2] radians a position (rope_freqs, on the device) -> x with its first
     rotary columns turned and scaled by mscale: pairs (i, i + rotary / 2), or (2 i, 2 i + 1) with interleaved.  With
     backward the gradient of x for a gradient x of the result.  out may be x."""

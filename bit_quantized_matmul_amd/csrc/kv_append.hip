@@ -12,10 +12,16 @@
 // An element that is infinite or NaN becomes the NaN code and has no part in the scale, so that a
 // token that overflowed spoils its own attention and not its neighbours'.
 //
-// A workgroup takes the tokens of one page and head; so no two write to the same scale.  Bound by its instructions,
-// 1285 a wave for 64 tokens of 128 columns (480 of them angles): 17900 tokens of 8 heads 36 us, 3.1 TB/s, where HBM
-// would take 23; single tokens of 64 sequences 6.6 us, of one 5.8, by the chain from lengths to pages to scales.  Sharing the
+// A workgroup takes the tokens of one page and head; so no two write to the same scale.  17900 tokens of 8 heads of 128: 32 to 36
+// us, 3.1 TB/s and more, where HBM would take 23.  Bound by neither: the vector unit is busy 39% of the time (1285
+// instructions a wave for 64 tokens, 480 of them angles), and a page's phases - loads, angles, the reduction and its barrier,
+// codes, stores - follow each other with nothing of the next page under way but what the other waves (four a SIMD) do.
+// Single tokens of 64 sequences 6.7 us, of one 5.6, by the chain from lengths to pages to scales.  Sharing the
 // angles among heads (a workgroup for 2, 4 or 8 of them) took as long or longer: its registers leave fewer waves.
+//
+// Rows that do not start on 16 bytes, and rotary % 16 or dim % 8 other than 0, are loaded an element at a time: 17900 tokens of
+// 8 x 128 66 us (30 aligned), of 8 x 80 with 40 turned 49, of 4 x 26 10.  fp32 rows 38 us.  256 columns leave one or two waves a
+// SIMD: 66 us, the same rate.
 #include "kv_common.h"
 
 namespace bqm {

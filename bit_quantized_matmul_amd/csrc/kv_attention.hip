@@ -20,7 +20,7 @@ namespace {
 // sequence times the heads that share the key head.  A workgroup takes `chunk` pages of a tile, its waves
 // every NW-th of them, straight into registers: a wave's loads of the next page's keys are on their way
 // while it weighs this page's scores, and its loads of the next values while it multiplies the next keys.
-// One token of 131072 positions, 8 key heads of 128: 52 us, 5.1 TB/s; 64 of up to 8192: 104 us, 4.5 TB/s.
+// One token of 131072 positions, 8 key heads of 128: 52 us, 5.1 TB/s; 64 of up to 8192: 106 us, 4.5 TB/s.
 template <typename T, int kDp, int NW>
 __global__ __launch_bounds__(64 * NW) void kv_stream_kernel(AttnArgs A, bool qvec, const T *__restrict__ q,
                                                             T *__restrict__ out) {

@@ -1,9 +1,19 @@
 // Attention over the paged 8-bit cache: many rows a sequence.
 //
-// Bound by arithmetic: 4 x 2048 rows of 8192 positions, 32 heads of 128 columns to 8: 1070 us, 900 TFLOP/s.  The vector
-// instructions (410 a wave and page, 128 of them conversions and 32 exponentials) are busy 69% of the time, the matrix
-// instructions (32) 40%; two waves a SIMD hide no more.  Codes widened once a workgroup, to fp16 in LDS, took a fourth of the vector
+// Bound by arithmetic: 4 x 2048 rows of 8192 positions, 32 heads of 128 columns to 8: 1068 to 1117 us a call from one machine to
+// another, 860 to 900 TFLOP/s.  The vector instructions (414 a wave and page: 128 conversions, 32 exponentials, and 64 that copy
+// the sums to other registers and back, since the second product is written twice, in the common branch and in the rare one) are
+// busy 69% of the time, the matrix instructions (32) 39%.  Each page also waits at its head for its number and its scales.
+// Codes widened once a workgroup, to fp16 in LDS, took a fourth of the vector
 // instructions away and 13% more time: twice the reads of LDS, whose latency two waves do not hide.
+//
+// Probabilities of 16-bit rows are one fp16 term: 2^-11 of each at most, of random sign, beside half a step of 2^-8 of a bf16
+// result and 2^-11 of an fp16 one.  (Against 64 bits, 512 rows of 2048: bf16 results off by 1.665e-3 of them, 1.660e-3 with
+// two terms; fp16 2.42e-4 and 2.08e-4.  Two terms take 30% more time: 1075 -> 1410 us.)
+//
+// Registers: 16 bits, 128 columns two waves a SIMD, with 8 registers spilled before the first page; 192 and 256 columns, and fp32
+// from 96 on, one wave; 256 columns spill 94, 11 of which are read again every page.  4 x 2048 rows of 8192, us with
+// 64 / 128 / 192 / 256 columns: bf16 712 / 1063 / 2425 / 4028, fp32 1143 / 2573 / 3620 / not here (6091 in tiles of 16).
 //
 // A tile is 128 queries of one key head, 32 a wave: the rows of a sequence times the heads
 // that share the key head.  Pages go to LDS as codes, without passing through registers, into one of two buffers
@@ -133,7 +143,7 @@ __global__ __launch_bounds__(64 * kWaves, (kDp > 128 || kTermsOf<T> > 1) ? 1 : 2
       if (!there || !any || start > last || (A.window && start + kPage <= first - A.window + 1)) continue;
 
       const uint8_t *kl = lds + at, *vl = lds + at + kKeyBytes;
-      // Scores.  Fragments are read two ahead; left to itself the compiler reads all of them first and spills.  The products
+      // Scores.  Fragments are read two ahead; left to itself the compiler reads all of them first and spills more.  The products
       // go before the other wave's softmax (4 x 2048 rows of 8192: 1180 us without, 1150 so).
       auto key = [&](int n) {                                            // fragment n: half page n / (kSteps / 2)
         // row 8 b + 4 h + j is token 16 h + 4 b + j

@@ -5,7 +5,8 @@
 //
 // and the gradient goes through the transposed matrix: the same with -sin.  The other columns are
 // copied.  A row is read and written once, which bounds the time: 16384 tokens of 32 heads of 128 bf16 columns, half of
-// them turned, 52 us, 5.2 TB/s; one token 2.1 us.
+// them turned, 53 us, 5.1 TB/s (fp32 125 us, 4.3 TB/s); one token 2.1 us.  Elements one by one, where rows do not start on 16 bytes
+// or the turned columns are no whole loads: 92 us; 32 x 80 with 40 turned 56 us, 12 x 26 10 us, 2 to 3 TB/s.
 //
 // A workgroup takes a few tokens: its threads first compute one angle each into LDS (cos and sin cost about
 // 50 instructions, and the heads share them), then turn the tokens' heads.

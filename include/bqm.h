@@ -494,7 +494,7 @@ int moe_ffn(const void *x, int dtype, int tokens, int hidden, int64_t x_stride, 
  * Turn the first `rotary` columns of every head by its token's position:
  *   y1 = mscale (x1 cos a - x2 sin a),  y2 = mscale (x1 sin a + x2 cos a),  a = positions[t] freqs[i],
  * for the pairs (x1, x2) = columns (i, i + rotary / 2) or, interleaved, (2 i, 2 i + 1); the other
- * columns are copied.  Angles are formed in fp64, the rest in fp32, y is rounded once.  backward: the
+ * columns are copied.  Angles, below 2^50 radians, are formed in fp64, the rest in fp32, y is rounded once.  backward: the
  * gradient's product with the transposed matrix (-sin for sin).
  * x, y [device] `dtype` [tokens, heads, dim], tokens and heads the given strides apart, a row's
  * columns side by side, rows not overlapping; y may be x with the same strides, and must not share
@@ -511,7 +511,7 @@ int rope(const void *x, int dtype, int tokens, int heads, int dim, int64_t x_tok
  * A batch of sequences.  Sequence s has lens[s] positions with its newest, which are rows
  * offsets[s] .. offsets[s + 1] - 1 of k, v or q (row s alone when offsets is NULL, and then
  * tokens = seqs); its newest row is position lens[s] - 1.  pages [seqs, width] int32, rows
- * pages_stride apart: positions 64 i .. 64 i + 63 lie in page pages[s, i].  offsets [seqs + 1] int32,
+ * pages_stride >= width apart: positions 64 i .. 64 i + 63 lie in page pages[s, i].  offsets [seqs + 1] int32,
  * ascending, and lens [seqs] int32.  All [device], and none of them leaves it: a launch is sized from
  * tokens, seqs, width and heads alone.  Offsets outside [0, tokens] are taken as the nearer end.  Positions below 0,
  * past the table's width or in a page outside [0, count) are not written and not attended to.
@@ -523,7 +523,7 @@ int rope(const void *x, int dtype, int tokens, int heads, int dim, int64_t x_tok
  * positions of the sequence before them; codes = E4M3(value / scale), and where the scale has grown the codes
  * before become E4M3(code * old scale / scale).  An infinite or NaN element becomes code 0x7F and has no part in
  * the scale.  Codes of later slots stay as they are.  k, v [device] `dtype` [tokens, heads, dim],
- * tokens and heads the given strides apart.  No page may be written for two sequences, or twice for
+ * tokens and heads the given strides apart, rows not overlapping.  No page may be written for two sequences, or twice for
  * one, in a call: which of them it then holds is not defined. */
 int kv_append(const void *k, const void *v, int dtype, int tokens, int heads, int dim, int64_t k_token_stride,
               int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride, const int32_t *offsets,
@@ -538,7 +538,7 @@ int kv_append(const void *k, const void *v, int dtype, int tokens, int heads, in
  * q is of 16 bits and sequences have many rows; p to 2^-36 or 2^-40 of the row's largest), the maxima and sums of the softmax are fp32, out is rounded once.  Sums of
  * values weigh the row's largest p as 1: values times positions have to stay below fp32's largest
  * number.  What is masked has no part in the result, whatever it holds; a NaN code that is attended to makes NaN.
- * q [device] `dtype` [tokens, heads, dim], tokens and heads the given strides apart; out [device] `dtype`
+ * q [device] `dtype` [tokens, heads, dim], tokens and heads the given strides apart, rows not overlapping; out [device] `dtype`
  * [tokens, heads, dim] contiguous.  workspace [device, 16-byte aligned, NULL if none is needed] of
  * kv_attention_workspace bytes needs no clearing and may be reused by the next call on the
  * stream.  tokens * heads < 2^24 (BQM_ENOTSUP). */
