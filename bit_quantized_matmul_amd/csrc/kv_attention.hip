@@ -161,7 +161,7 @@ __global__ __launch_bounds__(64 * NW) void kv_stream_kernel(AttnArgs A, bool qve
       }
       // exponents are taken from the page's largest score on: past 2^24 a score's own steps in fp32 are larger than 2^15, the
       // largest probability, has room for in fp16
-      const float lead = (most - m) + kUp;
+      const float lead = most > -INFINITY ? (most - m) + kUp : -INFINITY;
       f16x8 p[2][kPTerms];
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
@@ -354,7 +354,7 @@ int64_t above(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //   4 x 2048 of 4096     1274 / 498    1471 / 1111    2881 / 1877     737 / 528     1306 / 1166    2416 / 1601    2943 / 4530
 //   8 heads: 16 x 256 of 1024
 //                          75 / 55      92 / 110       190 / 165      44 / 52        79 / 104       150 / 145      196 / 314
-// fp32 of 256 columns, whose queries alone are 256 registers, stays in tiles of 16 (there is no other kernel of it).
+// fp32 of 256 columns, whose queries and sums are 256 registers, stays in tiles of 16 (there is no other kernel of it).
 struct ManyRule {
   int queries;                            // more than these a sequence
   int64_t work;                           // and no less than this

@@ -140,6 +140,33 @@ def test_scores_far_past_their_differences(news, width, window, sign, exponent, 
             assert np.all(np.abs(got[i, h] - want) <= t + half), (i, h)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("news,width", [(1, 0), (1, 2000), (150, 0), (150, WIDE)])
+@pytest.mark.parametrize("low", [[0], [1], [0, 1, 3]])
+def test_scores_below_fp32_beside_others(low, news, width, dtype):
+    """Pages whose scores are below -2^128 weigh nothing, also as a row's first; a row that sees no other key is not looked at."""
+    rng = np.random.default_rng(news)
+    length, dim = 250, 32
+    pages, off, count = batch(rng, [length], [news])
+    pages = widened(pages, width)
+    cache = okv.empty(count, 1, dim)
+    cache["k"][pages[0, low], ..., 0] = of8.encode(-448.0)               # times 2^125
+    cache["v"][:] = of8.encode(rng.integers(-8, 9, cache["v"].shape))
+    cache["k_scale"][:], cache["v_scale"][:] = 1.0, 1.0
+    q = np.zeros((news, 2, dim))
+    q[..., 0] = 1.0
+    _, d = rounded(q, dtype)
+    got = host(B.kv_attention(d, on_device(cache), ints(pages), ints([length]), ints(off), scale=2.0 ** 125))
+    k, v, _ = okv.values(cache, pages, 0, length, 0, dim)
+    for i in range(news):
+        see = (np.arange(length) <= length - news + i) & (k[:, 0] == 0.0)
+        if not see.any():
+            continue
+        want, mag = v[see].mean(0), np.abs(v[see]).mean(0)
+        t = 2.0 ** -18 * mag                                             # equal probabilities, exact; their sums and the quotient
+        assert np.all(np.abs(got[i] - want) <= t + torch.finfo(dtype).eps / 2 * (np.abs(want) + t)), i
+
+
 # ------------------------------------------------------------------ bits of the probabilities
 
 def cancelling(rng, count, kv, dim):
