@@ -470,10 +470,10 @@ int moe_combine(const void *y, int dtype, int64_t y_rows, int d, const int32_t *
  *   out[t] = sum_j w[t, j] W2[e_j] (silu(G[e_j] x_t) * (U[e_j] x_t)),  W13 = [G | U],
  * e_j and w[t, j] as moe_route gives them (the same ties, masks and renorm; a token without an
  * expert has a row of zeros).  x is not quantized: the products of its elements and the codes are summed
- * in fp32 (an fp32 x as three bf16 terms, the hidden rows as two or, for an fp32 x, three; sums of a block may pass
- * fp32's largest number before its scale, and products below 2^-108 lose bits), and out is
- * rounded once.  A row of x with a NaN or an infinity, and an expert, has a row of NaN; so has one with a
- * gate, an up value or their silu(gate) * up past fp32's largest number.
+ * in fp32 (an fp32 x as three bf16 terms, the hidden rows as two or, for an fp32 x, three; sums of a
+ * block may pass fp32's largest number before its scale, and products below 2^-108 lose bits), and out
+ * is rounded once.  A row of x with a NaN or an infinity, and an expert, has a row of NaN; so has one
+ * with a gate, an up value or their silu(gate) * up past fp32's largest number.
  * x [device] `dtype` [tokens, hidden], rows x_stride apart; logits [device] `logits_dtype` [tokens,
  * experts], rows logits_stride apart; w13 [device] [experts, 2 ffn, 128 ceil(hidden / 128)] and w2
  * [experts, hidden, 128 ceil(ffn / 128)] with their scales, both as fp8_pack writes them, 16-byte
@@ -535,13 +535,14 @@ int kv_append(const void *k, const void *v, int dtype, int tokens, int heads, in
  * cache with position(t) - window < j <= position(t) (window 0: no lower bound), keys and values of head
  * h / (heads / kv_heads).  A row that sees no position is zeros; rows of no sequence are not
  * written.  Products are summed in fp32 (q as one fp16 term, an fp32 q as two; p as two, or one where
- * q is of 16 bits and sequences have many rows; p to 2^-36 or 2^-40 of the row's largest), the maxima and sums of the softmax are fp32, out is rounded once.  Sums of
- * values weigh the row's largest p as 1: values times positions have to stay below fp32's largest
- * number.  What is masked has no part in the result, whatever it holds; a NaN code that is attended to makes NaN.
- * q [device] `dtype` [tokens, heads, dim], tokens and heads the given strides apart, rows not overlapping; out [device] `dtype`
- * [tokens, heads, dim] contiguous.  workspace [device, 16-byte aligned, NULL if none is needed] of
- * kv_attention_workspace bytes needs no clearing and may be reused by the next call on the
- * stream.  tokens * heads < 2^24 (BQM_ENOTSUP). */
+ * q is of 16 bits and sequences have many rows; p to 2^-36 or 2^-40 of the row's largest), the maxima
+ * and sums of the softmax are fp32, out is rounded once.  Scores have to stay within fp32, and, as sums of
+ * values weigh the row's largest p as 1, so have values times positions.  What is masked has no part in
+ * the result, whatever it holds; a NaN code that is attended to makes NaN.
+ * q [device] `dtype` [tokens, heads, dim], tokens and heads the given strides apart, rows not
+ * overlapping; out [device] `dtype` [tokens, heads, dim] contiguous.  workspace [device, 16-byte
+ * aligned, NULL if none is needed] of kv_attention_workspace bytes needs no clearing and may be reused
+ * by the next call on the stream.  tokens * heads < 2^24 (BQM_ENOTSUP). */
 int kv_attention_workspace(int tokens, int seqs, int heads, int kv_heads, int dim, int width, int64_t *bytes);
 int kv_attention(const void *q, int dtype, int tokens, int heads, int dim, int64_t q_token_stride, int64_t q_head_stride,
                  const int32_t *offsets, const int32_t *lens, int seqs, const int32_t *pages, int64_t pages_stride,
